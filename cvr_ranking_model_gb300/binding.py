@@ -23,7 +23,9 @@ TIMELINE_KERNELS = ["sparse", "seq_mlp", "seq_colsum", "tokenizer", "query", "at
                     "attention_tc"]
 
 STATUS = {0: "CVR_OK", 1: "CVR_E_ARG", 2: "CVR_E_SHAPE", 3: "CVR_E_ID_RANGE", 4: "CVR_E_OOM", 5: "CVR_E_CUDA",
-          6: "CVR_E_INPUT", 7: "CVR_E_TIMEOUT"}
+          6: "CVR_E_INPUT", 7: "CVR_E_TIMEOUT", 8: "CVR_E_PAGES"}
+
+DTYPE_BF16, DTYPE_F16, DTYPE_I8 = 0, 1, 2  # cvr_dtype
 
 _F = ctypes.POINTER(ctypes.c_float)
 
@@ -45,6 +47,14 @@ class Weights(ctypes.Structure):
         [(n, _F * MAX_LAYERS) for n in ("tm_w1", "tm_b1", "tm_w3", "tm_b3", "tm_w2", "tm_b2", "tm_gain")] + \
         [("ple_w", _F * 3), ("ple_b", _F * 3)] + \
         [(n, _F * 2) for n in ("gate_w", "gate_b", "head_w1", "head_b1", "head_w2", "head_b2")]
+
+
+class KvConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "page_size", "max_req", "max_pages",
+                                              "dtype", "cache_dtype", "window", "reserved")] + \
+        [("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+         ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+         ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class CvrError(RuntimeError):
@@ -105,6 +115,20 @@ def lib() -> ctypes.CDLL:
         L.cvr_cache_stats.restype = ctypes.c_int
         L.cvr_destroy.argtypes = [V]
         L.cvr_destroy.restype = None
+        L.cvr_kv_create.argtypes = [V, V, ctypes.POINTER(V)]
+        L.cvr_kv_create.restype = ctypes.c_int
+        L.cvr_kv_tables.argtypes = [V, i32, V, V, V, V, i32, V, V, V, V, V, i64]
+        L.cvr_kv_tables.restype = ctypes.c_int
+        L.cvr_kv_append.argtypes = [V, i64, V, V, i64, V, i64]
+        L.cvr_kv_append.restype = ctypes.c_int
+        L.cvr_kv_attend.argtypes = [V, i32, V, i64, V, V, f32, V, i64, V]
+        L.cvr_kv_attend.restype = ctypes.c_int
+        L.cvr_kv_sync.argtypes = [V]
+        L.cvr_kv_sync.restype = ctypes.c_int
+        L.cvr_kv_last_error.argtypes = [V]
+        L.cvr_kv_last_error.restype = ctypes.c_char_p
+        L.cvr_kv_destroy.argtypes = [V]
+        L.cvr_kv_destroy.restype = None
         _lib = L
     return _lib
 
@@ -296,6 +320,81 @@ class Scorer:
     def close(self) -> None:
         if getattr(self, "_h", None):
             self._lib.cvr_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def make_kv_config(q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, max_req: int,
+                   max_pages: int, dtype: int = DTYPE_BF16, cache_dtype: Optional[int] = None, window: int = 0,
+                   k: int = 0, k_strides: Sequence[int] = (), k_scale: int = 0, v: int = 0,
+                   v_strides: Sequence[int] = (), v_scale: int = 0) -> KvConfig:
+    """k, v, k_scale, v_scale: device pointers of the pools and their row scales (0 = none; v = 0 with k: K = V).
+    Strides (page, kv head, token) are in values; by default a pool is [page][kv head][token][head_dim]."""
+    c = KvConfig(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, max_req=max_req,
+                 max_pages=max_pages, dtype=dtype, cache_dtype=dtype if cache_dtype is None else cache_dtype,
+                 window=window, n_pages=n_pages, k=k or None, v=v or None, k_scale=k_scale or None,
+                 v_scale=v_scale or None)
+    dense = (kv_heads * page_size * head_dim, page_size * head_dim, head_dim)
+    for i in range(3):
+        c.k_stride[i] = int((k_strides or dense)[i])
+        c.v_stride[i] = int((v_strides or dense)[i])
+    return c
+
+
+class KvCache:
+    """One cvr_kv: the paged history cache's operators on the caller's pools. Arrays are device pointers (ints, 0 =
+    none), e.g. torch tensors' data_ptr(); calls only enqueue on `stream`, sync() waits and raises what they found."""
+
+    def __init__(self, config: KvConfig, stream: int = 0):
+        self._lib = lib()
+        self._h = None
+        h = ctypes.c_void_p()
+        st = self._lib.cvr_kv_create(ctypes.byref(config), ctypes.c_void_p(stream), ctypes.byref(h))
+        if st != 0:
+            raise CvrError(st, "cvr_kv_create failed (see stderr)")
+        self._h = h
+        self.config = config
+
+    def _check(self, st: int) -> int:
+        if st != 0:
+            raise CvrError(st, self.last_error())
+        return st
+
+    def tables(self, n_req: int, lens: int, table: int, new_lens: int = 0, held: int = 0, free_pages: int = 0,
+               n_free: int = 0, free_head: int = 0, pages: int = 0, free_head_out: int = 0, slots: int = 0,
+               n_slots: int = 0) -> None:
+        """cvr_kv_tables: block tables and slot maps from request lengths."""
+        self._check(self._lib.cvr_kv_tables(self._h, n_req, lens, new_lens, held, free_pages, n_free, free_head, table,
+                                            pages, free_head_out, slots, n_slots))
+
+    def append(self, n_tok: int, slots: int, k: int, v: int = 0, k_stride: int = 0, v_stride: int = 0) -> None:
+        """cvr_kv_append: the new tokens' rows to their slots (strides of tokens in values, 0 = dense)."""
+        dense = self.config.kv_heads * self.config.head_dim
+        self._check(self._lib.cvr_kv_append(self._h, n_tok, slots, k, k_stride or dense, v, v_stride or dense))
+
+    def attend(self, n_req: int, q: int, lens: int, table: int, scale: float, out: int, lse: int = 0,
+               q_stride: int = 0, out_stride: int = 0) -> None:
+        """cvr_kv_attend: one query token per request over its pages (strides of requests in values, 0 = dense)."""
+        dense = self.config.q_heads * self.config.head_dim
+        self._check(self._lib.cvr_kv_attend(self._h, n_req, q, q_stride or dense, lens, table, scale, out,
+                                            out_stride or dense, lse))
+
+    def sync(self, check: bool = True) -> int:
+        """cvr_kv_sync: waits for the stream; the status of the device-side checks."""
+        st = self._lib.cvr_kv_sync(self._h)
+        return self._check(st) if check else st
+
+    def last_error(self) -> str:
+        return self._lib.cvr_kv_last_error(self._h).decode()
+
+    def close(self) -> None:
+        if getattr(self, "_h", None):
+            self._lib.cvr_kv_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -689,6 +689,7 @@ const char* cvr_status_string(cvr_status s) {
     case CVR_E_CUDA: return "CUDA error";
     case CVR_E_INPUT: return "invalid offsets or request ids";
     case CVR_E_TIMEOUT: return "device wait timed out";
+    case CVR_E_PAGES: return "free pages ran out";
   }
   return "unknown status";
 }

@@ -51,7 +51,8 @@ typedef enum {
   CVR_E_OOM = 4,      /* device or pinned-host allocation failed */
   CVR_E_CUDA = 5,     /* a CUDA call failed (message in cvr_last_error) */
   CVR_E_INPUT = 6,    /* bag offsets decreasing, or request ids out of range / decreasing */
-  CVR_E_TIMEOUT = 7   /* a bounded device-side wait gave up (reported instead of hanging) */
+  CVR_E_TIMEOUT = 7,  /* a bounded device-side wait gave up (reported instead of hanging) */
+  CVR_E_PAGES = 8     /* cvr_kv_tables: the free list ran out of pages */
 } cvr_status;
 
 typedef struct cvr_handle cvr_handle;
@@ -282,6 +283,101 @@ cvr_status cvr_cache_stats(cvr_handle* h, int64_t* hits, int64_t* misses);
 
 /* Frees the handle's device memory, graphs and events. NULL is ignored. */
 void cvr_destroy(cvr_handle* h);
+
+/* ---------------------------------------------------------------------------------------------------------
+ * Paged history cache. cvr_score encodes a user's whole history on every call; a server that keeps histories
+ * (or any sequence's keys and values) resident in HBM stores them in pages of `page_size` tokens and touches
+ * only what is new. Three operators work on the caller's pools, on the handle's stream:
+ *   cvr_kv_tables  block tables and slot maps from request lengths, pages taken from a free list
+ *   cvr_kv_append  new key and value rows to their slots, in 16 bits or as 8-bit integers with a scale per row
+ *   cvr_kv_attend  one query token per request and head over that request's pages
+ * A slot is page * page_size + position in the page. With K = V (the ranking model's Query Decoding, whose
+ * encoded states serve as both) a cache has one pool.
+ * The three calls only enqueue (like cvr_score_async) and may be captured into a CUDA graph of the handle's
+ * stream; cvr_kv_sync waits and returns the status of the device-side checks. Calls never allocate.
+ * A handle is not thread-safe, and its calls and the graphs captured from it share its workspace: run them one
+ * after another, and use one handle per stream (handles may share pools). Pools are BORROWED and must stay
+ * valid while calls or graphs use them. */
+typedef struct cvr_kv cvr_kv;
+
+typedef enum { CVR_DTYPE_BF16 = 0, CVR_DTYPE_F16 = 1, CVR_DTYPE_I8 = 2 } cvr_dtype;
+
+typedef struct {
+  int32_t q_heads;     /* query heads, a multiple of kv_heads: query head i reads kv head i / (q_heads / kv_heads) */
+  int32_t kv_heads;    /* 1 .. 256; q_heads / kv_heads in [1, 64] */
+  int32_t head_dim;    /* 32, 64 or 128 */
+  int32_t page_size;   /* tokens per page: a power of two in [8, 256] */
+  int32_t max_req;     /* most requests of a call, 1 .. 65535 */
+  int32_t max_pages;   /* columns of a block table, >= 1; max_pages * page_size <= 2^30 */
+  int32_t dtype;       /* CVR_DTYPE_BF16 or CVR_DTYPE_F16: q, out and the new rows */
+  int32_t cache_dtype; /* the pools: `dtype`, or CVR_DTYPE_I8 */
+  int32_t window;      /* 0: a query sees the whole history; w > 0: its last w tokens */
+  int32_t reserved;    /* 0 */
+  int64_t n_pages;     /* pages of a pool, 1 .. 2^31 - 1 */
+  /* DEVICE pools, 16-byte aligned. The head_dim values of a row are contiguous; strides of page, kv head and token
+   * are in values, multiples of 16 bytes, and rows must not overlap (any nesting order of the three). k = NULL: a
+   * handle for cvr_kv_tables only. v = NULL: values are the keys (K = V; v_stride and v_scale are ignored). */
+  void *k, *v;
+  int64_t k_stride[3], v_stride[3];
+  /* with CVR_DTYPE_I8: fp32 [n_pages][kv_heads][page_size], one scale per row (a value is q * scale), 16-byte
+   * aligned; otherwise NULL */
+  float *k_scale, *v_scale;
+} cvr_kv_config;
+
+/* Creates a handle on the current CUDA device, working on `cuda_stream` (NULL = the legacy default stream).
+ * CVR_E_ARG for a bad configuration (reason on stderr), CVR_E_OOM / CVR_E_CUDA on device failures. */
+cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** out);
+
+/* Block tables and slot maps for n_req requests (0 <= n_req <= max_req), all arrays DEVICE:
+ *   lens      [n_req] int32 tokens of each request's history, the new ones included
+ *   new_lens  [n_req] int32 how many of them, the last ones, are new; NULL: one of each request that is not empty
+ *   held      [n_req] int32 leading entries of the request's table row that hold pages already; NULL: none
+ *   free_pages [n_free] int32 page ids; taken from position *free_head on (NULL: from 0), in request order
+ *   table     [n_req][max_pages] int32, in place: a request of n = ceil(lens / page_size) > held pages gets free pages
+ *             in entries held .. n - 1; no other entry is touched
+ *   pages     [n_req] int32 entries that hold pages afterwards (pass it as `held` of the next step); NULL: not written
+ *   free_head_out int32, *free_head plus the pages taken; NULL: not written. `pages` and `free_head_out` must be
+ *             other arrays than `held` and `free_head`: a call leaves its inputs as they were
+ *   slots     [n_slots] int64: the slots of the new tokens, requests in order, tokens in order; -1 behind the last.
+ *             NULL with n_slots = 0: none wanted
+ * Errors at cvr_kv_sync: CVR_E_INPUT for a length or held count out of range (used clamped) or more new tokens than
+ * n_slots (the rest is dropped); CVR_E_PAGES when the free list ends (the entries and slots without a page are -1);
+ * CVR_E_ID_RANGE for a page id outside the pool (its slots are -1). */
+cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const int32_t* new_lens, const int32_t* held,
+                         const int32_t* free_pages, int32_t n_free, const int32_t* free_head, int32_t* table,
+                         int32_t* pages, int32_t* free_head_out, int64_t* slots, int64_t n_slots);
+
+/* Writes n_tok tokens' rows (0 <= n_tok <= 2^31 - 1) to their slots:
+ *   slots [n_tok] int64; a negative slot skips its token (padding); a slot outside the pool is skipped and reported
+ *         (CVR_E_ID_RANGE). Of tokens with the same slot any may stay, in parts: give each its own
+ *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned; consecutive tokens k_stride / v_stride
+ *         values apart (a multiple of 8, at least kv_heads * head_dim). With K = V pass v = NULL.
+ * CVR_DTYPE_I8 pools: per row scale = max|x| / 127 and q = round-half-even(127 x / max|x|); a zero row has q = 0 and
+ * scale 0; a row with an infinity or NaN gets a scale that is not finite, so that it reads as no number. */
+cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride);
+
+/* Attention of one query token per request (0 <= n_req <= max_req; DEVICE arrays):
+ *   out[r][i] = sum_j softmax_j(scale q[r][i] . k_j) v_j over the tokens j the query sees: j < lens[r], and
+ *   j >= lens[r] - window when the window is not 0; the kv head of query head i as in the configuration
+ *   q, out [n_req][q_heads][head_dim] of `dtype`, 16-byte aligned, requests q_stride / out_stride values apart (a
+ *         multiple of 8, at least q_heads * head_dim); out must not overlap q or the pools
+ *   lens  [n_req] int32; a request of length 0 gives zeros (and lse = -infinity)
+ *   table [n_req][max_pages] int32: page ids of the first ceil(lens / page_size) entries; the rest is not read
+ *   scale finite; with the ranking model's temperature 1 / (tau * sqrt(head_dim))
+ *   lse   fp32 [n_req][q_heads] natural log of the softmax's denominator; NULL: not written
+ * What lies in a page behind the history (or before the window) never reaches the output, whatever its bits. Logits,
+ * softmax and sums are fp32. Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length
+ * outside [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read;
+ * out is not meaningful), CVR_E_TIMEOUT. */
+cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
+                         const int32_t* table, float scale, void* out, int64_t out_stride, float* lse);
+
+/* Waits for the handle's stream; the status of the device-side checks since the previous cvr_kv_sync. */
+cvr_status cvr_kv_sync(cvr_kv* h);
+const char* cvr_kv_last_error(const cvr_kv* h);
+/* Waits for the stream and frees the handle's memory (not the pools). NULL is ignored. */
+void cvr_kv_destroy(cvr_kv* h);
 
 #ifdef __cplusplus
 }
