@@ -13,7 +13,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB_DEFAULT = os.path.join(PKG, "libcvr.so")
 LIB_TIMELINE = os.path.join(PKG, "libcvr_timeline.so")
 LIB = LIB_TIMELINE if os.environ.get("CVR_TIMELINE") == "1" else LIB_DEFAULT
-SOURCES = ["cvr_api.cu", "k_sparse.cu", "k_mlp.cu", "k_gemm.cu", "k_ple.cu", "k_attn.cu", "k_attn_tc.cu", "cvr_kv.cu", "k_kv_pages.cu", "k_kv_attn.cu"]
+SOURCES = ["cvr_api.cu", "k_sparse.cu", "k_mlp.cu", "k_gemm.cu", "k_ple.cu", "k_attn.cu", "k_attn_tc.cu", "cvr_kv.cu", "k_kv_pages.cu", "k_kv_attn32.cu", "k_kv_attn64.cu",
+           "k_kv_attn128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -20,12 +20,7 @@
 using namespace cvr;
 typedef __nv_bfloat16 bf16;
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
+namespace cvr {
 EncodeTiledFn get_encoder() {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
@@ -37,6 +32,9 @@ EncodeTiledFn get_encoder() {
   }
   return fn;
 }
+}  // namespace cvr
+
+namespace {
 
 uint16_t f32_to_bf16_bits(float x) {
   uint32_t u;

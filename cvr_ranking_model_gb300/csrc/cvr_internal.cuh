@@ -507,6 +507,12 @@ inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// cuTensorMapEncodeTiled, looked up once (null when the driver has none)
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encoder();
+
 // kernel launchers (each returns the launch's error code)
 cudaError_t prepare_gemm_kernels();  // shared-memory attributes; once per device before any launch
 cudaError_t prepare_mlp_kernels();

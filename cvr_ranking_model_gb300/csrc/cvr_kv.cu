@@ -18,12 +18,20 @@ struct cvr_kv {
   cudaStream_t stream = nullptr;
   cvr_kv_config cfg{};
   int page_log2 = 0;
+  KvAttendKernel attend{};      // (kernel null: no pools)
+  CUtensorMap tm_k, tm_v;
+  void* ws = nullptr;           // the attention's workspace: parts, then the counters
+  float *part_o = nullptr, *part_ml = nullptr;
+  unsigned* count = nullptr;
+  size_t count_bytes = 0;
   int* err_host = nullptr;      // pinned, mapped: the error bits since the last sync
   int* err_host_dev = nullptr;  // its device address
   char last_error[256] = "";
 };
 
 namespace {
+
+constexpr int kMinTiles = 1;  // least tiles of an attention CTA's run
 
 cvr_status kv_fail(cvr_kv* h, cvr_status s, const char* fmt, ...) {
   va_list ap;
@@ -111,6 +119,58 @@ const char* bad_config(const cvr_kv_config* c) {
   return c->v ? bad_strides(c->v_stride, c) : nullptr;
 }
 
+// A pool as [page][head][half][token][line]: a copied box is one page's (or a tile's) rows of one head, in lines of at
+// most 128 bytes swizzled as the attention kernel reads them.
+bool encode_pool(CUtensorMap* m, void* base, const int64_t* stride, const cvr_kv_config* c, int tile) {
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return false;
+  const int eb = elt_bytes(c->cache_dtype), row = c->head_dim * eb, line = row < 128 ? row : 128;
+  // (the stride of a dimension of one row is never used, but has to be a valid one)
+  auto bytes = [&](int d, int64_t size) { return (cuuint64_t)(size == 1 ? 256 : stride[d] * eb); };
+  const cuuint64_t dims[5] = {(cuuint64_t)(line / eb), (cuuint64_t)c->page_size, (cuuint64_t)(row / line),
+                              (cuuint64_t)c->kv_heads, (cuuint64_t)c->n_pages};
+  const cuuint64_t strides[4] = {bytes(2, c->page_size), 128, bytes(1, c->kv_heads), bytes(0, c->n_pages)};
+  const cuuint32_t box[5] = {(cuuint32_t)(line / eb), (cuuint32_t)(c->page_size < tile ? c->page_size : tile),
+                             (cuuint32_t)(row / line), 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapSwizzle swizzle = line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  // L2 fetches whole runs of rows where a head's rows are next to each other, else no more than a row
+  const bool dense = stride[2] == c->head_dim;
+  const CUtensorMapL2promotion l2 = dense || row >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                    : row == 128        ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                    : row == 64         ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                        : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+  return enc(m, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Everything the attention of a handle with pools needs: the kernel, the pools' tensor maps and the workspace.
+cudaError_t prepare_attend(cvr_kv* h) {
+  const cvr_kv_config* c = &h->cfg;
+  const bool i8 = c->cache_dtype == CVR_DTYPE_I8;
+  const int group = c->q_heads / c->kv_heads;
+  h->attend = c->head_dim == 32   ? kv_attend_kernel_32(c->dtype, i8, group)
+              : c->head_dim == 64 ? kv_attend_kernel_64(c->dtype, i8, group)
+                                  : kv_attend_kernel_128(c->dtype, i8, group);
+  if (!encode_pool(&h->tm_k, c->k, c->k_stride, c, h->attend.tile)) return cudaErrorInvalidValue;
+  h->tm_v = h->tm_k;
+  if (c->v && !encode_pool(&h->tm_v, c->v, c->v_stride, c, h->attend.tile)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(h->attend.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h->attend.smem);
+  const size_t slots = (size_t)h->num_sms * h->attend.ctas_per_sm * 2 * group;
+  const size_t o_bytes = slots * c->head_dim * 4, ml_bytes = slots * 8;
+  h->count_bytes = (size_t)c->max_req * c->kv_heads * 4;
+  if (e == cudaSuccess) e = cudaMalloc(&h->ws, o_bytes + ml_bytes + h->count_bytes);
+  if (e != cudaSuccess) {
+    h->ws = nullptr;
+    return e;
+  }
+  h->part_o = static_cast<float*>(h->ws);
+  h->part_ml = h->part_o + slots * c->head_dim;
+  h->count = reinterpret_cast<unsigned*>(h->part_ml + slots * 2);
+  // (on the handle's stream, so that it is ordered before the first call whatever stream that is)
+  return cudaMemsetAsync(h->count, 0, h->count_bytes, h->stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -135,6 +195,7 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
     *h->err_host = 0;
     e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&h->err_host_dev), h->err_host, 0);
   }
+  if (e == cudaSuccess && cfg->k) e = prepare_attend(h);
   if (e != cudaSuccess) {
     fprintf(stderr, "cvr_kv_create: %s\n", cudaGetErrorString(e));
     cudaGetLastError();
@@ -234,18 +295,13 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
   KvAttendArgs a;
   a.q = q;
-  a.k = c.k;
   a.v = c.v;
   a.out = out;
   a.lse = lse;
   a.lens = lens;
   a.table = table;
   a.k_scale = c.k_scale;
-  a.v_scale = c.v_scale;
-  for (int i = 0; i < 3; ++i) {
-    a.k_stride[i] = c.k_stride[i];
-    a.v_stride[i] = c.v_stride[i];
-  }
+  a.v_scale = c.v ? c.v_scale : c.k_scale;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.n_pages = c.n_pages;
@@ -257,8 +313,27 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   a.page_log2 = h->page_log2;
   a.max_pages = c.max_pages;
   a.window = c.window;
+  a.min_tiles = kMinTiles;
+  a.part_o = h->part_o;
+  a.part_ml = h->part_ml;
+  a.count = h->count;
   a.err = h->err_host_dev;
-  const cudaError_t e = launch_kv_attend(a, c.dtype, c.cache_dtype == CVR_DTYPE_I8, c.head_dim, h->num_sms, h->stream);
+  // one CTA per least run of the tiles that there can be at most, at most as many as the SMs hold at once
+  const int64_t seen = c.window && c.window < c.max_pages * c.page_size ? c.window + h->attend.tile : (int64_t)c.max_pages * c.page_size;
+  const int64_t most = n_req * c.kv_heads * ((seen + h->attend.tile - 1) / h->attend.tile);
+  const int64_t want = (most + kMinTiles - 1) / kMinTiles, fit = (int64_t)h->num_sms * h->attend.ctas_per_sm;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(want < fit ? want : fit));
+  lc.blockDim = dim3(kKvAttendThreads);
+  lc.dynamicSmemBytes = h->attend.smem;
+  lc.stream = h->stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  void* args[] = {&a, &h->tm_k, &h->tm_v};
+  const cudaError_t e = cudaLaunchKernelExC(&lc, h->attend.kernel, args);
   return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_attend launch");
 }
 
@@ -271,7 +346,11 @@ cvr_status cvr_kv_sync(cvr_kv* h) {
   volatile int* word = h->err_host;
   const int ew = *word;
   *word = 0;
-  if (ew & kErrTimeout) return kv_fail(h, CVR_E_TIMEOUT, "a bounded device-side wait gave up");
+  if (ew & kErrTimeout) {
+    // a CTA that gave up may have left a counter part-way; the next call starts from zero
+    if (h->count) cudaMemset(h->count, 0, h->count_bytes);
+    return kv_fail(h, CVR_E_TIMEOUT, "a bounded device-side wait gave up");
+  }
   if (ew & kKvErrLens) return kv_fail(h, CVR_E_INPUT, "a length, new length, held count or list head is out of range");
   if (ew & kKvErrPages) return kv_fail(h, CVR_E_PAGES, "the free list ran out of pages");
   if (ew & kKvErrSlots) return kv_fail(h, CVR_E_INPUT, "more new tokens than the slot map holds");
@@ -291,6 +370,7 @@ void cvr_kv_destroy(cvr_kv* h) {
       cudaStreamSynchronize(h->stream);
       cudaFreeHost(h->err_host);
     }
+    if (h->ws) cudaFree(h->ws);
   }
   delete h;
 }

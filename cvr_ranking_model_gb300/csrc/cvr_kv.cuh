@@ -38,21 +38,34 @@ struct KvAppendArgs {
 };
 
 struct KvAttendArgs {
-  const void *q, *k, *v;  // v null: K = V
+  const void *q, *v;  // v null: K = V
   void* out;
   float* lse;
   const int32_t *lens, *table;
   const float *k_scale, *v_scale;
-  int64_t k_stride[3], v_stride[3];
   int64_t q_stride, out_stride, n_pages;
   float scale;
   int n_req, q_heads, kv_heads, group, page_log2, max_pages, window;
+  int min_tiles;    // least tiles of a CTA's run
+  // workspace: what a CTA leaves of the (request, head) that its run ends in [1] or began before it [0]
+  float *part_o, *part_ml;  // [CTA][2][group][head_dim], [CTA][2][group][m, l]
+  unsigned* count;          // [max_req][kv_heads] parts written (zero between calls)
   int* err;
 };
+
+constexpr int kKvAttendThreads = 160;  // four consumer warps and a producer
+// An instance of the attention kernel (const KvAttendArgs, K's and V's tensor maps).
+struct KvAttendKernel {
+  const void* kernel;
+  int smem, ctas_per_sm;
+  int tile;  // tokens per tile
+};
+KvAttendKernel kv_attend_kernel_32(int dtype, bool int8, int group);
+KvAttendKernel kv_attend_kernel_64(int dtype, bool int8, int group);
+KvAttendKernel kv_attend_kernel_128(int dtype, bool int8, int group);
 
 cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s);
 // dtype: a cvr_dtype of the rows; int8: the pool holds 8-bit integers
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, bool int8, int num_sms, cudaStream_t s);
-cudaError_t launch_kv_attend(const KvAttendArgs& a, int dtype, bool int8, int head_dim, int num_sms, cudaStream_t s);
 
 }  // namespace cvr

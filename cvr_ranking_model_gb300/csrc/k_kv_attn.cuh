@@ -1,0 +1,853 @@
+// Attention of one query token per request over a paged history (cvr_kv_attend of include/cvr.h): for query head i of
+// request r, with s_j = scale q . k_j over the tokens j that it sees,
+//   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  m = max_j s_j,  lse = m + ln sum_j exp(s_j - m).
+// Every K and V row is read once for all the query heads that share it, so the floor is the bytes of the seen rows.
+//
+// Work: a tile is up to 16 KB of one kv head's K rows and the V rows beside them. The tiles of all requests and heads
+// form one line (request, then head, then position); a persistent grid cuts it into equal runs, so ragged lengths,
+// few long histories and many short ones load the SMs alike. A CTA finds its run by scanning the lengths itself. What
+// a CTA leaves of a (request, head) that it shares with others goes to the workspace as (m, l, o); the last of them to
+// arrive joins the parts in order, so results do not depend on which it is.
+//
+// A CTA is one producer warp and four consumer warps. The producer turns page ids into TMA copies (a box per page)
+// into a ring of units, K and V in turn, swizzled so that ldmatrix reads without bank conflicts, and runs ahead across
+// requests. A consumer warp takes every fourth block of 16 tokens of a tile (or, for more than 16 query heads per kv head,
+// 16 of the heads): S = Q K^T and O += P V on mma.sync m16n8k16 with the running maximum, sum and O in registers.
+//   - mma.sync, not tcgen05: with at most 64 query rows a tile has 4 to 64 operations per byte read, an M = 128 MMA would
+//     be almost all padding, and P stays in registers between the two products. The tensor pipe is idle most of the time.
+//   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-9 in bf16) does not add to
+//     the output's. With at most 8 query rows the halves sit in the two halves of the 16-row tile, at no extra cost.
+//   - 8-bit rows become fp16 exactly (1024 + q by a byte permute, minus 1152); K's scale multiplies the logit, V's scale
+//     the weight, whose products are kept in fp16's range by the warp's largest scale so far.
+#pragma once
+
+#include <type_traits>
+
+#include "../../include/cvr.h"
+#include "cvr_kv.cuh"
+
+namespace cvr {
+namespace kv {
+
+constexpr int kConsumers = 4;                       // consumer warps
+constexpr int kThreads = (kConsumers + 1) * 32;     // and the producer
+static_assert(kThreads == kKvAttendThreads, "the launch's block");
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64
+template <bool I8, int D, int MODE>
+struct Shape {
+  static constexpr int MT = MODE == 3 ? 4 : MODE == 2 ? 2 : 1;  // 16-row tiles of query heads
+  static constexpr int KP = kConsumers / MT;                    // consumer warps that share a row tile's tokens
+  static constexpr int kRow = D * (I8 ? 1 : 2);                 // bytes of a row
+  static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
+  static constexpr int kHalves = kRow / kLine;
+  static constexpr int TK = 16384 / kRow < 256 ? 16384 / kRow : 256;  // tokens per tile
+  static constexpr int kUnit = TK * kRow;
+  static constexpr int kCtasPerSm = MT == 1 ? 2 : 1;
+  // ring units: what fits two CTAs (one for more than 16 query rows) into an SM beside the query and joining areas
+  static constexpr int kRing = (MT == 1 ? 5 : 9) * 16384 / kUnit;
+  static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
+  static constexpr int kQBytes = MT * 16 * kQRow;
+  static constexpr int kORow = D + (I8 ? 16 : 8);               // padded fp32 rows of the joining area
+  static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
+  // blocks of 16 tokens that a warp takes per tile, and per softmax step
+  static constexpr int NB = TK / 16 / KP, NBS = NB < 4 ? NB : 4;
+  // shared memory
+  static constexpr int oScale = kRing * kUnit;
+  static constexpr int oQ = oScale + kRing * kScaleBytes;
+  static constexpr int oO = oQ + 2 * kQBytes;
+  static constexpr int oStat = oO + kConsumers * 8 * kORow * 4;
+  static constexpr int oTile = oStat + 2 * kConsumers * 16 * 4;
+  static constexpr int oBar = oTile + kRing * 32;
+  static constexpr int kSmem = oBar + (2 * kRing + 5) * 8 + 64 + 1024;  // (1024: the ring's alignment)
+  static_assert(kSmem <= (kCtasPerSm == 2 ? 115712 : 232448), "two CTAs share an SM's 228 KB");
+};
+
+struct __align__(16) Tile {
+  int r, h, k0, flags;       // request, kv head, first token of the tile
+  int lo, len, i0, n_parts;  // tokens seen: [lo, len); CTAs i0 .. i0 + n_parts - 1 share this (request, head)
+};
+constexpr int kFirst = 1, kLast = 2, kStarts = 4;  // first / last tile of this CTA's part; the part holds the start
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) { return pack_bf16(a, b); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t x);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two of the four signed bytes of x as an fp16 pair: SEL picks the bytes (0x4140: 0 and 1, 0x4342: 2 and 3, 0x4240: 0 and
+// 2, 0x4341: 1 and 3); x ^ 0x80 per byte is q + 128, the bits 0x64.. are 1024 + (q + 128)
+template <int SEL>
+__device__ __forceinline__ uint32_t i8_pair(uint32_t x) {
+  const uint32_t u = __byte_perm(x ^ 0x80808080u, 0x64646464u, SEL);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// the tokens that a request of length `len` sees begin at the result
+__device__ __forceinline__ int seen_from(const KvAttendArgs& a, int len) { return a.window ? max(0, len - a.window) : 0; }
+__device__ __forceinline__ int clamped_len(const KvAttendArgs& a, int len) {
+  const int most = a.max_pages << a.page_log2;  // (at most 2^30)
+  return len < 0 ? 0 : min(len, most);
+}
+template <int TK>
+__device__ __forceinline__ int tiles_of(const KvAttendArgs& a, int len) {
+  return (len + TK - 1) / TK - seen_from(a, len) / TK;
+}
+
+template <typename T, bool I8, int D, int MODE>
+__global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
+    attend_kernel(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v) {
+  typedef Shape<I8, D, MODE> S;
+  constexpr int MT = S::MT, KP = S::KP, TK = S::TK, NB = S::NB, NBS = S::NBS, RING = S::kRing;
+  constexpr bool R8 = MODE == 0;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + S::oBar);
+  uint64_t* const empty = full + RING;
+  uint64_t* const q_full = empty + RING;   // [2]
+  uint64_t* const q_empty = q_full + 2;    // [2]
+  uint64_t* const meet = q_empty + 2;      // the consumer warps' barrier
+  volatile int* const abort_flag = reinterpret_cast<int*>(meet + 1);
+  int* const s_last = const_cast<int*>(abort_flag) + 1;
+  int64_t* const s_start = reinterpret_cast<int64_t*>(s_last + 1);  // (8-byte aligned: two ints after `meet`)
+  int* const s_req = reinterpret_cast<int*>(s_start + 1);
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(sm + S::oStat);     // scan scratch, before the first part ends
+  Tile* const tiles = reinterpret_cast<Tile*>(sm + S::oTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.kv_heads, G = a.group;
+  const bool two = a.v != nullptr;  // V is a pool of its own
+
+  if (tid == 0) {
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kConsumers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, kConsumers);
+    }
+    mbar_init(meet, kConsumers);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    if (two) tma_prefetch_desc(&tm_v);
+  }
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- this CTA's run of the line of tiles ----
+  const int chunk = (a.n_req + kThreads - 1) / kThreads;
+  const int c0 = min(tid * chunk, a.n_req), c1 = min(c0 + chunk, a.n_req);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int r = c0; r < c1; ++r) {
+    const int raw = __ldg(a.lens + r), len = clamped_len(a, raw);
+    bad |= raw != len;
+    mine += tiles_of<TK>(a, len);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(a.err, kKvErrLens);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += u;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  cta_sync();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w <= kConsumers; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  total *= H;
+  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_tiles);
+  const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
+  const int64_t n_tiles = begin < end ? end - begin : 0;
+  if (n_tiles > 0 && begin >= before * H && begin < (before + mine) * H) {
+    for (int r = c0; r < c1; ++r) {
+      const int t = tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r)));
+      if (begin < (before + t) * H) {
+        *s_start = before;
+        *s_req = r;
+        break;
+      }
+      before += t;
+    }
+  }
+  cta_sync();
+
+  if (warp == kConsumers) {
+    // ================= producer =================
+    const int log2_br = min(a.page_log2, 31 - __clz(TK));  // rows of a box: a page, or a tile of a longer page
+    const int br = 1 << log2_br, n_box_max = TK >> log2_br;
+    int slot = 0, filled = 0;  // the ring's next unit, and the units filled so far (at most RING)
+    uint32_t phase = 0;        // parity of the ring's round
+    bool ok = true;
+    int last_parts = 0;
+    if (n_tiles > 0) {
+      int r = *s_req, wb = r;  // lens of the 32 requests from wb on, one per lane
+      int64_t P = *s_start;    // tiles of one head before request r
+      int wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
+      int len = __shfl_sync(0xffffffffu, wl, 0), lo = seen_from(a, len), t0 = lo / TK, n_t = tiles_of<TK>(a, len);
+      int h = (int)((begin - P * H) / n_t), t = (int)((begin - P * H) % n_t);
+      int parts = 0;  // parts begun
+      int i0 = 0, n_parts = 1;
+      bool starts = true;
+      Tile cur, nxt;
+      int cur_page = 0, nxt_page = 0, cur_need = 0, nxt_need = 0;
+      // the tile (r, h, t), number i of this CTA: its description, and in lane b the page of its box b
+      auto prepare = [&](int64_t i) {
+        if (i > 0) {
+          if (++t == n_t) {
+            t = 0;
+            if (++h == H) {
+              h = 0;
+              P += n_t;
+              int from = r + 1;
+              unsigned some;
+              while (true) {  // the next request with a tile
+                if (from >= wb + 32) {
+                  wb = from;
+                  wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
+                }
+                some = __ballot_sync(0xffffffffu, wl > 0 && wb + lane >= from);
+                if (some || wb + 32 >= a.n_req) break;
+                from = wb + 32;
+              }
+              const int src = some ? __ffs(some) - 1 : 0;
+              r = min(wb + src, a.n_req - 1);
+              len = __shfl_sync(0xffffffffu, wl, src);
+              lo = seen_from(a, len);
+              t0 = lo / TK;
+              n_t = max(1, tiles_of<TK>(a, len));
+            }
+          }
+        }
+        const bool first = i == 0 || t == 0;
+        if (first) {
+          const int64_t fb = P * H + (int64_t)h * n_t;
+          starts = fb >= begin;
+          i0 = (int)(fb / per);
+          n_parts = (int)((fb + n_t - 1) / per) - i0 + 1;
+        }
+        nxt.r = r;
+        nxt.h = h;
+        nxt.k0 = (t0 + t) * TK;
+        nxt.flags = (first ? kFirst : 0) | (i == n_tiles - 1 || t == n_t - 1 ? kLast : 0) | (starts ? kStarts : 0);
+        nxt.lo = lo;
+        nxt.len = len;
+        nxt.i0 = i0;
+        nxt.n_parts = n_parts;
+        const int at = nxt.k0 + (lane << log2_br);
+        nxt_need = lane < n_box_max && at < len && at + br > lo;
+        nxt_page = nxt_need ? __ldg(a.table + (int64_t)r * a.max_pages + (at >> a.page_log2)) : 0;
+      };
+      prepare(0);
+      for (int64_t i = 0; i < n_tiles && ok; ++i) {
+        cur = nxt;
+        cur_page = nxt_page;
+        cur_need = nxt_need;
+        if (i + 1 < n_tiles) prepare(i + 1);  // (its page ids arrive while this tile waits for the ring)
+        if (cur_need && (cur_page < 0 || cur_page >= a.n_pages)) {
+          atomicOr(a.err, kKvErrPage);
+          cur_page = 0;
+        }
+        const int n_box = __popc(__ballot_sync(0xffffffffu, cur_need != 0));
+        const int row = (cur.k0 + (lane << log2_br)) & ((1 << a.page_log2) - 1);
+        const int64_t scale_at = (((int64_t)cur_page * H + cur.h) << a.page_log2) + row;
+        if (cur.flags & kFirst) {
+          // the part's query rows
+          const int b = parts & 1;
+          ok = mbar_wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
+          __syncwarp();
+          const T* q = static_cast<const T*>(a.q) + cur.r * a.q_stride + (int64_t)cur.h * G * D;
+          for (int g = lane; g < G; g += 32) bulk_load(smem_u32(sm + S::oQ + b * S::kQBytes + g * S::kQRow), q + g * D, D * 2, q_full + b);
+          ++parts;
+        }
+#pragma unroll 1
+        for (int w = 0; w < (two ? 2 : 1); ++w) {
+          ok = mbar_wait_warp(empty + slot, phase ^ 1, abort_flag, a.err);
+          if (!ok) break;
+          if (lane == 0) {
+            if (w == 0) tiles[slot] = cur;
+            mbar_expect_tx(full + slot, (uint32_t)(n_box * br) * (S::kRow + (I8 ? 4 : 0)));
+          }
+          __syncwarp();
+          if (cur_need) {
+            uint8_t* dst = sm + slot * S::kUnit + (lane << log2_br) * S::kRow;
+            tma_load_5d(dst, w ? &tm_v : &tm_k, full + slot, 0, row, 0, cur.h, cur_page);
+            if (I8)
+              bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
+                        (w ? a.v_scale : a.k_scale) + scale_at, 4 << log2_br, full + slot);
+          }
+          filled = min(filled + 1, RING);
+          if (++slot == RING) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      last_parts = parts;
+    }
+    // requests that see nothing, shared out over the grid
+    for (int rb = blockIdx.x * 32; rb < a.n_req; rb += gridDim.x * 32) {
+      const bool none = rb + lane < a.n_req && clamped_len(a, __ldg(a.lens + rb + lane)) == 0;
+      unsigned m = __ballot_sync(0xffffffffu, none);
+      while (m) {
+        const int r = rb + __ffs(m) - 1;
+        m &= m - 1;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_stride);
+        for (int i = lane; i < a.q_heads * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int i = lane; i < a.q_heads; i += 32) a.lse[(int64_t)r * a.q_heads + i] = -INFINITY;
+      }
+    }
+    // the copies in flight land before the CTA's shared memory can go, also when a consumer's wait gave up
+    for (int u = 0; u < filled; ++u) {
+      if (--slot < 0) {
+        slot = RING - 1;
+        phase ^= 1;
+      }
+      mbar_drain(full + slot, phase);
+    }
+    for (int p = max(0, last_parts - 2); p < last_parts; ++p) mbar_drain(q_full + (p & 1), (p >> 1) & 1);
+    return;
+  }
+
+  // ================= consumers =================
+  const int gid = lane >> 2, tig = lane & 3;
+  const int mt = warp % MT, kp = warp / MT;  // row tile, share of the tokens
+  const int log2_br = min(a.page_log2, 31 - __clz(TK));
+  const float sl2 = a.scale * kLog2e;
+  // p is kept times 2^12 in fp16 (it is at most 1), so that small weights keep their bits
+  constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
+  constexpr float kShift = kF16 ? 12.f : 0.f;
+  typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
+  uint32_t meets = 0;
+  bool ok = true;
+  auto consumer_sync = [&]() {  // a bounded barrier of the four warps
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    ok = mbar_wait_warp(meet, meets & 1, abort_flag, a.err) && ok;
+    ++meets;
+  };
+  // byte offset of a row's line within a unit, for the row of token `key` of the tile (its second half follows at
+  // half_step), and the swizzle of the 8 rows that a matrix is loaded from
+  auto row_at = [&](int key) -> uint32_t {
+    return (uint32_t)(((key >> log2_br) * S::kHalves << log2_br) + (key & ((1 << log2_br) - 1))) * S::kLine;
+  };
+  const uint32_t half_step = (uint32_t)S::kLine << log2_br;
+  const int l7 = lane & 7;
+  const uint32_t swz = (S::kLine == 128 ? l7 : S::kLine == 64 ? (l7 >> 1) & 3 : (l7 >> 2) & 1) << 4;
+  auto chunk_at = [&](int c) -> uint32_t {  // the row's 16-byte piece c
+    return (c >> 3) * half_step + ((uint32_t)((c & 7) << 4) ^ swz);
+  };
+
+  uint32_t qf[D / 16][4];
+  float o[D / 8][4];
+  float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+  float cA = sl2, cB = sl2;       // logit factors of rows A (gid) and B (gid + 8)
+  float vmax = 0x1p-100f;         // 8 bits: the largest row scale of V so far (floored)
+  int ks = 0, parts = 0;          // the ring's next unit, and parts begun
+  uint32_t phase = 0;
+  float* const s_o = reinterpret_cast<float*>(sm + S::oO);
+  float* const s_m = reinterpret_cast<float*>(sm + S::oStat);
+  float* const s_l = s_m + kConsumers * 16;
+
+  for (int64_t i = 0; i < n_tiles; ++i) {
+    ok = mbar_wait_warp(full + ks, phase, abort_flag, a.err);
+    if (!ok) return;
+    const Tile tl = tiles[ks];
+    const uint32_t k_unit = smem_u32(sm + ks * S::kUnit);
+    if (tl.flags & kFirst) {
+      const int b = parts & 1;
+      ok = mbar_wait_warp(q_full + b, (parts >> 1) & 1, abort_flag, a.err);
+      if (!ok) return;
+      const uint8_t* qs = sm + S::oQ + b * S::kQBytes + mt * 16 * S::kQRow;
+      const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
+      if (!I8) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
+          qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) : 0u;
+          qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) : 0u;
+          qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) : 0u;
+          qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) : 0u;
+        }
+      } else {
+        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
+        float mulA = 1.f, mulB = 1.f;
+        uint2 xa[D / 16], xb[D / 16];
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
+          xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
+          xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
+        }
+        if (std::is_same<T, __nv_bfloat16>::value) {
+          // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
+          // of it, 2^-25 of it below
+          float bigA = 0.f, bigB = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
+            bigA = fmaxf(fmaxf(bigA, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+            bigB = fmaxf(fmaxf(bigB, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(z.x), fabsf(z.y)));
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
+            bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
+          }
+          const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
+          const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
+          mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
+          mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
+          cA = fitA ? sl2 * __uint_as_float(eA << 23) : sl2;
+          cB = fitB ? sl2 * __uint_as_float(eB << 23) : sl2;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
+          qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
+          qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
+          qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
+          qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty + b);
+      ++parts;
+      mA = mB = -INFINITY;
+      lA = lB = 0.f;
+      vmax = 0x1p-100f;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    }
+    const int vs_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
+    const uint32_t vs_phase = vs_slot < ks ? phase ^ 1 : phase;
+    const uint32_t v_unit = smem_u32(sm + vs_slot * S::kUnit);
+    const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + ks * S::kScaleBytes);
+    const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + vs_slot * S::kScaleBytes);
+    // tokens of the tile that are seen, and whether that is not all of them
+    const int j0 = max(tl.lo - tl.k0, 0), j1 = min(tl.len - tl.k0, TK);
+    const bool partial = j0 > 0 || j1 < TK;
+
+#pragma unroll 1
+    for (int sub = 0; sub < NB / NBS; ++sub) {
+      float s[NBS][2][4];
+#pragma unroll
+      for (int b = 0; b < NBS; ++b) {
+        const int key = ((sub * NBS + b) * KP + kp) * 16;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
+        if (key + 16 > j0 && key < j1) {
+          // matrices: tokens 0-7 and 8-15 of the block, two 16-byte pieces each
+          const uint32_t base = k_unit + row_at(key + (lane >> 4) * 8 + l7);
+          if (!I8) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t f[4];
+              ldsm4(f, base + chunk_at(2 * k + ((lane >> 3) & 1)));
+              mma16816<M>(s[b][0], qf[k], f[0], f[1]);
+              mma16816<M>(s[b][1], qf[k], f[2], f[3]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t f[4];
+              ldsm4(f, base + chunk_at(2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                mma16816<M>(s[b][0], qf[2 * k + e], i8_pair<0x4140>(f[e]), i8_pair<0x4342>(f[e]));
+                mma16816<M>(s[b][1], qf[2 * k + e], i8_pair<0x4140>(f[2 + e]), i8_pair<0x4342>(f[2 + e]));
+              }
+            }
+          }
+        }
+      }
+      // logits in units of ln 2; tokens that are not seen are out
+      float nA = mA, nB = mB;
+#pragma unroll
+      for (int b = 0; b < NBS; ++b)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
+          float k0 = 1.f, k1 = 1.f;
+          if (I8) {
+            const float2 sc = *reinterpret_cast<const float2*>(k_sc + key);
+            k0 = sc.x;
+            k1 = sc.y;
+          }
+          s[b][n][0] *= I8 ? cA * k0 : cA;
+          s[b][n][1] *= I8 ? cA * k1 : cA;
+          if (!R8) {
+            s[b][n][2] *= I8 ? cB * k0 : cB;
+            s[b][n][3] *= I8 ? cB * k1 : cB;
+          }
+          if (partial) {
+            if (key < j0 || key >= j1) s[b][n][0] = s[b][n][2] = -INFINITY;
+            if (key + 1 < j0 || key + 1 >= j1) s[b][n][1] = s[b][n][3] = -INFINITY;
+          }
+          nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
+          if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
+        }
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
+        if (!R8) nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
+      }
+      float w_mul = 1.f;  // 8 bits: weights enter the second product times 2^14 / vmax
+      float grow = 1.f;
+      if (I8) {
+        float big = vmax;
+#pragma unroll
+        for (int b = 0; b < NBS; ++b)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
+            if (sub == 0 && b == 0 && n == 0 && two) {
+              ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
+              if (!ok) return;
+            }
+            const float2 sc = *reinterpret_cast<const float2*>(v_sc + key);
+            if (key >= j0 && key < j1) big = fmaxf(big, sc.x);
+            if (key + 1 >= j0 && key + 1 < j1) big = fmaxf(big, sc.y);
+          }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+        grow = vmax / big;
+        vmax = big;
+        w_mul = 0x1p14f / big;
+      }
+      // (a maximum of -infinity is left out of the exponent: nothing was seen, or every logit is -infinity)
+      const float baseA = nA == -INFINITY ? 0.f : nA, baseB = nB == -INFINITY ? 0.f : nB;
+      if (__any_sync(0xffffffffu, nA > mA || (!R8 && nB > mB) || grow != 1.f)) {
+        const float fA = ex2(mA - baseA), fB = R8 ? fA : ex2(mB - baseB);
+        lA *= fA;
+        if (!R8) lB *= fB;
+        const float gA = fA * grow, gB = fB * grow;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= gA;
+          o[j][1] *= gA;
+          o[j][2] *= gB;
+          o[j][3] *= gB;
+        }
+        mA = nA;
+        mB = nB;
+      }
+      if (!I8 && sub == 0 && two) {
+        ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
+        if (!ok) return;
+      }
+      const float subA = baseA - kShift, subB = baseB - kShift;
+#pragma unroll
+      for (int b = 0; b < NBS; ++b) {
+        const int key0 = ((sub * NBS + b) * KP + kp) * 16;
+        if (!(key0 + 16 > j0 && key0 < j1)) continue;
+        uint32_t hi[4], lw[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float pA0 = ex2(s[b][n][0] - subA), pA1 = ex2(s[b][n][1] - subA), pB0 = 0.f, pB1 = 0.f;
+          lA += pA0 + pA1;
+          if (!R8) {
+            pB0 = ex2(s[b][n][2] - subB);
+            pB1 = ex2(s[b][n][3] - subB);
+            lB += pB0 + pB1;
+          }
+          if (I8) {
+            const int key = key0 + n * 8 + 2 * tig;
+            const float2 sc = *reinterpret_cast<const float2*>(v_sc + key);
+            const float w0 = key >= j0 && key < j1 ? sc.x * w_mul : 0.f;
+            const float w1 = key + 1 >= j0 && key + 1 < j1 ? sc.y * w_mul : 0.f;
+            pA0 *= w0;
+            pA1 *= w1;
+            pB0 *= w0;
+            pB1 *= w1;
+          }
+          const uint32_t hA = pack2<M>(pA0, pA1);
+          const float2 fA = unpack2<M>(hA);
+          const uint32_t dA = pack2<M>(pA0 - fA.x, pA1 - fA.y);
+          hi[2 * n] = hA;
+          if (R8) {
+            hi[2 * n + 1] = dA;
+          } else {
+            const uint32_t hB = pack2<M>(pB0, pB1);
+            const float2 fB = unpack2<M>(hB);
+            hi[2 * n + 1] = hB;
+            lw[2 * n] = dA;
+            lw[2 * n + 1] = pack2<M>(pB0 - fB.x, pB1 - fB.y);
+          }
+        }
+        // rows of V that are not seen may hold anything: their bits are cleared (0 times an infinity is no number)
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (!I8 && partial) {
+          const int key = key0 + 2 * tig;
+          keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
+          keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
+        }
+        const uint32_t base = v_unit + row_at(key0 + ((lane >> 3) & 1) * 8 + l7);
+        if (!I8) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t f[4];
+            ldsm4_trans(f, base + chunk_at(2 * c + (lane >> 4)));
+            if (partial) {
+              f[0] &= keep0;
+              f[1] &= keep1;
+              f[2] &= keep0;
+              f[3] &= keep1;
+            }
+            mma16816<M>(o[2 * c], hi, f[0], f[1]);
+            mma16816<M>(o[2 * c + 1], hi, f[2], f[3]);
+            if (!R8) {
+              mma16816<M>(o[2 * c], lw, f[0], f[1]);
+              mma16816<M>(o[2 * c + 1], lw, f[2], f[3]);
+            }
+          }
+        } else {
+          // a loaded pair of bytes is two dims of one token: the even and the odd dims of 16 form one n-tile each
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t f[4];
+            ldsm4_trans(f, base + chunk_at(2 * c + (lane >> 4)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t e0 = i8_pair<0x4240>(f[2 * e]), e1 = i8_pair<0x4240>(f[2 * e + 1]);
+              const uint32_t d0 = i8_pair<0x4341>(f[2 * e]), d1 = i8_pair<0x4341>(f[2 * e + 1]);
+              mma16816<M>(o[4 * c + 2 * e], hi, e0, e1);
+              mma16816<M>(o[4 * c + 2 * e + 1], hi, d0, d1);
+              if (!R8) {
+                mma16816<M>(o[4 * c + 2 * e], lw, e0, e1);
+                mma16816<M>(o[4 * c + 2 * e + 1], lw, d0, d1);
+              }
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(empty + ks);
+      if (two) mbar_arrive(empty + vs_slot);
+    }
+    phase = vs_slot + 1 == RING ? vs_phase ^ 1 : vs_phase;
+    ks = vs_slot + 1 == RING ? 0 : vs_slot + 1;
+    if (!(tl.flags & kLast)) continue;
+
+    // ---- the part's end: the warps' (m, l, o) to shared memory, 8 rows of each tile at a time, and summed ----
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      lA += __shfl_xor_sync(0xffffffffu, lA, d);
+      if (!R8) lB += __shfl_xor_sync(0xffffffffu, lB, d);
+    }
+    const float o_mul = I8 ? vmax * 0x1p-14f : 1.f;
+    const int part_slot = (int)blockIdx.x * 2 + ((tl.flags & kStarts) ? 1 : 0);
+    constexpr int VEC = MT * D / 16 < 4 ? MT * D / 16 : 4;  // values per thread and step
+    constexpr int kPerRow = D / VEC;
+#pragma unroll
+    for (int pass = 0; pass < (R8 ? 1 : 2); ++pass) {
+      consumer_sync();  // (the previous pass or part has been read)
+      if (!ok) return;
+      float* dst = s_o + (warp * 8 + gid) * S::kORow;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const float x = (R8 ? o[j][0] + o[j][2] : o[j][2 * pass]) * o_mul;
+        const float y = (R8 ? o[j][1] + o[j][3] : o[j][2 * pass + 1]) * o_mul;
+        if (!I8) {
+          *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
+        } else if (j & 1) {
+          // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)
+          const float u = (R8 ? o[j - 1][0] + o[j - 1][2] : o[j - 1][2 * pass]) * o_mul;
+          const float v = (R8 ? o[j - 1][1] + o[j - 1][3] : o[j - 1][2 * pass + 1]) * o_mul;
+          *reinterpret_cast<float4*>(dst + (j >> 1) * 16 + 4 * tig) = make_float4(u, x, v, y);
+        }
+      }
+      if (tig == 0) {
+        s_m[warp * 16 + gid] = pass ? mB : mA;
+        s_l[warp * 16 + gid] = pass ? lB : lA;
+      }
+      consumer_sync();
+      if (!ok) return;
+      for (int x = tid; x < 8 * MT * kPerRow; x += kConsumers * 32) {
+        const int row8 = x / kPerRow, c = (x - row8 * kPerRow) * VEC;
+        const int rt = row8 >> 3, g = rt * 16 + pass * 8 + (row8 & 7);
+        if (g >= G) continue;
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * 16 + (row8 & 7)]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float l = 0.f, acc[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int p = 0; p < KP; ++p) {
+          const int w = p * MT + rt;
+          const float f = ex2(s_m[w * 16 + (row8 & 7)] - base);
+          l += f * s_l[w * 16 + (row8 & 7)];
+          const float* src = s_o + (w * 8 + (row8 & 7)) * S::kORow + c;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[e] += f * src[e];
+        }
+        const int qh = tl.h * G + g;
+        if (tl.n_parts == 1) {
+          T* dst_o = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + c;
+          uint32_t pk[VEC / 2];
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) pk[e / 2] = pack2<T>(acc[e] / l, acc[e + 1] / l);
+          if (VEC == 4) *reinterpret_cast<uint2*>(dst_o) = make_uint2(pk[0], pk[VEC / 2 - 1]);
+          else *reinterpret_cast<uint32_t*>(dst_o) = pk[0];
+          if (c == 0 && a.lse) a.lse[(int64_t)tl.r * a.q_heads + qh] = (base - kShift) * kLn2 + logf(l);
+        } else {
+          float* dst_o = a.part_o + ((int64_t)part_slot * G + g) * D + c;
+          if (VEC == 4) __stcg(reinterpret_cast<float4*>(dst_o), make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]));
+          else __stcg(reinterpret_cast<float2*>(dst_o), make_float2(acc[0], acc[1]));
+          if (c == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + (int64_t)part_slot * G + g, make_float2(top, l));
+        }
+      }
+    }
+    if (tl.n_parts == 1) continue;
+
+    // ---- the last CTA of this (request, head) to get here joins the parts ----
+    __threadfence();
+    consumer_sync();
+    if (!ok) return;
+    unsigned* count = a.count + (int64_t)tl.r * H + tl.h;
+    if (tid == 0) {
+      const bool last = atomicAdd(count, 1u) == (unsigned)(tl.n_parts - 1);
+      if (last) *count = 0u;  // ready for the next call
+      *s_last = last;
+      __threadfence();
+    }
+    consumer_sync();
+    if (!ok) return;
+    if (!*s_last) continue;
+    constexpr int VL = D / 32;  // values per lane: a warp joins a row
+    for (int g = warp; g < G; g += kConsumers) {
+      float top = -INFINITY, l = 0.f, acc[VL];
+#pragma unroll
+      for (int e = 0; e < VL; ++e) acc[e] = 0.f;
+      for (int p0 = 0; p0 < tl.n_parts; p0 += 32) {
+        const int p = p0 + lane, n = min(32, tl.n_parts - p0);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (int64_t)((tl.i0 + p) * 2 + (p == 0)) * G + g);
+        float most = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        most = fmaxf(most, top);
+        const float base = most == -INFINITY ? 0.f : most;
+        const float w = ex2(ml.x - base), f = ex2(top - base);
+        float part_l = ml.y * w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, d);
+        l = l * f + part_l;
+        top = most;
+#pragma unroll
+        for (int e = 0; e < VL; ++e) acc[e] *= f;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          const float* src = a.part_o + ((int64_t)((tl.i0 + p0 + k) * 2 + (p0 + k == 0)) * G + g) * D + lane * VL;
+          float x[VL];
+          if (VL == 4) *reinterpret_cast<float4*>(x) = __ldcg(reinterpret_cast<const float4*>(src));
+          else if (VL == 2) *reinterpret_cast<float2*>(x) = __ldcg(reinterpret_cast<const float2*>(src));
+          else x[0] = __ldcg(src);
+#pragma unroll
+          for (int e = 0; e < VL; ++e) acc[e] += wk * x[e];
+        }
+      }
+      const int qh = tl.h * G + g;
+      T* dst_o = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + lane * VL;
+      if (VL == 4) *reinterpret_cast<uint2*>(dst_o) = make_uint2(pack2<T>(acc[0] / l, acc[1] / l), pack2<T>(acc[VL - 2] / l, acc[VL - 1] / l));
+      else if (VL == 2) *reinterpret_cast<uint32_t*>(dst_o) = pack2<T>(acc[0] / l, acc[VL - 1] / l);
+      else {
+        const uint32_t x = pack2<T>(acc[0] / l, 0.f);
+        *reinterpret_cast<uint16_t*>(dst_o) = (uint16_t)x;
+      }
+      if (lane == 0 && a.lse)
+        a.lse[(int64_t)tl.r * a.q_heads + qh] = ((top == -INFINITY ? 0.f : top) - kShift) * kLn2 + logf(l);
+    }
+  }
+}
+
+// The instance for a configuration: its kernel, shared memory, CTAs per SM and tile.
+template <int D>
+KvAttendKernel instance(int dtype, bool int8, int group) {
+  const int mode = group <= 8 ? 0 : group <= 16 ? 1 : group <= 32 ? 2 : 3;
+  auto of = [&](auto t, auto i8, auto m) {
+    typedef decltype(t) T;
+    typedef Shape<decltype(i8)::value, D, decltype(m)::value> S;
+    return KvAttendKernel{reinterpret_cast<const void*>(&attend_kernel<T, decltype(i8)::value, D, decltype(m)::value>), S::kSmem,
+                          S::kCtasPerSm, S::TK};
+  };
+  auto by_mode = [&](auto t, auto i8) {
+    if (mode == 0) return of(t, i8, std::integral_constant<int, 0>());
+    if (mode == 1) return of(t, i8, std::integral_constant<int, 1>());
+    if (mode == 2) return of(t, i8, std::integral_constant<int, 2>());
+    return of(t, i8, std::integral_constant<int, 3>());
+  };
+  if (dtype == CVR_DTYPE_BF16) return int8 ? by_mode(__nv_bfloat16(), std::true_type()) : by_mode(__nv_bfloat16(), std::false_type());
+  return int8 ? by_mode(__half(), std::true_type()) : by_mode(__half(), std::false_type());
+}
+
+}  // namespace kv
+}  // namespace cvr
