@@ -23,6 +23,7 @@ struct cvr_kv {
   void* ws = nullptr;           // the attention's workspace: parts, then the counters
   float *part_o = nullptr, *part_ml = nullptr;
   unsigned* count = nullptr;
+  int n_places = 0;
   size_t count_bytes = 0;
   int* err_host = nullptr;      // pinned, mapped: the error bits since the last sync
   int* err_host_dev = nullptr;  // its device address
@@ -156,17 +157,17 @@ cudaError_t prepare_attend(cvr_kv* h) {
   h->tm_v = h->tm_k;
   if (c->v && !encode_pool(&h->tm_v, c->v, c->v_stride, c, h->attend.tile)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(h->attend.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h->attend.smem);
-  const size_t slots = (size_t)h->num_sms * h->attend.ctas_per_sm * 2 * group;
-  const size_t o_bytes = slots * c->head_dim * 4, ml_bytes = slots * 8;
-  h->count_bytes = (size_t)c->max_req * c->kv_heads * 4;
-  if (e == cudaSuccess) e = cudaMalloc(&h->ws, o_bytes + ml_bytes + h->count_bytes);
+  h->n_places = h->num_sms * h->attend.ctas_per_sm * 2;
+  const size_t rows = (size_t)h->n_places * group;
+  h->count_bytes = (size_t)h->n_places * 2 * 4;
+  if (e == cudaSuccess) e = cudaMalloc(&h->ws, rows * (c->head_dim + 2) * 4 + h->count_bytes);
   if (e != cudaSuccess) {
     h->ws = nullptr;
     return e;
   }
   h->part_o = static_cast<float*>(h->ws);
-  h->part_ml = h->part_o + slots * c->head_dim;
-  h->count = reinterpret_cast<unsigned*>(h->part_ml + slots * 2);
+  h->part_ml = h->part_o + rows * c->head_dim;
+  h->count = reinterpret_cast<unsigned*>(h->part_ml + rows * 2);
   // (on the handle's stream, so that it is ordered before the first call whatever stream that is)
   return cudaMemsetAsync(h->count, 0, h->count_bytes, h->stream);
 }
@@ -317,6 +318,7 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.count = h->count;
+  a.n_places = h->n_places;
   a.err = h->err_host_dev;
   // one CTA per least run of the tiles that there can be at most, at most as many as the SMs hold at once
   const int64_t seen = c.window && c.window < c.max_pages * c.page_size ? c.window + h->attend.tile : (int64_t)c.max_pages * c.page_size;
@@ -354,6 +356,7 @@ cvr_status cvr_kv_sync(cvr_kv* h) {
   if (ew & kKvErrLens) return kv_fail(h, CVR_E_INPUT, "a length, new length, held count or list head is out of range");
   if (ew & kKvErrPages) return kv_fail(h, CVR_E_PAGES, "the free list ran out of pages");
   if (ew & kKvErrSlots) return kv_fail(h, CVR_E_INPUT, "more new tokens than the slot map holds");
+  if (ew & kKvErrSize) return kv_fail(h, CVR_E_SHAPE, "the histories of one call are too long together");
   if (ew & kKvErrPage) return kv_fail(h, CVR_E_ID_RANGE, "a page id is outside the pool");
   if (ew & kKvErrSlot) return kv_fail(h, CVR_E_ID_RANGE, "a slot is outside the pool (its token was skipped)");
   h->last_error[0] = 0;

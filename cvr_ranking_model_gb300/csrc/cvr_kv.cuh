@@ -14,6 +14,7 @@ constexpr int kKvErrLens = 2;    // a length, new length, held count or list hea
 constexpr int kKvErrSlot = 4;    // a slot outside the pool
 constexpr int kKvErrSlots = 16;  // more new tokens than the slot map holds
 constexpr int kKvErrPages = 32;  // the free list ran out
+constexpr int kKvErrSize = 64;   // more tiles than one call can take
 static_assert(kErrTimeout == 8, "the bounded waits report into the same word");
 
 struct KvTablesArgs {
@@ -46,10 +47,11 @@ struct KvAttendArgs {
   int64_t q_stride, out_stride, n_pages;
   float scale;
   int n_req, q_heads, kv_heads, group, page_log2, max_pages, window;
-  int min_tiles;    // least tiles of a CTA's run
-  // workspace: what a CTA leaves of the (request, head) that its run ends in [1] or began before it [0]
-  float *part_o, *part_ml;  // [CTA][2][group][head_dim], [CTA][2][group][m, l]
-  unsigned* count;          // [max_req][kv_heads] parts written (zero between calls)
+  int min_tiles;    // least tiles of a CTA's even share
+  // workspace: what a CTA leaves of a (request, head) that it shares with others
+  float *part_o, *part_ml;  // [n_places][group][head_dim], [n_places][group][m, l]
+  unsigned* count;          // [2][n_places] parts of a group, groups of a (request, head) written (zero between calls)
+  int n_places;
   int* err;
 };
 

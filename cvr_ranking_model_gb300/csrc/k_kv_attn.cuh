@@ -34,6 +34,13 @@ constexpr int kThreads = (kConsumers + 1) * 32;     // and the producer
 static_assert(kThreads == kKvAttendThreads, "the launch's block");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+struct __align__(16) Tile {
+  int r, h, k0, flags;       // request, kv head, first token of the tile; kFirst .., the part's number << kPartShift
+  int lo, len, i0, n_parts;  // tokens seen: [lo, len); the (request, head) has n_parts parts, of CTAs i0, i0 + 1, ..
+};
+constexpr int kLast = 1, kPartShift = 1;  // last tile of a part
+constexpr int kGroup = 16;                // parts that are joined at once
+
 // MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64
 template <bool I8, int D, int MODE>
 struct Shape {
@@ -42,33 +49,31 @@ struct Shape {
   static constexpr int kRow = D * (I8 ? 1 : 2);                 // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int TK = 16384 / kRow < 256 ? 16384 / kRow : 256;  // tokens per tile
+  static constexpr int kCtasPerSm = MT > 1 ? 1 : D < 128 ? 4 : 2;
+  static constexpr int kUnitMost = kCtasPerSm <= 2 ? 16384 : 8192;
+  static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
-  static constexpr int kCtasPerSm = MT == 1 ? 2 : 1;
-  // ring units: what fits two CTAs (one for more than 16 query rows) into an SM beside the query and joining areas
-  static constexpr int kRing = (MT == 1 ? 5 : 9) * 16384 / kUnit;
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
-  static constexpr int kQBytes = MT * 16 * kQRow;
+  static constexpr int kQBytes = (MODE == 0 ? 8 : MT * 16) * kQRow;
   static constexpr int kORow = D + (I8 ? 16 : 8);               // padded fp32 rows of the joining area
   static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
-  static constexpr int NB = TK / 16 / KP, NBS = NB < 4 ? NB : 4;
+  static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
+  // ring units: what is left of this CTA's share of the SM's 228 KB (1 KB of it reserved, 1 KB for the ring's alignment)
+  static constexpr int kShare = kCtasPerSm == 1 ? 232448 : 233472 / kCtasPerSm - 1024;
+  static constexpr int kFixed = 2 * kQBytes + kConsumers * 8 * kORow * 4 + 2 * kConsumers * 16 * 4 + 5 * 8 + 64 + 1024;
+  static constexpr int kRing = (kShare - kFixed) / (kUnit + kScaleBytes + (int)sizeof(Tile) + 16);
   // shared memory
   static constexpr int oScale = kRing * kUnit;
   static constexpr int oQ = oScale + kRing * kScaleBytes;
   static constexpr int oO = oQ + 2 * kQBytes;
   static constexpr int oStat = oO + kConsumers * 8 * kORow * 4;
   static constexpr int oTile = oStat + 2 * kConsumers * 16 * 4;
-  static constexpr int oBar = oTile + kRing * 32;
-  static constexpr int kSmem = oBar + (2 * kRing + 5) * 8 + 64 + 1024;  // (1024: the ring's alignment)
-  static_assert(kSmem <= (kCtasPerSm == 2 ? 115712 : 232448), "two CTAs share an SM's 228 KB");
+  static constexpr int oBar = oTile + kRing * (int)sizeof(Tile);
+  static constexpr int kSmem = oBar + (2 * kRing + 5) * 8 + 64 + 1024;
+  static_assert(kSmem <= kShare && kRing >= 4, "K and V units of two tiles at least");
 };
 
-struct __align__(16) Tile {
-  int r, h, k0, flags;       // request, kv head, first token of the tile
-  int lo, len, i0, n_parts;  // tokens seen: [lo, len); CTAs i0 .. i0 + n_parts - 1 share this (request, head)
-};
-constexpr int kFirst = 1, kLast = 2, kStarts = 4;  // first / last tile of this CTA's part; the part holds the start
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -146,6 +151,16 @@ __device__ __forceinline__ int tiles_of(const KvAttendArgs& a, int len) {
   return (len + TK - 1) / TK - seen_from(a, len) / TK;
 }
 
+// where part p of a (request, head) that begins in CTA i0's run lies in the workspace: a CTA has two places, [1] for what
+// begins in its run and goes on, [0] for what began before
+__device__ __forceinline__ int part_place(int i0, int p) { return (i0 + p) * 2 + (p == 0); }
+
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* p) {
+  unsigned v;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 template <typename T, bool I8, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     attend_kernel(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap tm_k,
@@ -162,9 +177,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   uint64_t* const meet = q_empty + 2;      // the consumer warps' barrier
   volatile int* const abort_flag = reinterpret_cast<int*>(meet + 1);
   int* const s_last = const_cast<int*>(abort_flag) + 1;
-  int64_t* const s_start = reinterpret_cast<int64_t*>(s_last + 1);  // (8-byte aligned: two ints after `meet`)
-  int* const s_req = reinterpret_cast<int*>(s_start + 1);
-  int64_t* const s_sum = reinterpret_cast<int64_t*>(sm + S::oStat);     // scan scratch, before the first part ends
+  uint32_t* const s_sum = reinterpret_cast<uint32_t*>(sm + S::oStat);  // scan scratch, before the first part ends
+  int* const s_start = s_last + 1;  // request of the CTA's first tile, and the tiles per head before it
   Tile* const tiles = reinterpret_cast<Tile*>(sm + S::oTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.kv_heads, G = a.group;
@@ -188,44 +202,47 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   pdl_trigger();
   pdl_wait();
 
-  // ---- this CTA's run of the line of tiles ----
-  const int chunk = (a.n_req + kThreads - 1) / kThreads;
-  const int c0 = min(tid * chunk, a.n_req), c1 = min(c0 + chunk, a.n_req);
-  int64_t mine = 0;
+  // ---- this CTA's run of the line of tiles: every thread sums a few requests' tiles, saturating ----
+  const int few = (a.n_req + kThreads - 1) / kThreads;
+  const int r0 = min(tid * few, a.n_req), r1 = min(r0 + few, a.n_req);
+  auto add = [](uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); };
+  uint32_t mine = 0;
   bool bad = false;
-  for (int r = c0; r < c1; ++r) {
+  for (int r = r0; r < r1; ++r) {
     const int raw = __ldg(a.lens + r), len = clamped_len(a, raw);
     bad |= raw != len;
-    mine += tiles_of<TK>(a, len);
+    mine = add(mine, tiles_of<TK>(a, len));
   }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kKvErrLens);
-  int64_t incl = mine;
+  uint32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += u;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl = add(incl, u);
   }
   if (lane == 31) s_sum[warp] = incl;
   cta_sync();
-  int64_t before = incl - mine, total = 0;
+  uint32_t before = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w <= kConsumers; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
+    if (w < warp) before = add(before, s_sum[w]);
+    all = add(all, s_sum[w]);
   }
-  total *= H;
-  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_tiles);
-  const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
-  const int64_t n_tiles = begin < end ? end - begin : 0;
-  if (n_tiles > 0 && begin >= before * H && begin < (before + mine) * H) {
-    for (int r = c0; r < c1; ++r) {
-      const int t = tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r)));
-      if (begin < (before + t) * H) {
-        *s_start = before;
-        *s_req = r;
+  const bool fits = (uint64_t)all * H <= 0x7fffffffu;
+  if (!fits && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kKvErrSize);
+  const int total = fits ? (int)all * H : 0;
+  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, a.min_tiles);
+  const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min((int64_t)begin + per, (int64_t)total);
+  const int n_tiles = end - begin;
+  if (n_tiles > 0 && begin >= (int)before * H && begin < (int)(before + mine) * H) {
+    for (int r = r0; r < r1; ++r) {
+      const int n = tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r)));
+      if (begin < ((int)before + n) * H) {
+        s_start[0] = r;
+        s_start[1] = (int)before;
         break;
       }
-      before += t;
+      before += n;
     }
   }
   cta_sync();
@@ -236,105 +253,112 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     const int br = 1 << log2_br, n_box_max = TK >> log2_br;
     int slot = 0, filled = 0;  // the ring's next unit, and the units filled so far (at most RING)
     uint32_t phase = 0;        // parity of the ring's round
-    bool ok = true;
-    int last_parts = 0;
+    int parts = 0;             // parts begun
     if (n_tiles > 0) {
-      int r = *s_req, wb = r;  // lens of the 32 requests from wb on, one per lane
-      int64_t P = *s_start;    // tiles of one head before request r
-      int wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
-      int len = __shfl_sync(0xffffffffu, wl, 0), lo = seen_from(a, len), t0 = lo / TK, n_t = tiles_of<TK>(a, len);
-      int h = (int)((begin - P * H) / n_t), t = (int)((begin - P * H) % n_t);
-      int parts = 0;  // parts begun
-      int i0 = 0, n_parts = 1;
-      bool starts = true;
-      Tile cur, nxt;
-      int cur_page = 0, nxt_page = 0, cur_need = 0, nxt_need = 0;
-      // the tile (r, h, t), number i of this CTA: its description, and in lane b the page of its box b
-      auto prepare = [&](int64_t i) {
-        if (i > 0) {
-          if (++t == n_t) {
-            t = 0;
-            if (++h == H) {
-              h = 0;
-              P += n_t;
-              int from = r + 1;
-              unsigned some;
-              while (true) {  // the next request with a tile
-                if (from >= wb + 32) {
-                  wb = from;
-                  wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
-                }
-                some = __ballot_sync(0xffffffffu, wl > 0 && wb + lane >= from);
-                if (some || wb + 32 >= a.n_req) break;
-                from = wb + 32;
-              }
-              const int src = some ? __ffs(some) - 1 : 0;
-              r = min(wb + src, a.n_req - 1);
-              len = __shfl_sync(0xffffffffu, wl, src);
-              lo = seen_from(a, len);
-              t0 = lo / TK;
-              n_t = max(1, tiles_of<TK>(a, len));
-            }
-          }
-        }
-        const bool first = i == 0 || t == 0;
-        if (first) {
-          const int64_t fb = P * H + (int64_t)h * n_t;
-          starts = fb >= begin;
-          i0 = (int)(fb / per);
-          n_parts = (int)((fb + n_t - 1) / per) - i0 + 1;
-        }
-        nxt.r = r;
-        nxt.h = h;
-        nxt.k0 = (t0 + t) * TK;
-        nxt.flags = (first ? kFirst : 0) | (i == n_tiles - 1 || t == n_t - 1 ? kLast : 0) | (starts ? kStarts : 0);
-        nxt.lo = lo;
-        nxt.len = len;
-        nxt.i0 = i0;
-        nxt.n_parts = n_parts;
-        const int at = nxt.k0 + (lane << log2_br);
-        nxt_need = lane < n_box_max && at < len && at + br > lo;
-        nxt_page = nxt_need ? __ldg(a.table + (int64_t)r * a.max_pages + (at >> a.page_log2)) : 0;
+      // Page ids come 32 entries of a table row at a time, one per lane, and ahead of their use: the row's next 32, and the
+      // first 32 of the next request. A tile's entries never straddle two batches (both begin at a multiple of its count).
+      auto entries = [&](int row, int e) { return e + lane < a.max_pages ? __ldg(a.table + (int64_t)row * a.max_pages + e + lane) : 0; };
+      int wb = s_start[0], wl = 0;  // lengths of the 32 requests from wb on, one per lane
+      auto window = [&](int from) {
+        wb = from;
+        wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
       };
-      prepare(0);
-      for (int64_t i = 0; i < n_tiles && ok; ++i) {
-        cur = nxt;
-        cur_page = nxt_page;
-        cur_need = nxt_need;
-        if (i + 1 < n_tiles) prepare(i + 1);  // (its page ids arrive while this tile waits for the ring)
-        if (cur_need && (cur_page < 0 || cur_page >= a.n_pages)) {
-          atomicOr(a.err, kKvErrPage);
-          cur_page = 0;
+      auto first_entry = [&](int length) { return (seen_from(a, length) / TK * TK) >> a.page_log2; };
+      // the next request with a tile from `from` on (n_req: none), its length and first page ids
+      int n_r = 0, n_len = 0, n_ids = 0;
+      auto look_ahead = [&](int from) {
+        unsigned some;
+        while (true) {
+          if (from >= wb + 32) window(from);
+          some = __ballot_sync(0xffffffffu, wl > 0 && wb + lane >= from);
+          if (some || wb + 32 >= a.n_req) break;
+          from = wb + 32;
         }
-        const int n_box = __popc(__ballot_sync(0xffffffffu, cur_need != 0));
-        const int row = (cur.k0 + (lane << log2_br)) & ((1 << a.page_log2) - 1);
-        const int64_t scale_at = (((int64_t)cur_page * H + cur.h) << a.page_log2) + row;
-        if (cur.flags & kFirst) {
+        n_r = some ? wb + __ffs(some) - 1 : a.n_req;
+        n_len = some ? __shfl_sync(0xffffffffu, wl, __ffs(some) - 1) : 0;
+        n_ids = some ? entries(n_r, first_entry(n_len)) : 0;
+      };
+      int P = s_start[1], r = 0, h = 0, t = 0, n_t = 1, t0 = 0, len = 0, lo = 0;  // P: tiles per head before request r
+      int e0 = 0, ids = 0, more_ids = 0;  // entries e0 + lane and e0 + 32 + lane of the request's table row
+      auto enter = [&]() {  // the request that was looked ahead to
+        r = n_r;
+        len = n_len;
+        lo = seen_from(a, len);
+        t0 = lo / TK;
+        n_t = max(1, tiles_of<TK>(a, len));
+      };
+      auto rewind = [&]() {  // to the request's first pages
+        e0 = first_entry(len);
+        more_ids = entries(r, e0 + 32);
+      };
+      window(wb);
+      look_ahead(wb);
+      enter();
+      h = (begin - P * H) / n_t;
+      t = (begin - P * H) - h * n_t;
+      e0 = ((t0 + t) * TK) >> a.page_log2;  // (the run may begin anywhere in its request)
+      ids = entries(r, e0);
+      more_ids = entries(r, e0 + 32);
+      bool ahead = false;  // looked ahead from this request
+      int i0 = 0, n_parts = 1;
+      bool ok = true;
+      for (int at = begin; at < end; ++at) {
+        const bool first = at == begin || t == 0;
+        const int k0 = (t0 + t) * TK;
+        if (first) {
+          const int fb = P * H + h * n_t;
+          i0 = fb / per;
+          n_parts = (fb + n_t - 1) / per - i0 + 1;
           // the part's query rows
           const int b = parts & 1;
           ok = mbar_wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
           __syncwarp();
-          const T* q = static_cast<const T*>(a.q) + cur.r * a.q_stride + (int64_t)cur.h * G * D;
+          const T* q = static_cast<const T*>(a.q) + r * a.q_stride + (int64_t)h * G * D;
           for (int g = lane; g < G; g += 32) bulk_load(smem_u32(sm + S::oQ + b * S::kQBytes + g * S::kQRow), q + g * D, D * 2, q_full + b);
           ++parts;
         }
+        if ((k0 >> a.page_log2) >= e0 + 32) {
+          ids = more_ids;
+          e0 += 32;
+          more_ids = entries(r, e0 + 32);
+        }
+        // in lane b: box b of the tile, wanted if any of its tokens is seen
+        const int from = k0 + (lane << log2_br), row = from & ((1 << a.page_log2) - 1);
+        const bool need = lane < n_box_max && from < len && from + br > lo;
+        int page = __shfl_sync(0xffffffffu, ids, ((from >> a.page_log2) - e0) & 31);
+        if (need && (page < 0 || page >= a.n_pages)) {
+          atomicOr(a.err, kKvErrPage);
+          page = 0;
+        }
+        const int n_box = __popc(__ballot_sync(0xffffffffu, need));
 #pragma unroll 1
         for (int w = 0; w < (two ? 2 : 1); ++w) {
           ok = mbar_wait_warp(empty + slot, phase ^ 1, abort_flag, a.err);
           if (!ok) break;
           if (lane == 0) {
-            if (w == 0) tiles[slot] = cur;
+            if (w == 0) {
+              Tile tl;
+              tl.r = r;
+              tl.h = h;
+              tl.k0 = k0;
+              tl.flags = (at + 1 == end || t + 1 == n_t ? kLast : 0) | (((int)blockIdx.x - i0) << kPartShift);
+              tl.lo = lo;
+              tl.len = len;
+              tl.i0 = i0;
+              tl.n_parts = n_parts;
+              tiles[slot] = tl;
+            }
             mbar_expect_tx(full + slot, (uint32_t)(n_box * br) * (S::kRow + (I8 ? 4 : 0)));
           }
           __syncwarp();
-          if (cur_need) {
+          if (need) {
             uint8_t* dst = sm + slot * S::kUnit + (lane << log2_br) * S::kRow;
-            tma_load_5d(dst, w ? &tm_v : &tm_k, full + slot, 0, row, 0, cur.h, cur_page);
+            tma_load_5d(dst, w ? &tm_v : &tm_k, full + slot, 0, row, 0, h, page);
             if (I8)
               bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
-                        (w ? a.v_scale : a.k_scale) + scale_at, 4 << log2_br, full + slot);
+                        (w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row), 4 << log2_br, full + slot);
           }
           filled = min(filled + 1, RING);
           if (++slot == RING) {
@@ -342,8 +366,26 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             phase ^= 1;
           }
         }
+        if (!ok) break;
+        // on to the next tile: of the head, of the next head, of the next request
+        if (++t == n_t && at + 1 < end) {
+          t = 0;
+          if (++h < H) {
+            ids = entries(r, first_entry(len));
+          } else {
+            h = 0;
+            P += n_t;
+            if (!ahead) look_ahead(r + 1);
+            ids = n_ids;
+            enter();
+            ahead = false;
+          }
+          rewind();
+        } else if (!ahead && h + 1 == H) {
+          look_ahead(r + 1);
+          ahead = true;
+        }
       }
-      last_parts = parts;
     }
     // requests that see nothing, shared out over the grid
     for (int rb = blockIdx.x * 32; rb < a.n_req; rb += gridDim.x * 32) {
@@ -366,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       }
       mbar_drain(full + slot, phase);
     }
-    for (int p = max(0, last_parts - 2); p < last_parts; ++p) mbar_drain(q_full + (p & 1), (p >> 1) & 1);
+    for (int p = max(0, parts - 2); p < parts; ++p) mbar_drain(q_full + (p & 1), (p >> 1) & 1);
     return;
   }
 
@@ -375,9 +417,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const int mt = warp % MT, kp = warp / MT;  // row tile, share of the tokens
   const int log2_br = min(a.page_log2, 31 - __clz(TK));
   const float sl2 = a.scale * kLog2e;
-  // p is kept times 2^12 in fp16 (it is at most 1), so that small weights keep their bits
+  // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8,
+  // with 8-bit rows times 2^8 / vmax.
+  constexpr float kGrow = 6.f, kWeight = 256.f;
   constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
-  constexpr float kShift = kF16 ? 12.f : 0.f;
+  constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
   uint32_t meets = 0;
   bool ok = true;
@@ -387,312 +431,315 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     ok = mbar_wait_warp(meet, meets & 1, abort_flag, a.err) && ok;
     ++meets;
   };
-  // byte offset of a row's line within a unit, for the row of token `key` of the tile (its second half follows at
-  // half_step), and the swizzle of the 8 rows that a matrix is loaded from
-  auto row_at = [&](int key) -> uint32_t {
+  // Addresses of ldmatrix rows in a unit. A unit is boxes of [half][row][line]; block_at is the offset of a 16-token
+  // block's first row, a lane adds its row and its 16-byte piece, swizzled by the row (row_off, piece below): matrices
+  // 0 .. 3 are (rows 0-7, 8-15) x (two pieces), in the order that the K or the V fragments want. 32 bytes further along the
+  // rows is an exclusive or (lines are 128-byte aligned, or the bits above the swizzle's belong to the row).
+  const uint32_t half_step = (uint32_t)S::kLine << log2_br;
+  const int l7 = lane & 7, up8 = (lane >> 3) & 1, up16 = lane >> 4;
+  const uint32_t swz = (S::kLine == 128 ? l7 : S::kLine == 64 ? (l7 >> 1) & 3 : (l7 >> 2) & 1) << 4;
+  auto row_off = [&](int upper) -> uint32_t {
+    return l7 * S::kLine + upper * (log2_br >= 4 ? 8 * S::kLine : S::kHalves * 8 * S::kLine);
+  };
+  const uint32_t lane_k = row_off(up16) + ((up8 << 4) ^ swz), lane_v = row_off(up8) + ((up16 << 4) ^ swz);
+  auto block_at = [&](int key) -> uint32_t {
     return (uint32_t)(((key >> log2_br) * S::kHalves << log2_br) + (key & ((1 << log2_br) - 1))) * S::kLine;
   };
-  const uint32_t half_step = (uint32_t)S::kLine << log2_br;
-  const int l7 = lane & 7;
-  const uint32_t swz = (S::kLine == 128 ? l7 : S::kLine == 64 ? (l7 >> 1) & 3 : (l7 >> 2) & 1) << 4;
-  auto chunk_at = [&](int c) -> uint32_t {  // the row's 16-byte piece c
-    return (c >> 3) * half_step + ((uint32_t)((c & 7) << 4) ^ swz);
+  auto piece = [&](uint32_t addr, int k) -> uint32_t {
+    return (addr ^ (uint32_t)(k * 32 % S::kLine)) + (k * 32 / S::kLine) * half_step;
   };
 
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-  float cA = sl2, cB = sl2;       // logit factors of rows A (gid) and B (gid + 8)
-  float vmax = 0x1p-100f;         // 8 bits: the largest row scale of V so far (floored)
-  int ks = 0, parts = 0;          // the ring's next unit, and parts begun
+  int ks = 0, parts = 0;  // the ring's next unit, and parts begun
   uint32_t phase = 0;
   float* const s_o = reinterpret_cast<float*>(sm + S::oO);
   float* const s_m = reinterpret_cast<float*>(sm + S::oStat);
   float* const s_l = s_m + kConsumers * 16;
 
-  for (int64_t i = 0; i < n_tiles; ++i) {
-    ok = mbar_wait_warp(full + ks, phase, abort_flag, a.err);
+  for (int i = 0; i < n_tiles;) {
+    // ---- a part: the tiles of one (request, head) in this CTA's run ----
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+    float cA = sl2, cB = sl2;  // logit factors of rows A (gid) and B (gid + 8)
+    float vmax = 0x1p-100f, w_mul = kWeight * 0x1p100f;  // 8 bits: the largest row scale of V so far (floored)
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    Tile tl;
+    const int b = parts & 1;
+    ok = mbar_wait_warp(q_full + b, (parts >> 1) & 1, abort_flag, a.err);
     if (!ok) return;
-    const Tile tl = tiles[ks];
-    const uint32_t k_unit = smem_u32(sm + ks * S::kUnit);
-    if (tl.flags & kFirst) {
-      const int b = parts & 1;
-      ok = mbar_wait_warp(q_full + b, (parts >> 1) & 1, abort_flag, a.err);
-      if (!ok) return;
-      const uint8_t* qs = sm + S::oQ + b * S::kQBytes + mt * 16 * S::kQRow;
-      const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
-      if (!I8) {
+    const uint8_t* qs = sm + S::oQ + b * S::kQBytes + mt * 16 * S::kQRow;
+    const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
+    if (!I8) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
-          qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) : 0u;
-          qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) : 0u;
-          qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) : 0u;
-          qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) : 0u;
-        }
-      } else {
-        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
-        float mulA = 1.f, mulB = 1.f;
-        uint2 xa[D / 16], xb[D / 16];
+      for (int k = 0; k < D / 16; ++k) {
+        const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
+        qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) : 0u;
+        qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) : 0u;
+        qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) : 0u;
+        qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) : 0u;
+      }
+    } else {
+      // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
+      float mulA = 1.f, mulB = 1.f;
+      uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
-          xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
-          xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
-        }
-        if (std::is_same<T, __nv_bfloat16>::value) {
-          // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
-          // of it, 2^-25 of it below
-          float bigA = 0.f, bigB = 0.f;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
-            bigA = fmaxf(fmaxf(bigA, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
-            bigB = fmaxf(fmaxf(bigB, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(z.x), fabsf(z.y)));
-          }
-#pragma unroll
-          for (int d = 1; d < 4; d <<= 1) {
-            bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
-            bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
-          }
-          const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
-          const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
-          mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
-          mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
-          cA = fitA ? sl2 * __uint_as_float(eA << 23) : sl2;
-          cB = fitB ? sl2 * __uint_as_float(eB << 23) : sl2;
-        }
+      for (int k = 0; k < D / 16; ++k) {
+        const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
+        xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
+        xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
+      }
+      if (std::is_same<T, __nv_bfloat16>::value) {
+        // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
+        // of it, 2^-25 of it below
+        float bigA = 0.f, bigB = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
-          qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
-          qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
-          qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
-          qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
+          bigA = fmaxf(fmaxf(bigA, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+          bigB = fmaxf(fmaxf(bigB, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(z.x), fabsf(z.y)));
         }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
+          bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
+        }
+        const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
+        const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
+        mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
+        mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
+        cA = fitA ? sl2 * __uint_as_float(eA << 23) : sl2;
+        cB = fitB ? sl2 * __uint_as_float(eB << 23) : sl2;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty + b);
-      ++parts;
-      mA = mB = -INFINITY;
-      lA = lB = 0.f;
-      vmax = 0x1p-100f;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+      for (int k = 0; k < D / 16; ++k) {
+        const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
+        qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
+        qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
+        qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
+        qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
+      }
     }
-    const int vs_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
-    const uint32_t vs_phase = vs_slot < ks ? phase ^ 1 : phase;
-    const uint32_t v_unit = smem_u32(sm + vs_slot * S::kUnit);
-    const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + ks * S::kScaleBytes);
-    const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + vs_slot * S::kScaleBytes);
-    // tokens of the tile that are seen, and whether that is not all of them
-    const int j0 = max(tl.lo - tl.k0, 0), j1 = min(tl.len - tl.k0, TK);
-    const bool partial = j0 > 0 || j1 < TK;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty + b);
+    ++parts;
+    do {
+      ok = mbar_wait_warp(full + ks, phase, abort_flag, a.err);
+      if (!ok) return;
+      tl = tiles[ks];
+      ++i;
+      const uint32_t k_unit = smem_u32(sm + ks * S::kUnit);
+      const int vs_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
+      const uint32_t vs_phase = vs_slot < ks ? phase ^ 1 : phase;
+      const uint32_t v_unit = smem_u32(sm + vs_slot * S::kUnit);
+      const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + ks * S::kScaleBytes);
+      const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + vs_slot * S::kScaleBytes);
+      // tokens of the tile that are seen, and whether that is not all of them
+      const int j0 = max(tl.lo - tl.k0, 0), j1 = min(tl.len - tl.k0, TK);
+      const bool partial = j0 > 0 || j1 < TK;
 
 #pragma unroll 1
-    for (int sub = 0; sub < NB / NBS; ++sub) {
-      float s[NBS][2][4];
+      for (int sub = 0; sub < NB / NBS; ++sub) {
+        // S = Q K^T: two chains of products per 8 tokens, so that their latencies overlap
+        float s[NBS][2][4];
 #pragma unroll
-      for (int b = 0; b < NBS; ++b) {
-        const int key = ((sub * NBS + b) * KP + kp) * 16;
+        for (int b = 0; b < NBS; ++b) {
+          const int key = ((sub * NBS + b) * KP + kp) * 16;
+          float odd[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
-        if (key + 16 > j0 && key < j1) {
-          // matrices: tokens 0-7 and 8-15 of the block, two 16-byte pieces each
-          const uint32_t base = k_unit + row_at(key + (lane >> 4) * 8 + l7);
-          if (!I8) {
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t f[4];
-              ldsm4(f, base + chunk_at(2 * k + ((lane >> 3) & 1)));
-              mma16816<M>(s[b][0], qf[k], f[0], f[1]);
-              mma16816<M>(s[b][1], qf[k], f[2], f[3]);
-            }
-          } else {
+            for (int e = 0; e < 4; ++e) s[b][n][e] = odd[n][e] = 0.f;
+          if (key + 16 > j0 && key < j1) {
+            const uint32_t base = k_unit + block_at(key) + lane_k;
+            if (!I8) {
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t f[4];
-              ldsm4(f, base + chunk_at(2 * k + ((lane >> 3) & 1)));
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t f[4];
+                ldsm4(f, piece(base, k));
+                mma16816<M>(k & 1 ? odd[0] : s[b][0], qf[k], f[0], f[1]);
+                mma16816<M>(k & 1 ? odd[1] : s[b][1], qf[k], f[2], f[3]);
+              }
+            } else {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                mma16816<M>(s[b][0], qf[2 * k + e], i8_pair<0x4140>(f[e]), i8_pair<0x4342>(f[e]));
-                mma16816<M>(s[b][1], qf[2 * k + e], i8_pair<0x4140>(f[2 + e]), i8_pair<0x4342>(f[2 + e]));
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t f[4];
+                ldsm4(f, piece(base, k));
+                mma16816<M>(s[b][0], qf[2 * k], i8_pair<0x4140>(f[0]), i8_pair<0x4342>(f[0]));
+                mma16816<M>(s[b][1], qf[2 * k], i8_pair<0x4140>(f[2]), i8_pair<0x4342>(f[2]));
+                mma16816<M>(odd[0], qf[2 * k + 1], i8_pair<0x4140>(f[1]), i8_pair<0x4342>(f[1]));
+                mma16816<M>(odd[1], qf[2 * k + 1], i8_pair<0x4140>(f[3]), i8_pair<0x4342>(f[3]));
               }
             }
           }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < (R8 ? 2 : 4); ++e) s[b][n][e] += odd[n][e];
         }
-      }
-      // logits in units of ln 2; tokens that are not seen are out
-      float nA = mA, nB = mB;
-#pragma unroll
-      for (int b = 0; b < NBS; ++b)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
-          float k0 = 1.f, k1 = 1.f;
-          if (I8) {
-            const float2 sc = *reinterpret_cast<const float2*>(k_sc + key);
-            k0 = sc.x;
-            k1 = sc.y;
-          }
-          s[b][n][0] *= I8 ? cA * k0 : cA;
-          s[b][n][1] *= I8 ? cA * k1 : cA;
-          if (!R8) {
-            s[b][n][2] *= I8 ? cB * k0 : cB;
-            s[b][n][3] *= I8 ? cB * k1 : cB;
-          }
-          if (partial) {
-            if (key < j0 || key >= j1) s[b][n][0] = s[b][n][2] = -INFINITY;
-            if (key + 1 < j0 || key + 1 >= j1) s[b][n][1] = s[b][n][3] = -INFINITY;
-          }
-          nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
-          if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
+        if (sub == 0 && two) {
+          ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
+          if (!ok) return;
         }
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
-        if (!R8) nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
-      }
-      float w_mul = 1.f;  // 8 bits: weights enter the second product times 2^14 / vmax
-      float grow = 1.f;
-      if (I8) {
-        float big = vmax;
+        // logits in units of ln 2; tokens that are not seen are out
+        float nA = -INFINITY, nB = -INFINITY, big = 0.f;
+        float2 sv[NBS][2];  // 8 bits: V's row scales
 #pragma unroll
         for (int b = 0; b < NBS; ++b)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
-            if (sub == 0 && b == 0 && n == 0 && two) {
-              ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
-              if (!ok) return;
+            float2 sk = make_float2(1.f, 1.f);
+            if (I8) {
+              sk = *reinterpret_cast<const float2*>(k_sc + key);
+              sv[b][n] = *reinterpret_cast<const float2*>(v_sc + key);
             }
-            const float2 sc = *reinterpret_cast<const float2*>(v_sc + key);
-            if (key >= j0 && key < j1) big = fmaxf(big, sc.x);
-            if (key + 1 >= j0 && key + 1 < j1) big = fmaxf(big, sc.y);
-          }
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-        grow = vmax / big;
-        vmax = big;
-        w_mul = 0x1p14f / big;
-      }
-      // (a maximum of -infinity is left out of the exponent: nothing was seen, or every logit is -infinity)
-      const float baseA = nA == -INFINITY ? 0.f : nA, baseB = nB == -INFINITY ? 0.f : nB;
-      if (__any_sync(0xffffffffu, nA > mA || (!R8 && nB > mB) || grow != 1.f)) {
-        const float fA = ex2(mA - baseA), fB = R8 ? fA : ex2(mB - baseB);
-        lA *= fA;
-        if (!R8) lB *= fB;
-        const float gA = fA * grow, gB = fB * grow;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[j][0] *= gA;
-          o[j][1] *= gA;
-          o[j][2] *= gB;
-          o[j][3] *= gB;
-        }
-        mA = nA;
-        mB = nB;
-      }
-      if (!I8 && sub == 0 && two) {
-        ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
-        if (!ok) return;
-      }
-      const float subA = baseA - kShift, subB = baseB - kShift;
-#pragma unroll
-      for (int b = 0; b < NBS; ++b) {
-        const int key0 = ((sub * NBS + b) * KP + kp) * 16;
-        if (!(key0 + 16 > j0 && key0 < j1)) continue;
-        uint32_t hi[4], lw[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float pA0 = ex2(s[b][n][0] - subA), pA1 = ex2(s[b][n][1] - subA), pB0 = 0.f, pB1 = 0.f;
-          lA += pA0 + pA1;
-          if (!R8) {
-            pB0 = ex2(s[b][n][2] - subB);
-            pB1 = ex2(s[b][n][3] - subB);
-            lB += pB0 + pB1;
-          }
-          if (I8) {
-            const int key = key0 + n * 8 + 2 * tig;
-            const float2 sc = *reinterpret_cast<const float2*>(v_sc + key);
-            const float w0 = key >= j0 && key < j1 ? sc.x * w_mul : 0.f;
-            const float w1 = key + 1 >= j0 && key + 1 < j1 ? sc.y * w_mul : 0.f;
-            pA0 *= w0;
-            pA1 *= w1;
-            pB0 *= w0;
-            pB1 *= w1;
-          }
-          const uint32_t hA = pack2<M>(pA0, pA1);
-          const float2 fA = unpack2<M>(hA);
-          const uint32_t dA = pack2<M>(pA0 - fA.x, pA1 - fA.y);
-          hi[2 * n] = hA;
-          if (R8) {
-            hi[2 * n + 1] = dA;
-          } else {
-            const uint32_t hB = pack2<M>(pB0, pB1);
-            const float2 fB = unpack2<M>(hB);
-            hi[2 * n + 1] = hB;
-            lw[2 * n] = dA;
-            lw[2 * n + 1] = pack2<M>(pB0 - fB.x, pB1 - fB.y);
-          }
-        }
-        // rows of V that are not seen may hold anything: their bits are cleared (0 times an infinity is no number)
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (!I8 && partial) {
-          const int key = key0 + 2 * tig;
-          keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
-          keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
-        }
-        const uint32_t base = v_unit + row_at(key0 + ((lane >> 3) & 1) * 8 + l7);
-        if (!I8) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t f[4];
-            ldsm4_trans(f, base + chunk_at(2 * c + (lane >> 4)));
-            if (partial) {
-              f[0] &= keep0;
-              f[1] &= keep1;
-              f[2] &= keep0;
-              f[3] &= keep1;
-            }
-            mma16816<M>(o[2 * c], hi, f[0], f[1]);
-            mma16816<M>(o[2 * c + 1], hi, f[2], f[3]);
+            s[b][n][0] *= I8 ? cA * sk.x : cA;
+            s[b][n][1] *= I8 ? cA * sk.y : cA;
             if (!R8) {
-              mma16816<M>(o[2 * c], lw, f[0], f[1]);
-              mma16816<M>(o[2 * c + 1], lw, f[2], f[3]);
+              s[b][n][2] *= I8 ? cB * sk.x : cB;
+              s[b][n][3] *= I8 ? cB * sk.y : cB;
+            }
+            if (partial) {
+              if (key < j0 || key >= j1) {
+                s[b][n][0] = s[b][n][2] = -INFINITY;
+                if (I8) sv[b][n].x = 0.f;
+              }
+              if (key + 1 < j0 || key + 1 >= j1) {
+                s[b][n][1] = s[b][n][3] = -INFINITY;
+                if (I8) sv[b][n].y = 0.f;
+              }
+            }
+            nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
+            if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
+            if (I8) big = fmaxf(big, fmaxf(fabsf(sv[b][n].x), fabsf(sv[b][n].y)));
+          }
+        // The exponents' base follows the running maximum only when a logit passes it by more than kGrow, and the weights'
+        // divisor the largest V scale when a scale passes it: most steps then need neither shuffles nor a rescaling.
+        if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || (I8 && big > vmax))) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
+            if (!R8) nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
+            if (I8) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+          }
+          nA = fmaxf(nA, mA);
+          nB = fmaxf(nB, mB);
+          const float fA = nA == mA ? 1.f : ex2(mA - nA), fB = R8 ? fA : nB == mB ? 1.f : ex2(mB - nB);
+          mA = nA;
+          mB = nB;
+          lA *= fA;
+          if (!R8) lB *= fB;
+          float gA = fA, gB = fB;
+          if (I8) {
+            big = fmaxf(big, vmax);
+            gA *= vmax / big;
+            gB *= vmax / big;
+            vmax = big;
+            w_mul = kWeight / big;
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= gA;
+            o[j][1] *= gA;
+            o[j][2] *= gB;
+            o[j][3] *= gB;
+          }
+        }
+        // (a base of -infinity is left out of the exponent: nothing was seen yet, or every logit is -infinity)
+        const float subA = (mA == -INFINITY ? 0.f : mA) - kShift, subB = (mB == -INFINITY ? 0.f : mB) - kShift;
+#pragma unroll
+        for (int b = 0; b < NBS; ++b) {
+          const int key0 = ((sub * NBS + b) * KP + kp) * 16;
+          if (!(key0 + 16 > j0 && key0 < j1)) continue;
+          uint32_t hi[4], lw[4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float pA0 = ex2(s[b][n][0] - subA), pA1 = ex2(s[b][n][1] - subA), pB0 = 0.f, pB1 = 0.f;
+            lA += pA0 + pA1;
+            if (!R8) {
+              pB0 = ex2(s[b][n][2] - subB);
+              pB1 = ex2(s[b][n][3] - subB);
+              lB += pB0 + pB1;
+            }
+            if (I8) {
+              const float w0 = sv[b][n].x * w_mul, w1 = sv[b][n].y * w_mul;
+              pA0 *= w0;
+              pA1 *= w1;
+              pB0 *= w0;
+              pB1 *= w1;
+            }
+            const uint32_t hA = pack2<M>(pA0, pA1);
+            const float2 fA = unpack2<M>(hA);
+            const uint32_t dA = pack2<M>(pA0 - fA.x, pA1 - fA.y);
+            hi[2 * n] = hA;
+            if (R8) {
+              hi[2 * n + 1] = dA;
+            } else {
+              const uint32_t hB = pack2<M>(pB0, pB1);
+              const float2 fB = unpack2<M>(hB);
+              hi[2 * n + 1] = hB;
+              lw[2 * n] = dA;
+              lw[2 * n + 1] = pack2<M>(pB0 - fB.x, pB1 - fB.y);
             }
           }
-        } else {
-          // a loaded pair of bytes is two dims of one token: the even and the odd dims of 16 form one n-tile each
+          // rows of V that are not seen may hold anything: their bits are cleared (0 times an infinity is no number)
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+          if (!I8 && partial) {
+            const int key = key0 + 2 * tig;
+            keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
+            keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
+          }
+          const uint32_t base = v_unit + block_at(key0) + lane_v;
+          if (!I8) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t f[4];
-            ldsm4_trans(f, base + chunk_at(2 * c + (lane >> 4)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t e0 = i8_pair<0x4240>(f[2 * e]), e1 = i8_pair<0x4240>(f[2 * e + 1]);
-              const uint32_t d0 = i8_pair<0x4341>(f[2 * e]), d1 = i8_pair<0x4341>(f[2 * e + 1]);
-              mma16816<M>(o[4 * c + 2 * e], hi, e0, e1);
-              mma16816<M>(o[4 * c + 2 * e + 1], hi, d0, d1);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t f[4];
+              ldsm4_trans(f, piece(base, c));
+              if (partial) {
+                f[0] &= keep0;
+                f[1] &= keep1;
+                f[2] &= keep0;
+                f[3] &= keep1;
+              }
+              mma16816<M>(o[2 * c], hi, f[0], f[1]);
+              mma16816<M>(o[2 * c + 1], hi, f[2], f[3]);
               if (!R8) {
-                mma16816<M>(o[4 * c + 2 * e], lw, e0, e1);
-                mma16816<M>(o[4 * c + 2 * e + 1], lw, d0, d1);
+                mma16816<M>(o[2 * c], lw, f[0], f[1]);
+                mma16816<M>(o[2 * c + 1], lw, f[2], f[3]);
+              }
+            }
+          } else {
+            // a loaded pair of bytes is two dims of one token: the even and the odd dims of 16 form one n-tile each
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t f[4];
+              ldsm4_trans(f, piece(base, c));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t e0 = i8_pair<0x4240>(f[2 * e]), e1 = i8_pair<0x4240>(f[2 * e + 1]);
+                const uint32_t d0 = i8_pair<0x4341>(f[2 * e]), d1 = i8_pair<0x4341>(f[2 * e + 1]);
+                mma16816<M>(o[4 * c + 2 * e], hi, e0, e1);
+                mma16816<M>(o[4 * c + 2 * e + 1], hi, d0, d1);
+                if (!R8) {
+                  mma16816<M>(o[4 * c + 2 * e], lw, e0, e1);
+                  mma16816<M>(o[4 * c + 2 * e + 1], lw, d0, d1);
+                }
               }
             }
           }
         }
       }
-    }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(empty + ks);
-      if (two) mbar_arrive(empty + vs_slot);
-    }
-    phase = vs_slot + 1 == RING ? vs_phase ^ 1 : vs_phase;
-    ks = vs_slot + 1 == RING ? 0 : vs_slot + 1;
-    if (!(tl.flags & kLast)) continue;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(empty + ks);
+        if (two) mbar_arrive(empty + vs_slot);
+      }
+      phase = vs_slot + 1 == RING ? vs_phase ^ 1 : vs_phase;
+      ks = vs_slot + 1 == RING ? 0 : vs_slot + 1;
+    } while (!(tl.flags & kLast));
 
     // ---- the part's end: the warps' (m, l, o) to shared memory, 8 rows of each tile at a time, and summed ----
 #pragma unroll
@@ -700,10 +747,21 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       lA += __shfl_xor_sync(0xffffffffu, lA, d);
       if (!R8) lB += __shfl_xor_sync(0xffffffffu, lB, d);
     }
-    const float o_mul = I8 ? vmax * 0x1p-14f : 1.f;
-    const int part_slot = (int)blockIdx.x * 2 + ((tl.flags & kStarts) ? 1 : 0);
-    constexpr int VEC = MT * D / 16 < 4 ? MT * D / 16 : 4;  // values per thread and step
-    constexpr int kPerRow = D / VEC;
+    const float o_mul = I8 ? vmax / kWeight : 1.f;
+    // values c .. c + 3 of query row g, all tokens joined: the output; or so far: to a place of the workspace
+    auto finish = [&](int g, int c, float m, float l, const float* acc) {
+      const int qh = tl.h * G + g;
+      T* dst = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + c;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc[0] / l, acc[1] / l), pack2<T>(acc[2] / l, acc[3] / l));
+      if (c == 0 && a.lse) a.lse[(int64_t)tl.r * a.q_heads + qh] = ((m == -INFINITY ? 0.f : m) - kShift) * kLn2 + logf(l);
+    };
+    auto keep = [&](int to, int g, int c, float m, float l, const float* acc) {
+      __stcg(reinterpret_cast<float4*>(a.part_o + ((int64_t)to * G + g) * D + c), make_float4(acc[0], acc[1], acc[2], acc[3]));
+      if (c == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + (int64_t)to * G + g, make_float2(m, l));
+    };
+    const int part = tl.flags >> kPartShift;
+    const int place = part_place(tl.i0, part);
+    constexpr int kPerRow = D / 4;  // 4 values per thread
 #pragma unroll
     for (int pass = 0; pass < (R8 ? 1 : 2); ++pass) {
       consumer_sync();  // (the previous pass or part has been read)
@@ -729,103 +787,98 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       consumer_sync();
       if (!ok) return;
       for (int x = tid; x < 8 * MT * kPerRow; x += kConsumers * 32) {
-        const int row8 = x / kPerRow, c = (x - row8 * kPerRow) * VEC;
+        const int row8 = x / kPerRow, c = (x - row8 * kPerRow) * 4;
         const int rt = row8 >> 3, g = rt * 16 + pass * 8 + (row8 & 7);
         if (g >= G) continue;
         float top = -INFINITY;
 #pragma unroll
         for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * 16 + (row8 & 7)]);
         const float base = top == -INFINITY ? 0.f : top;
-        float l = 0.f, acc[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+        float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
           const int w = p * MT + rt;
           const float f = ex2(s_m[w * 16 + (row8 & 7)] - base);
           l += f * s_l[w * 16 + (row8 & 7)];
-          const float* src = s_o + (w * 8 + (row8 & 7)) * S::kORow + c;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) acc[e] += f * src[e];
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + (row8 & 7)) * S::kORow + c);
+          acc[0] += f * v.x;
+          acc[1] += f * v.y;
+          acc[2] += f * v.z;
+          acc[3] += f * v.w;
         }
-        const int qh = tl.h * G + g;
-        if (tl.n_parts == 1) {
-          T* dst_o = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + c;
-          uint32_t pk[VEC / 2];
-#pragma unroll
-          for (int e = 0; e < VEC; e += 2) pk[e / 2] = pack2<T>(acc[e] / l, acc[e + 1] / l);
-          if (VEC == 4) *reinterpret_cast<uint2*>(dst_o) = make_uint2(pk[0], pk[VEC / 2 - 1]);
-          else *reinterpret_cast<uint32_t*>(dst_o) = pk[0];
-          if (c == 0 && a.lse) a.lse[(int64_t)tl.r * a.q_heads + qh] = (base - kShift) * kLn2 + logf(l);
-        } else {
-          float* dst_o = a.part_o + ((int64_t)part_slot * G + g) * D + c;
-          if (VEC == 4) __stcg(reinterpret_cast<float4*>(dst_o), make_float4(acc[0], acc[1], acc[VEC - 2], acc[VEC - 1]));
-          else __stcg(reinterpret_cast<float2*>(dst_o), make_float2(acc[0], acc[1]));
-          if (c == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + (int64_t)part_slot * G + g, make_float2(top, l));
-        }
+        if (tl.n_parts == 1) finish(g, c, top, l, acc);
+        else keep(place, g, c, top, l, acc);
       }
     }
     if (tl.n_parts == 1) continue;
 
-    // ---- the last CTA of this (request, head) to get here joins the parts ----
-    __threadfence();
-    consumer_sync();
-    if (!ok) return;
-    unsigned* count = a.count + (int64_t)tl.r * H + tl.h;
-    if (tid == 0) {
-      const bool last = atomicAdd(count, 1u) == (unsigned)(tl.n_parts - 1);
-      if (last) *count = 0u;  // ready for the next call
-      *s_last = last;
-      __threadfence();
-    }
-    consumer_sync();
-    if (!ok) return;
-    if (!*s_last) continue;
-    constexpr int VL = D / 32;  // values per lane: a warp joins a row
-    for (int g = warp; g < G; g += kConsumers) {
-      float top = -INFINITY, l = 0.f, acc[VL];
+    // ---- joining: the last of a group of 16 parts to get here joins the group, the last group's joiner the groups ----
+    // A release by one thread after the warps' meeting covers what all of them wrote.
+    auto is_last = [&](unsigned* count, int of) -> bool {
+      consumer_sync();
+      if (ok && tid == 0) {
+        const bool last = add_acq_rel(count) == (unsigned)(of - 1);
+        if (last) *count = 0u;  // ready for the next call
+        *s_last = last;
+      }
+      consumer_sync();
+      return ok && *s_last;
+    };
+    // parts p0, p0 + step, .. (n of them): every thread joins 4 values of a row, kAtOnce parts in flight
+    auto join = [&](int p0, int step, int n, bool to_out) {
+      constexpr int kAtOnce = D == 128 ? 16 : 8;
+      for (int x0 = warp * 32; x0 < G * kPerRow; x0 += kConsumers * 32) {
+        const int x = min(x0 + lane, G * kPerRow - 1), g = x / kPerRow, c = (x - g * kPerRow) * 4;
+        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < n; b += kAtOnce) {
+          float2 ml[kAtOnce];
+          float4 v[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < VL; ++e) acc[e] = 0.f;
-      for (int p0 = 0; p0 < tl.n_parts; p0 += 32) {
-        const int p = p0 + lane, n = min(32, tl.n_parts - p0);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (int64_t)((tl.i0 + p) * 2 + (p == 0)) * G + g);
-        float most = ml.x;
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t from = (int64_t)part_place(tl.i0, p0 + min(b + k, n - 1) * step) * G + g;
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + from);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + c));
+          }
+          float top = m;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        most = fmaxf(most, top);
-        const float base = most == -INFINITY ? 0.f : most;
-        const float w = ex2(ml.x - base), f = ex2(top - base);
-        float part_l = ml.y * w;
+          for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+          const float base = top == -INFINITY ? 0.f : top, f = ex2(m - base);
+          l *= f;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, d);
-        l = l * f + part_l;
-        top = most;
+          for (int e = 0; e < 4; ++e) acc[e] *= f;
 #pragma unroll
-        for (int e = 0; e < VL; ++e) acc[e] *= f;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w, k);
-          const float* src = a.part_o + ((int64_t)((tl.i0 + p0 + k) * 2 + (p0 + k == 0)) * G + g) * D + lane * VL;
-          float x[VL];
-          if (VL == 4) *reinterpret_cast<float4*>(x) = __ldcg(reinterpret_cast<const float4*>(src));
-          else if (VL == 2) *reinterpret_cast<float2*>(x) = __ldcg(reinterpret_cast<const float2*>(src));
-          else x[0] = __ldcg(src);
-#pragma unroll
-          for (int e = 0; e < VL; ++e) acc[e] += wk * x[e];
+          for (int k = 0; k < kAtOnce; ++k)
+            if (b + k < n) {
+              const float w = ex2(ml[k].x - base);
+              l += w * ml[k].y;
+              acc[0] += w * v[k].x;
+              acc[1] += w * v[k].y;
+              acc[2] += w * v[k].z;
+              acc[3] += w * v[k].w;
+            }
+          m = top;
         }
+        __syncwarp();  // (a row's lanes, one warp, have read the first part, whose place the group's sum takes)
+        if (x0 + lane != x) continue;
+        if (to_out) finish(g, c, m, l, acc);
+        else keep(part_place(tl.i0, p0), g, c, m, l, acc);
       }
-      const int qh = tl.h * G + g;
-      T* dst_o = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + lane * VL;
-      if (VL == 4) *reinterpret_cast<uint2*>(dst_o) = make_uint2(pack2<T>(acc[0] / l, acc[1] / l), pack2<T>(acc[VL - 2] / l, acc[VL - 1] / l));
-      else if (VL == 2) *reinterpret_cast<uint32_t*>(dst_o) = pack2<T>(acc[0] / l, acc[VL - 1] / l);
-      else {
-        const uint32_t x = pack2<T>(acc[0] / l, 0.f);
-        *reinterpret_cast<uint16_t*>(dst_o) = (uint16_t)x;
+    };
+    const int g0 = part / kGroup * kGroup, in_group = min(kGroup, tl.n_parts - g0);
+    const int n_groups = (tl.n_parts + kGroup - 1) / kGroup;
+    if (in_group > 1) {
+      if (!is_last(a.count + part_place(tl.i0, g0), in_group)) {
+        if (!ok) return;
+        continue;
       }
-      if (lane == 0 && a.lse)
-        a.lse[(int64_t)tl.r * a.q_heads + qh] = ((top == -INFINITY ? 0.f : top) - kShift) * kLn2 + logf(l);
+      join(g0, 1, in_group, n_groups == 1);
     }
+    if (n_groups == 1) continue;
+    if (!is_last(a.count + a.n_places + part_place(tl.i0, 0), n_groups)) {
+      if (!ok) return;
+      continue;
+    }
+    join(0, kGroup, n_groups, true);
   }
 }
 

@@ -363,13 +363,14 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  *   q, out [n_req][q_heads][head_dim] of `dtype`, 16-byte aligned, requests q_stride / out_stride values apart (a
  *         multiple of 8, at least q_heads * head_dim); out must not overlap q or the pools
  *   lens  [n_req] int32; a request of length 0 gives zeros (and lse = -infinity)
- *   table [n_req][max_pages] int32: page ids of the first ceil(lens / page_size) entries; the rest is not read
+ *   table [n_req][max_pages] int32: page ids in the first ceil(lens / page_size) entries; the rest is ignored
  *   scale finite; with the ranking model's temperature 1 / (tau * sqrt(head_dim))
  *   lse   fp32 [n_req][q_heads] natural log of the softmax's denominator; NULL: not written
  * What lies in a page behind the history (or before the window) never reaches the output, whatever its bits. Logits,
  * softmax and sums are fp32. Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length
  * outside [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read;
- * out is not meaningful), CVR_E_TIMEOUT. */
+ * out is not meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not written,
+ * but for the empty requests), CVR_E_TIMEOUT. */
 cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
                          const int32_t* table, float scale, void* out, int64_t out_stride, float* lse);
 
