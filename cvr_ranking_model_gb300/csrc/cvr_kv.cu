@@ -32,8 +32,6 @@ struct cvr_kv {
 
 namespace {
 
-constexpr int kMinTiles = 1;  // least tiles of an attention CTA's run
-
 cvr_status kv_fail(cvr_kv* h, cvr_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -314,18 +312,17 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   a.page_log2 = h->page_log2;
   a.max_pages = c.max_pages;
   a.window = c.window;
-  a.min_tiles = kMinTiles;
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.count = h->count;
   a.n_places = h->n_places;
   a.err = h->err_host_dev;
-  // one CTA per least run of the tiles that there can be at most, at most as many as the SMs hold at once
+  // one CTA per tile that there can be at most, at most as many as the SMs hold at once
   const int64_t seen = c.window && c.window < c.max_pages * c.page_size ? c.window + h->attend.tile : (int64_t)c.max_pages * c.page_size;
   const int64_t most = n_req * c.kv_heads * ((seen + h->attend.tile - 1) / h->attend.tile);
-  const int64_t want = (most + kMinTiles - 1) / kMinTiles, fit = (int64_t)h->num_sms * h->attend.ctas_per_sm;
+  const int64_t fit = (int64_t)h->num_sms * h->attend.ctas_per_sm;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(want < fit ? want : fit));
+  lc.gridDim = dim3((unsigned)(most < fit ? most : fit));
   lc.blockDim = dim3(kKvAttendThreads);
   lc.dynamicSmemBytes = h->attend.smem;
   lc.stream = h->stream;

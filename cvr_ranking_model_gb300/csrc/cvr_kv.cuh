@@ -47,7 +47,6 @@ struct KvAttendArgs {
   int64_t q_stride, out_stride, n_pages;
   float scale;
   int n_req, q_heads, kv_heads, group, page_log2, max_pages, window;
-  int min_tiles;    // least tiles of a CTA's even share
   // workspace: what a CTA leaves of a (request, head) that it shares with others
   float *part_o, *part_ml;  // [n_places][group][head_dim], [n_places][group][m, l]
   unsigned* count;          // [2][n_places] parts of a group, groups of a (request, head) written (zero between calls)

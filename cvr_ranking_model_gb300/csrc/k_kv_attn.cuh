@@ -34,12 +34,12 @@ constexpr int kThreads = (kConsumers + 1) * 32;     // and the producer
 static_assert(kThreads == kKvAttendThreads, "the launch's block");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-struct __align__(16) Tile {
-  int r, h, k0, flags;       // request, kv head, first token of the tile; kFirst .., the part's number << kPartShift
+// A part: the tiles of one (request, kv head) in a CTA's run.
+struct __align__(16) Part {
+  int r, h, k0, n_tiles;     // request, kv head, first token of the first tile
   int lo, len, i0, n_parts;  // tokens seen: [lo, len); the (request, head) has n_parts parts, of CTAs i0, i0 + 1, ..
 };
-constexpr int kLast = 1, kPartShift = 1;  // last tile of a part
-constexpr int kGroup = 16;                // parts that are joined at once
+constexpr int kGroup = 16;  // parts that are joined at once
 
 // MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64
 template <bool I8, int D, int MODE>
@@ -49,27 +49,28 @@ struct Shape {
   static constexpr int kRow = D * (I8 ? 1 : 2);                 // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int kCtasPerSm = MT > 1 ? 1 : D < 128 ? 4 : 2;
-  static constexpr int kUnitMost = kCtasPerSm <= 2 ? 16384 : 8192;
+  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 ? 3 : 2) : 2;
+  static constexpr int kUnitMost = kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
   static constexpr int kQBytes = (MODE == 0 ? 8 : MT * 16) * kQRow;
   static constexpr int kORow = D + (I8 ? 16 : 8);               // padded fp32 rows of the joining area
+  static constexpr int kOBytes = kConsumers * 8 * kORow * 4 + 2 * kConsumers * 8 * 4;  // with its rows' m and l
+  static constexpr int kOAreas = D == 32 ? 2 : 1;              // (two spare a barrier per use, where they fit)
   static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
   // ring units: what is left of this CTA's share of the SM's 228 KB (1 KB of it reserved, 1 KB for the ring's alignment)
   static constexpr int kShare = kCtasPerSm == 1 ? 232448 : 233472 / kCtasPerSm - 1024;
-  static constexpr int kFixed = 2 * kQBytes + kConsumers * 8 * kORow * 4 + 2 * kConsumers * 16 * 4 + 5 * 8 + 64 + 1024;
-  static constexpr int kRing = (kShare - kFixed) / (kUnit + kScaleBytes + (int)sizeof(Tile) + 16);
+  static constexpr int kFixed = 2 * kQBytes + kOAreas * kOBytes + 3 * (int)sizeof(Part) + 5 * 8 + 64 + 1024;
+  static constexpr int kRing = (kShare - kFixed) / (kUnit + kScaleBytes + 16);
   // shared memory
   static constexpr int oScale = kRing * kUnit;
   static constexpr int oQ = oScale + kRing * kScaleBytes;
   static constexpr int oO = oQ + 2 * kQBytes;
-  static constexpr int oStat = oO + kConsumers * 8 * kORow * 4;
-  static constexpr int oTile = oStat + 2 * kConsumers * 16 * 4;
-  static constexpr int oBar = oTile + kRing * (int)sizeof(Tile);
+  static constexpr int oPart = oO + kOAreas * kOBytes;
+  static constexpr int oBar = oPart + 3 * (int)sizeof(Part);
   static constexpr int kSmem = oBar + (2 * kRing + 5) * 8 + 64 + 1024;
   static_assert(kSmem <= kShare && kRing >= 4, "K and V units of two tiles at least");
 };
@@ -93,21 +94,32 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-template <typename T>
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// c (+)= a b; FIRST: the accumulator starts from zero
+template <typename T, bool FIRST = false>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (FIRST) {
+    if (std::is_same<T, __half>::value)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  } else {
+    if (std::is_same<T, __half>::value)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -126,13 +138,42 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// two of the four signed bytes of x as an fp16 pair: SEL picks the bytes (0x4140: 0 and 1, 0x4342: 2 and 3, 0x4240: 0 and
-// 2, 0x4341: 1 and 3); x ^ 0x80 per byte is q + 128, the bits 0x64.. are 1024 + (q + 128)
+// two of the four bytes of x, biased signed values (q ^ 0x80 = q + 128), as an fp16 pair: SEL picks the bytes (0x4140: 0 and
+// 1, 0x4342: 2 and 3, 0x4240: 0 and 2, 0x4341: 1 and 3); the bits 0x64.. are 1024 + (q + 128). `k64` holds 0x64646464.
 template <int SEL>
-__device__ __forceinline__ uint32_t i8_pair(uint32_t x) {
-  const uint32_t u = __byte_perm(x ^ 0x80808080u, 0x64646464u, SEL);
+__device__ __forceinline__ uint32_t i8_pair(uint32_t x, uint32_t k64) {
+  const uint32_t u = __byte_perm(x, k64, SEL);
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// A wait of a whole warp, bounded like mbar_wait: the hardware may hold a polling warp for up to 1 ms at a time, so that
+// waiting warps do not take the others' issue slots.
+__device__ __forceinline__ bool try_wait_1ms(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (__all_sync(0xffffffffu, try_wait_1ms(bar, parity))) return true;
+    const bool late = global_timer_ns() - t0 > 1000000000ull;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || late)) {
+      if (late) {
+        *abort_flag = 1;
+        atomicOr(err, kErrTimeout);
+      }
+      __syncwarp();
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag, err);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -177,9 +218,9 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   uint64_t* const meet = q_empty + 2;      // the consumer warps' barrier
   volatile int* const abort_flag = reinterpret_cast<int*>(meet + 1);
   int* const s_last = const_cast<int*>(abort_flag) + 1;
-  uint32_t* const s_sum = reinterpret_cast<uint32_t*>(sm + S::oStat);  // scan scratch, before the first part ends
+  uint32_t* const s_sum = reinterpret_cast<uint32_t*>(sm + S::oPart);  // scan scratch, before the first part
   int* const s_start = s_last + 1;  // request of the CTA's first tile, and the tiles per head before it
-  Tile* const tiles = reinterpret_cast<Tile*>(sm + S::oTile);
+  Part* const s_part = reinterpret_cast<Part*>(sm + S::oPart);  // [2] with the query rows, [1] the early part
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.kv_heads, G = a.group;
   const bool two = a.v != nullptr;  // V is a pool of its own
@@ -231,7 +272,9 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const bool fits = (uint64_t)all * H <= 0x7fffffffu;
   if (!fits && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kKvErrSize);
   const int total = fits ? (int)all * H : 0;
-  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, a.min_tiles);
+  // An even share of the tiles; at least two where requests have two or more on average: a split costs a join (about 2 us at
+  // a call's end), a second tile about 0.5 us. One request of 200 tokens of 4 x 32: 4.7 us in 4 runs, 5.8 us in 8.
+  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, (int)all >= 2 * a.n_req ? 2 : 1);
   const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min((int64_t)begin + per, (int64_t)total);
   const int n_tiles = end - begin;
   if (n_tiles > 0 && begin >= (int)before * H && begin < (int)(before + mine) * H) {
@@ -287,10 +330,6 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         t0 = lo / TK;
         n_t = max(1, tiles_of<TK>(a, len));
       };
-      auto rewind = [&]() {  // to the request's first pages
-        e0 = first_entry(len);
-        more_ids = entries(r, e0 + 32);
-      };
       window(wb);
       look_ahead(wb);
       enter();
@@ -299,92 +338,81 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       e0 = ((t0 + t) * TK) >> a.page_log2;  // (the run may begin anywhere in its request)
       ids = entries(r, e0);
       more_ids = entries(r, e0 + 32);
-      bool ahead = false;  // looked ahead from this request
-      int i0 = 0, n_parts = 1;
       bool ok = true;
-      for (int at = begin; at < end; ++at) {
-        const bool first = at == begin || t == 0;
-        const int k0 = (t0 + t) * TK;
-        if (first) {
-          const int fb = P * H + h * n_t;
-          i0 = fb / per;
-          n_parts = (fb + n_t - 1) / per - i0 + 1;
-          // the part's query rows
-          const int b = parts & 1;
-          ok = mbar_wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
-          __syncwarp();
-          const T* q = static_cast<const T*>(a.q) + r * a.q_stride + (int64_t)h * G * D;
-          for (int g = lane; g < G; g += 32) bulk_load(smem_u32(sm + S::oQ + b * S::kQBytes + g * S::kQRow), q + g * D, D * 2, q_full + b);
-          ++parts;
-        }
-        if ((k0 >> a.page_log2) >= e0 + 32) {
-          ids = more_ids;
-          e0 += 32;
-          more_ids = entries(r, e0 + 32);
-        }
-        // in lane b: box b of the tile, wanted if any of its tokens is seen
-        const int from = k0 + (lane << log2_br), row = from & ((1 << a.page_log2) - 1);
-        const bool need = lane < n_box_max && from < len && from + br > lo;
-        int page = __shfl_sync(0xffffffffu, ids, ((from >> a.page_log2) - e0) & 31);
-        if (need && (page < 0 || page >= a.n_pages)) {
-          atomicOr(a.err, kKvErrPage);
-          page = 0;
-        }
-        const int n_box = __popc(__ballot_sync(0xffffffffu, need));
-#pragma unroll 1
-        for (int w = 0; w < (two ? 2 : 1); ++w) {
-          ok = mbar_wait_warp(empty + slot, phase ^ 1, abort_flag, a.err);
-          if (!ok) break;
-          if (lane == 0) {
-            if (w == 0) {
-              Tile tl;
-              tl.r = r;
-              tl.h = h;
-              tl.k0 = k0;
-              tl.flags = (at + 1 == end || t + 1 == n_t ? kLast : 0) | (((int)blockIdx.x - i0) << kPartShift);
-              tl.lo = lo;
-              tl.len = len;
-              tl.i0 = i0;
-              tl.n_parts = n_parts;
-              tiles[slot] = tl;
-            }
-            mbar_expect_tx(full + slot, (uint32_t)(n_box * br) * (S::kRow + (I8 ? 4 : 0)));
-          }
-          __syncwarp();
-          if (need) {
-            uint8_t* dst = sm + slot * S::kUnit + (lane << log2_br) * S::kRow;
-            tma_load_5d(dst, w ? &tm_v : &tm_k, full + slot, 0, row, 0, h, page);
-            if (I8)
-              bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
-                        (w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row), 4 << log2_br, full + slot);
-          }
-          filled = min(filled + 1, RING);
-          if (++slot == RING) {
-            slot = 0;
-            phase ^= 1;
-          }
-        }
+      const uint64_t box_bytes = (uint64_t)br * (S::kRow + (I8 ? 4 : 0));
+      for (int at = begin; at < end && ok;) {
+        // ---- a part: its query rows and description, then its tiles ----
+        const int n = min(n_t - t, end - at), b = parts & 1;
+        ok = wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
         if (!ok) break;
-        // on to the next tile: of the head, of the next head, of the next request
-        if (++t == n_t && at + 1 < end) {
-          t = 0;
-          if (++h < H) {
-            ids = entries(r, first_entry(len));
-          } else {
-            h = 0;
-            P += n_t;
-            if (!ahead) look_ahead(r + 1);
-            ids = n_ids;
-            enter();
-            ahead = false;
-          }
-          rewind();
-        } else if (!ahead && h + 1 == H) {
-          look_ahead(r + 1);
-          ahead = true;
+        if (lane == 0) {
+          const int fb = P * H + h * n_t;
+          Part pt;
+          pt.r = r;
+          pt.h = h;
+          pt.k0 = (t0 + t) * TK;
+          pt.n_tiles = n;
+          pt.lo = lo;
+          pt.len = len;
+          pt.i0 = fb / per;
+          pt.n_parts = (fb + n_t - 1) / per - pt.i0 + 1;
+          s_part[b] = pt;
+          mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
         }
+        __syncwarp();
+        const T* q = static_cast<const T*>(a.q) + r * a.q_stride + (int64_t)h * G * D;
+        for (int g = lane; g < G; g += 32) bulk_load(smem_u32(sm + S::oQ + b * S::kQBytes + g * S::kQRow), q + g * D, D * 2, q_full + b);
+        ++parts;
+        if (h + 1 == H && n == n_t - t && at + n < end) look_ahead(r + 1);  // (its lengths and page ids arrive meanwhile)
+        for (int i = 0; i < n && ok; ++i) {
+          const int k0 = (t0 + t + i) * TK;
+          if ((k0 >> a.page_log2) >= e0 + 32) {
+            ids = more_ids;
+            e0 += 32;
+            more_ids = entries(r, e0 + 32);
+          }
+          // in lane b: box b of the tile, wanted if any of its tokens is seen
+          const int from = k0 + (lane << log2_br), row = from & ((1 << a.page_log2) - 1);
+          const bool need = lane < n_box_max && from < len && from + br > lo;
+          int page = __shfl_sync(0xffffffffu, ids, ((from >> a.page_log2) - e0) & 31);
+          if (need && (unsigned)page >= (unsigned)a.n_pages) {
+            atomicOr(a.err, kKvErrPage);
+            page = 0;
+          }
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need)) * (uint32_t)box_bytes;
+#pragma unroll 1
+          for (int w = 0; w < (two ? 2 : 1); ++w) {
+            ok = wait_warp(empty + slot, phase ^ 1, abort_flag, a.err);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(full + slot, bytes);
+            __syncwarp();
+            if (need) {
+              tma_load_5d(sm + slot * S::kUnit + (lane << log2_br) * S::kRow, w ? &tm_v : &tm_k, full + slot, 0, row, 0, h, page);
+              if (I8)
+                bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
+                          (w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row), 4 << log2_br, full + slot);
+            }
+            filled = min(filled + 1, RING);
+            if (++slot == RING) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        // on to the next head, or the next request
+        at += n;
+        if (at >= end) break;
+        t = 0;
+        if (++h < H) {
+          ids = entries(r, first_entry(len));
+        } else {
+          h = 0;
+          P += n_t;
+          ids = n_ids;
+          enter();
+        }
+        e0 = first_entry(len);
+        more_ids = entries(r, e0 + 32);
       }
     }
     // requests that see nothing, shared out over the grid
@@ -416,19 +444,25 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const int gid = lane >> 2, tig = lane & 3;
   const int mt = warp % MT, kp = warp / MT;  // row tile, share of the tokens
   const int log2_br = min(a.page_log2, 31 - __clz(TK));
-  const float sl2 = a.scale * kLog2e;
+  // Logits in units of ln 2 are c q . k with c >= 0 (q is negated for a negative scale, and a scale of zero is the least
+  // number above it: a token that is not seen has q . k = -infinity, whose product must stay that).
+  const float c_all = fmaxf(fabsf(a.scale) * kLog2e, 1.4e-45f);
+  const bool negate = a.scale < 0.f;
   // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8,
   // with 8-bit rows times 2^8 / vmax.
   constexpr float kGrow = 6.f, kWeight = 256.f;
   constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
+  constexpr uint32_t kOnes = std::is_same<M, __half>::value ? 0x3c003c00u : 0x3f803f80u;
+  uint32_t k64 = 0;
+  if (I8) asm volatile("mov.b32 %0, 0x64646464;" : "=r"(k64));  // (kept in a register)
   uint32_t meets = 0;
   bool ok = true;
   auto consumer_sync = [&]() {  // a bounded barrier of the four warps
     __syncwarp();
     if (lane == 0) mbar_arrive(meet);
-    ok = mbar_wait_warp(meet, meets & 1, abort_flag, a.err) && ok;
+    ok = wait_warp(meet, meets & 1, abort_flag, a.err) && ok;
     ++meets;
   };
   // Addresses of ldmatrix rows in a unit. A unit is boxes of [half][row][line]; block_at is the offset of a 16-token
@@ -441,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   auto row_off = [&](int upper) -> uint32_t {
     return l7 * S::kLine + upper * (log2_br >= 4 ? 8 * S::kLine : S::kHalves * 8 * S::kLine);
   };
-  const uint32_t lane_k = row_off(up16) + ((up8 << 4) ^ swz), lane_v = row_off(up8) + ((up16 << 4) ^ swz);
+  const uint32_t ring = smem_u32(sm);
+  const uint32_t lane_k = ring + row_off(up16) + ((up8 << 4) ^ swz), lane_v = ring + row_off(up8) + ((up16 << 4) ^ swz);
   auto block_at = [&](int key) -> uint32_t {
     return (uint32_t)(((key >> log2_br) * S::kHalves << log2_br) + (key & ((1 << log2_br) - 1))) * S::kLine;
   };
@@ -449,141 +484,145 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     return (addr ^ (uint32_t)(k * 32 % S::kLine)) + (k * 32 / S::kLine) * half_step;
   };
 
-  int ks = 0, parts = 0;  // the ring's next unit, and parts begun
+  int ks = 0, parts = 0, areas = 0;  // the ring's next unit, parts begun, joining areas used
   uint32_t phase = 0;
-  float* const s_o = reinterpret_cast<float*>(sm + S::oO);
-  float* const s_m = reinterpret_cast<float*>(sm + S::oStat);
-  float* const s_l = s_m + kConsumers * 16;
+  // A part that the CTA before began and that ends within this run: counted when it is done, looked at when the run is
+  // through (in s_part[2]).
+  bool early = false;
+  unsigned early_count = 0;  // (thread 0: the parts counted before it)
 
-  for (int i = 0; i < n_tiles;) {
+  for (int done = 0; done < n_tiles;) {
     // ---- a part: the tiles of one (request, head) in this CTA's run ----
     uint32_t qf[D / 16][4];
-    float o[D / 8][4];
+    float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-    float cA = sl2, cB = sl2;  // logit factors of rows A (gid) and B (gid + 8)
+    float cA = c_all, cB = c_all;  // logit factors of rows A (gid) and B (gid + 8)
     float vmax = 0x1p-100f, w_mul = kWeight * 0x1p100f;  // 8 bits: the largest row scale of V so far (floored)
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    Tile tl;
-    const int b = parts & 1;
-    ok = mbar_wait_warp(q_full + b, (parts >> 1) & 1, abort_flag, a.err);
+    const int qb = parts & 1;
+    ok = wait_warp(q_full + qb, (parts >> 1) & 1, abort_flag, a.err);
     if (!ok) return;
-    const uint8_t* qs = sm + S::oQ + b * S::kQBytes + mt * 16 * S::kQRow;
-    const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
-    if (!I8) {
+    const Part pt = s_part[qb];
+    {
+      const uint8_t* qs = sm + S::oQ + qb * S::kQBytes + mt * 16 * S::kQRow;
+      const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
+      if (!I8) {
+        const uint32_t flip = negate ? 0x80008000u : 0u;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
-        qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) : 0u;
-        qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) : 0u;
-        qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) : 0u;
-        qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) : 0u;
-      }
-    } else {
-      // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
-      float mulA = 1.f, mulB = 1.f;
-      uint2 xa[D / 16], xb[D / 16];
+        for (int k = 0; k < D / 16; ++k) {
+          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
+          qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) ^ flip : 0u;
+          qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) ^ flip : 0u;
+          qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) ^ flip : 0u;
+          qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) ^ flip : 0u;
+        }
+      } else {
+        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
+        float mulA = 1.f, mulB = 1.f;
+        uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
-        xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
-        xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
-      }
-      if (std::is_same<T, __nv_bfloat16>::value) {
-        // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
-        // of it, 2^-25 of it below
-        float bigA = 0.f, bigB = 0.f;
+        for (int k = 0; k < D / 16; ++k) {
+          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
+          xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
+          xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
+        }
+        if (std::is_same<T, __nv_bfloat16>::value) {
+          // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
+          // of it, 2^-25 of it below
+          float bigA = 0.f, bigB = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
+            bigA = fmaxf(fmaxf(bigA, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+            bigB = fmaxf(fmaxf(bigB, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(z.x), fabsf(z.y)));
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
+            bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
+          }
+          const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
+          const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
+          mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
+          mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
+          cA = fitA ? fmaxf(c_all * __uint_as_float(eA << 23), 1.4e-45f) : c_all;
+          cB = fitB ? fmaxf(c_all * __uint_as_float(eB << 23), 1.4e-45f) : c_all;
+        }
+        if (negate) {
+          mulA = -mulA;
+          mulB = -mulB;
+        }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
-          bigA = fmaxf(fmaxf(bigA, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
-          bigB = fmaxf(fmaxf(bigB, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(z.x), fabsf(z.y)));
+          qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
+          qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
+          qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
+          qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
         }
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
-          bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
-        }
-        const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
-        const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
-        mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
-        mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
-        cA = fitA ? sl2 * __uint_as_float(eA << 23) : sl2;
-        cB = fitB ? sl2 * __uint_as_float(eB << 23) : sl2;
-      }
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
-        qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
-        qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
-        qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
-        qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_empty + b);
+    if (lane == 0) mbar_arrive(q_empty + qb);
     ++parts;
-    do {
-      ok = mbar_wait_warp(full + ks, phase, abort_flag, a.err);
-      if (!ok) return;
-      tl = tiles[ks];
-      ++i;
-      const uint32_t k_unit = smem_u32(sm + ks * S::kUnit);
-      const int vs_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
-      const uint32_t vs_phase = vs_slot < ks ? phase ^ 1 : phase;
-      const uint32_t v_unit = smem_u32(sm + vs_slot * S::kUnit);
-      const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + ks * S::kScaleBytes);
-      const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + vs_slot * S::kScaleBytes);
-      // tokens of the tile that are seen, and whether that is not all of them
-      const int j0 = max(tl.lo - tl.k0, 0), j1 = min(tl.len - tl.k0, TK);
-      const bool partial = j0 > 0 || j1 < TK;
+    done += pt.n_tiles;
 
+    // One tile: its K and V units, and its tokens [j0, j1) that are seen. Whole tiles take the instance without masks.
+    auto step = [&](auto masked, int k_slot, int v_slot, uint32_t v_phase, int j0, int j1) {
+      constexpr bool MASK = decltype(masked)::value;
+      const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + k_slot * S::kScaleBytes);
+      const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + v_slot * S::kScaleBytes);
 #pragma unroll 1
       for (int sub = 0; sub < NB / NBS; ++sub) {
-        // S = Q K^T: two chains of products per 8 tokens, so that their latencies overlap
+        // S = Q K^T
         float s[NBS][2][4];
 #pragma unroll
         for (int b = 0; b < NBS; ++b) {
           const int key = ((sub * NBS + b) * KP + kp) * 16;
-          float odd[2][4];
+          if (MASK && !(key + 16 > j0 && key < j1)) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[b][n][e] = odd[n][e] = 0.f;
-          if (key + 16 > j0 && key < j1) {
-            const uint32_t base = k_unit + block_at(key) + lane_k;
-            if (!I8) {
+              for (int e = 0; e < 4; ++e) s[b][n][e] = 0.f;
+            continue;
+          }
+          const uint32_t base = lane_k + k_slot * S::kUnit + block_at(key);
+          if (!I8) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                uint32_t f[4];
-                ldsm4(f, piece(base, k));
-                mma16816<M>(k & 1 ? odd[0] : s[b][0], qf[k], f[0], f[1]);
-                mma16816<M>(k & 1 ? odd[1] : s[b][1], qf[k], f[2], f[3]);
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t f[4];
+              ldsm4(f, piece(base, k));
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                if (k == 0) mma16816<M, true>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
+                else mma16816<M>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
               }
-            } else {
+            }
+          } else {
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k) {
-                uint32_t f[4];
-                ldsm4(f, piece(base, k));
-                mma16816<M>(s[b][0], qf[2 * k], i8_pair<0x4140>(f[0]), i8_pair<0x4342>(f[0]));
-                mma16816<M>(s[b][1], qf[2 * k], i8_pair<0x4140>(f[2]), i8_pair<0x4342>(f[2]));
-                mma16816<M>(odd[0], qf[2 * k + 1], i8_pair<0x4140>(f[1]), i8_pair<0x4342>(f[1]));
-                mma16816<M>(odd[1], qf[2 * k + 1], i8_pair<0x4140>(f[3]), i8_pair<0x4342>(f[3]));
+            for (int k = 0; k < D / 16; k += 2) {
+              uint32_t f[4];
+              ldsm4(f, piece(base, k / 2));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] ^= 0x80808080u;
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const uint32_t e0 = i8_pair<0x4140>(f[2 * n], k64), e1 = i8_pair<0x4342>(f[2 * n], k64);
+                const uint32_t d0 = i8_pair<0x4140>(f[2 * n + 1], k64), d1 = i8_pair<0x4342>(f[2 * n + 1], k64);
+                if (k == 0) mma16816<M, true>(s[b][n], qf[k], e0, e1);
+                else mma16816<M>(s[b][n], qf[k], e0, e1);
+                mma16816<M>(s[b][n], qf[k + 1], d0, d1);
               }
             }
           }
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < (R8 ? 2 : 4); ++e) s[b][n][e] += odd[n][e];
         }
         if (sub == 0 && two) {
-          ok = mbar_wait_warp(full + vs_slot, vs_phase, abort_flag, a.err);
+          ok = wait_warp(full + v_slot, v_phase, abort_flag, a.err);
           if (!ok) return;
         }
-        // logits in units of ln 2; tokens that are not seen are out
         float nA = -INFINITY, nB = -INFINITY, big = 0.f;
         float2 sv[NBS][2];  // 8 bits: V's row scales
 #pragma unroll
@@ -591,18 +630,17 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
-            float2 sk = make_float2(1.f, 1.f);
             if (I8) {
-              sk = *reinterpret_cast<const float2*>(k_sc + key);
+              const float2 sk = *reinterpret_cast<const float2*>(k_sc + key);
               sv[b][n] = *reinterpret_cast<const float2*>(v_sc + key);
+              s[b][n][0] *= sk.x;
+              s[b][n][1] *= sk.y;
+              if (!R8) {
+                s[b][n][2] *= sk.x;
+                s[b][n][3] *= sk.y;
+              }
             }
-            s[b][n][0] *= I8 ? cA * sk.x : cA;
-            s[b][n][1] *= I8 ? cA * sk.y : cA;
-            if (!R8) {
-              s[b][n][2] *= I8 ? cB * sk.x : cB;
-              s[b][n][3] *= I8 ? cB * sk.y : cB;
-            }
-            if (partial) {
+            if (MASK) {  // tokens that are not seen are out
               if (key < j0 || key >= j1) {
                 s[b][n][0] = s[b][n][2] = -INFINITY;
                 if (I8) sv[b][n].x = 0.f;
@@ -616,6 +654,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
             if (I8) big = fmaxf(big, fmaxf(fabsf(sv[b][n].x), fabsf(sv[b][n].y)));
           }
+        nA *= cA;
+        if (!R8) nB *= cB;
         // The exponents' base follows the running maximum only when a logit passes it by more than kGrow, and the weights'
         // divisor the largest V scale when a scale passes it: most steps then need neither shuffles nor a rescaling.
         if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || (I8 && big > vmax))) {
@@ -630,15 +670,18 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           const float fA = nA == mA ? 1.f : ex2(mA - nA), fB = R8 ? fA : nB == mB ? 1.f : ex2(mB - nB);
           mA = nA;
           mB = nB;
-          lA *= fA;
-          if (!R8) lB *= fB;
           float gA = fA, gB = fB;
           if (I8) {
+            lA *= fA;
+            if (!R8) lB *= fB;
             big = fmaxf(big, vmax);
             gA *= vmax / big;
             gB *= vmax / big;
             vmax = big;
             w_mul = kWeight / big;
+          } else {
+            ls[0] *= fA;
+            ls[2] *= fB;
           }
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
@@ -649,22 +692,22 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           }
         }
         // (a base of -infinity is left out of the exponent: nothing was seen yet, or every logit is -infinity)
-        const float subA = (mA == -INFINITY ? 0.f : mA) - kShift, subB = (mB == -INFINITY ? 0.f : mB) - kShift;
+        const float subA = kShift - (mA == -INFINITY ? 0.f : mA), subB = kShift - (mB == -INFINITY ? 0.f : mB);
 #pragma unroll
         for (int b = 0; b < NBS; ++b) {
           const int key0 = ((sub * NBS + b) * KP + kp) * 16;
-          if (!(key0 + 16 > j0 && key0 < j1)) continue;
+          if (MASK && !(key0 + 16 > j0 && key0 < j1)) continue;
           uint32_t hi[4], lw[4];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float pA0 = ex2(s[b][n][0] - subA), pA1 = ex2(s[b][n][1] - subA), pB0 = 0.f, pB1 = 0.f;
-            lA += pA0 + pA1;
+            float pA0 = ex2(fmaf(s[b][n][0], cA, subA)), pA1 = ex2(fmaf(s[b][n][1], cA, subA)), pB0 = 0.f, pB1 = 0.f;
             if (!R8) {
-              pB0 = ex2(s[b][n][2] - subB);
-              pB1 = ex2(s[b][n][3] - subB);
-              lB += pB0 + pB1;
+              pB0 = ex2(fmaf(s[b][n][2], cB, subB));
+              pB1 = ex2(fmaf(s[b][n][3], cB, subB));
             }
             if (I8) {
+              lA += pA0 + pA1;
+              if (!R8) lB += pB0 + pB1;
               const float w0 = sv[b][n].x * w_mul, w1 = sv[b][n].y * w_mul;
               pA0 *= w0;
               pA1 *= w1;
@@ -685,20 +728,24 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               lw[2 * n + 1] = pack2<M>(pB0 - fB.x, pB1 - fB.y);
             }
           }
+          if (!I8) {
+            mma16816<M>(ls, hi, kOnes, kOnes);
+            if (!R8) mma16816<M>(ls, lw, kOnes, kOnes);
+          }
           // rows of V that are not seen may hold anything: their bits are cleared (0 times an infinity is no number)
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (!I8 && partial) {
+          if (!I8 && MASK) {
             const int key = key0 + 2 * tig;
             keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
             keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
           }
-          const uint32_t base = v_unit + block_at(key0) + lane_v;
+          const uint32_t base = lane_v + v_slot * S::kUnit + block_at(key0);
           if (!I8) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t f[4];
               ldsm4_trans(f, piece(base, c));
-              if (partial) {
+              if (MASK) {
                 f[0] &= keep0;
                 f[1] &= keep1;
                 f[2] &= keep0;
@@ -718,9 +765,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               uint32_t f[4];
               ldsm4_trans(f, piece(base, c));
 #pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] ^= 0x80808080u;
+#pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t e0 = i8_pair<0x4240>(f[2 * e]), e1 = i8_pair<0x4240>(f[2 * e + 1]);
-                const uint32_t d0 = i8_pair<0x4341>(f[2 * e]), d1 = i8_pair<0x4341>(f[2 * e + 1]);
+                const uint32_t e0 = i8_pair<0x4240>(f[2 * e], k64), e1 = i8_pair<0x4240>(f[2 * e + 1], k64);
+                const uint32_t d0 = i8_pair<0x4341>(f[2 * e], k64), d1 = i8_pair<0x4341>(f[2 * e + 1], k64);
                 mma16816<M>(o[4 * c + 2 * e], hi, e0, e1);
                 mma16816<M>(o[4 * c + 2 * e + 1], hi, d0, d1);
                 if (!R8) {
@@ -732,100 +781,143 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           }
         }
       }
+    };
+    for (int i = 0; i < pt.n_tiles; ++i) {
+      ok = wait_warp(full + ks, phase, abort_flag, a.err);
+      if (!ok) return;
+      const int v_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
+      const uint32_t v_phase = v_slot < ks ? phase ^ 1 : phase;
+      const int k0 = pt.k0 + i * TK;
+      if (D < 128 && k0 >= pt.lo && k0 + TK <= pt.len) step(std::false_type(), ks, v_slot, v_phase, 0, TK);
+      else step(std::true_type(), ks, v_slot, v_phase, max(pt.lo - k0, 0), min(pt.len - k0, TK));
+      if (!ok) return;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(empty + ks);
-        if (two) mbar_arrive(empty + vs_slot);
+        if (two) mbar_arrive(empty + v_slot);
       }
-      phase = vs_slot + 1 == RING ? vs_phase ^ 1 : vs_phase;
-      ks = vs_slot + 1 == RING ? 0 : vs_slot + 1;
-    } while (!(tl.flags & kLast));
+      phase = v_slot + 1 == RING ? v_phase ^ 1 : v_phase;
+      ks = v_slot + 1 == RING ? 0 : v_slot + 1;
+    }
 
     // ---- the part's end: the warps' (m, l, o) to shared memory, 8 rows of each tile at a time, and summed ----
+    if (I8) {
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      lA += __shfl_xor_sync(0xffffffffu, lA, d);
-      if (!R8) lB += __shfl_xor_sync(0xffffffffu, lB, d);
+      for (int d = 1; d < 4; d <<= 1) {
+        lA += __shfl_xor_sync(0xffffffffu, lA, d);
+        if (!R8) lB += __shfl_xor_sync(0xffffffffu, lB, d);
+      }
+    } else {
+      lA = R8 ? ls[0] + ls[2] : ls[0];
+      lB = ls[2];
     }
     const float o_mul = I8 ? vmax / kWeight : 1.f;
-    // values c .. c + 3 of query row g, all tokens joined: the output; or so far: to a place of the workspace
-    auto finish = [&](int g, int c, float m, float l, const float* acc) {
-      const int qh = tl.h * G + g;
-      T* dst = static_cast<T*>(a.out) + (int64_t)tl.r * a.out_stride + (int64_t)qh * D + c;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc[0] / l, acc[1] / l), pack2<T>(acc[2] / l, acc[3] / l));
-      if (c == 0 && a.lse) a.lse[(int64_t)tl.r * a.q_heads + qh] = ((m == -INFINITY ? 0.f : m) - kShift) * kLn2 + logf(l);
+    // values c .. c + 3 of query row g of a (request, head), all tokens joined: the output; or so far: to a place of the
+    // workspace
+    auto finish = [&](const Part& of, int g, int c, float m, float l, const float* acc) {
+      const int qh = of.h * G + g;
+      T* dst = static_cast<T*>(a.out) + (int64_t)of.r * a.out_stride + (int64_t)qh * D + c;
+      const float inv = 1.f / l;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv));
+      if (c == 0 && a.lse) a.lse[(int64_t)of.r * a.q_heads + qh] = ((m == -INFINITY ? 0.f : m) - kShift) * kLn2 + logf(l);
     };
     auto keep = [&](int to, int g, int c, float m, float l, const float* acc) {
       __stcg(reinterpret_cast<float4*>(a.part_o + ((int64_t)to * G + g) * D + c), make_float4(acc[0], acc[1], acc[2], acc[3]));
       if (c == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + (int64_t)to * G + g, make_float2(m, l));
     };
-    const int part = tl.flags >> kPartShift;
-    const int place = part_place(tl.i0, part);
+    const int part = (int)blockIdx.x - pt.i0, place = part_place(pt.i0, part);
     constexpr int kPerRow = D / 4;  // 4 values per thread
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < (R8 ? 1 : 2); ++pass) {
-      consumer_sync();  // (the previous pass or part has been read)
-      if (!ok) return;
-      float* dst = s_o + (warp * 8 + gid) * S::kORow;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const float x = (R8 ? o[j][0] + o[j][2] : o[j][2 * pass]) * o_mul;
-        const float y = (R8 ? o[j][1] + o[j][3] : o[j][2 * pass + 1]) * o_mul;
-        if (!I8) {
-          *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
-        } else if (j & 1) {
-          // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)
-          const float u = (R8 ? o[j - 1][0] + o[j - 1][2] : o[j - 1][2 * pass]) * o_mul;
-          const float v = (R8 ? o[j - 1][1] + o[j - 1][3] : o[j - 1][2 * pass + 1]) * o_mul;
-          *reinterpret_cast<float4*>(dst + (j >> 1) * 16 + 4 * tig) = make_float4(u, x, v, y);
-        }
+      if (S::kOAreas == 1) {
+        consumer_sync();  // (the previous pass or part has been read; with two areas, the barrier of the use between says so)
+        if (!ok) return;
       }
-      if (tig == 0) {
-        s_m[warp * 16 + gid] = pass ? mB : mA;
-        s_l[warp * 16 + gid] = pass ? lB : lA;
+      float* const s_o = reinterpret_cast<float*>(sm + S::oO + (S::kOAreas == 1 ? 0 : (areas & 1)) * S::kOBytes);
+      float* const s_m = s_o + kConsumers * 8 * S::kORow;
+      float* const s_l = s_m + kConsumers * 8;
+      ++areas;
+      if (mt * 16 + pass * 8 + gid < G) {
+        float* dst = s_o + (warp * 8 + gid) * S::kORow;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          const float x = (R8 ? o[j][0] + o[j][2] : pass ? o[j][2] : o[j][0]) * o_mul;
+          const float y = (R8 ? o[j][1] + o[j][3] : pass ? o[j][3] : o[j][1]) * o_mul;
+          if (!I8) {
+            *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
+          } else if (j & 1) {
+            // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)
+            const float u = (R8 ? o[j - 1][0] + o[j - 1][2] : pass ? o[j - 1][2] : o[j - 1][0]) * o_mul;
+            const float v = (R8 ? o[j - 1][1] + o[j - 1][3] : pass ? o[j - 1][3] : o[j - 1][1]) * o_mul;
+            *reinterpret_cast<float4*>(dst + (j >> 1) * 16 + 4 * tig) = make_float4(u, x, v, y);
+          }
+        }
+        if (tig == 0) {
+          s_m[warp * 8 + gid] = pass ? mB : mA;
+          s_l[warp * 8 + gid] = pass ? lB : lA;
+        }
       }
       consumer_sync();
       if (!ok) return;
       for (int x = tid; x < 8 * MT * kPerRow; x += kConsumers * 32) {
         const int row8 = x / kPerRow, c = (x - row8 * kPerRow) * 4;
-        const int rt = row8 >> 3, g = rt * 16 + pass * 8 + (row8 & 7);
+        const int rt = row8 >> 3, rr = row8 & 7, g = rt * 16 + pass * 8 + rr;
         if (g >= G) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * 16 + (row8 & 7)]);
+        for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * 8 + rr]);
         const float base = top == -INFINITY ? 0.f : top;
         float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
           const int w = p * MT + rt;
-          const float f = ex2(s_m[w * 16 + (row8 & 7)] - base);
-          l += f * s_l[w * 16 + (row8 & 7)];
-          const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + (row8 & 7)) * S::kORow + c);
+          const float f = ex2(s_m[w * 8 + rr] - base);
+          l += f * s_l[w * 8 + rr];
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * S::kORow + c);
           acc[0] += f * v.x;
           acc[1] += f * v.y;
           acc[2] += f * v.z;
           acc[3] += f * v.w;
         }
-        if (tl.n_parts == 1) finish(g, c, top, l, acc);
+        if (pt.n_parts == 1) finish(pt, g, c, top, l, acc);
         else keep(place, g, c, top, l, acc);
       }
     }
-    if (tl.n_parts == 1) continue;
 
     // ---- joining: the last of a group of 16 parts to get here joins the group, the last group's joiner the groups ----
     // A release by one thread after the warps' meeting covers what all of them wrote.
-    auto is_last = [&](unsigned* count, int of) -> bool {
+    if (pt.n_parts > 1 && done < n_tiles) {
+      // (not the run's last part: counted now, looked at when the run is through)
+      consumer_sync();
+      if (!ok) return;
+      early = true;
+      if (tid == 0) s_part[2] = pt;
+      if (tid == 0) early_count = add_acq_rel(a.count + part_place(pt.i0, part / kGroup * kGroup));
+    }
+    if (done < n_tiles) continue;
+    // This part and the early one; of each its group of parts, then the groups. A count is of what precedes the own.
+#pragma unroll 1
+    for (int k = early ? 3 : 1; k >= 0; --k) {
+      const bool groups = !(k & 1);
+      const Part of = k >> 1 ? s_part[2] : pt;
+      const int g0 = groups ? 0 : ((int)blockIdx.x - of.i0) / kGroup * kGroup;
+      const int n_groups = (of.n_parts + kGroup - 1) / kGroup;
+      const int n = groups ? n_groups : min(kGroup, of.n_parts - g0), every = groups ? kGroup : 1;
+      if (of.n_parts == 1 || (groups && n_groups == 1)) continue;
+      unsigned* const count = a.count + (groups ? a.n_places : 0) + part_place(of.i0, g0);
       consumer_sync();
       if (ok && tid == 0) {
-        const bool last = add_acq_rel(count) == (unsigned)(of - 1);
+        const bool last = (k == 3 ? early_count : add_acq_rel(count)) == (unsigned)(n - 1);
         if (last) *count = 0u;  // ready for the next call
         *s_last = last;
       }
       consumer_sync();
-      return ok && *s_last;
-    };
-    // parts p0, p0 + step, .. (n of them): every thread joins 4 values of a row, kAtOnce parts in flight
-    auto join = [&](int p0, int step, int n, bool to_out) {
+      if (!ok) return;
+      if (!*s_last) {
+        if (!groups) --k;  // (another CTA joins this group, and sees to the groups)
+        continue;
+      }
+      // parts g0, g0 + every, .. (n of them): every thread joins 4 values of a row, kAtOnce parts in flight
       constexpr int kAtOnce = D == 128 ? 16 : 8;
       for (int x0 = warp * 32; x0 < G * kPerRow; x0 += kConsumers * 32) {
         const int x = min(x0 + lane, G * kPerRow - 1), g = x / kPerRow, c = (x - g * kPerRow) * 4;
@@ -834,51 +926,36 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           float2 ml[kAtOnce];
           float4 v[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            const int64_t from = (int64_t)part_place(tl.i0, p0 + min(b + k, n - 1) * step) * G + g;
-            ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + from);
-            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + c));
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int64_t from = (int64_t)part_place(of.i0, g0 + min(b + u, n - 1) * every) * G + g;
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + from);
+            v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + c));
           }
           float top = m;
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+          for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, ml[u].x);
           const float base = top == -INFINITY ? 0.f : top, f = ex2(m - base);
           l *= f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] *= f;
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k)
-            if (b + k < n) {
-              const float w = ex2(ml[k].x - base);
-              l += w * ml[k].y;
-              acc[0] += w * v[k].x;
-              acc[1] += w * v[k].y;
-              acc[2] += w * v[k].z;
-              acc[3] += w * v[k].w;
+          for (int u = 0; u < kAtOnce; ++u)
+            if (b + u < n) {
+              const float w = ex2(ml[u].x - base);
+              l += w * ml[u].y;
+              acc[0] += w * v[u].x;
+              acc[1] += w * v[u].y;
+              acc[2] += w * v[u].z;
+              acc[3] += w * v[u].w;
             }
           m = top;
         }
         __syncwarp();  // (a row's lanes, one warp, have read the first part, whose place the group's sum takes)
         if (x0 + lane != x) continue;
-        if (to_out) finish(g, c, m, l, acc);
-        else keep(part_place(tl.i0, p0), g, c, m, l, acc);
+        if (groups || n_groups == 1) finish(of, g, c, m, l, acc);
+        else keep(part_place(of.i0, g0), g, c, m, l, acc);
       }
-    };
-    const int g0 = part / kGroup * kGroup, in_group = min(kGroup, tl.n_parts - g0);
-    const int n_groups = (tl.n_parts + kGroup - 1) / kGroup;
-    if (in_group > 1) {
-      if (!is_last(a.count + part_place(tl.i0, g0), in_group)) {
-        if (!ok) return;
-        continue;
-      }
-      join(g0, 1, in_group, n_groups == 1);
     }
-    if (n_groups == 1) continue;
-    if (!is_last(a.count + a.n_places + part_place(tl.i0, 0), n_groups)) {
-      if (!ok) return;
-      continue;
-    }
-    join(0, kGroup, n_groups, true);
   }
 }
 
