@@ -359,6 +359,10 @@ class KvCache:
             raise CvrError(st, "cvr_kv_create failed (see stderr)")
         self._h = h
         self.config = config
+        self._row, self._q_row = config.kv_heads * config.head_dim, config.q_heads * config.head_dim
+        # (a decode step's calls are short: their entry points are looked up once)
+        self._tables, self._append, self._attend = (self._lib.cvr_kv_tables, self._lib.cvr_kv_append,
+                                                    self._lib.cvr_kv_attend)
 
     def _check(self, st: int) -> int:
         if st != 0:
@@ -369,20 +373,24 @@ class KvCache:
                n_free: int = 0, free_head: int = 0, pages: int = 0, free_head_out: int = 0, slots: int = 0,
                n_slots: int = 0) -> None:
         """cvr_kv_tables: block tables and slot maps from request lengths."""
-        self._check(self._lib.cvr_kv_tables(self._h, n_req, lens, new_lens, held, free_pages, n_free, free_head, table,
-                                            pages, free_head_out, slots, n_slots))
+        st = self._tables(self._h, n_req, lens, new_lens, held, free_pages, n_free, free_head, table, pages, free_head_out,
+                          slots, n_slots)
+        if st:
+            self._check(st)
 
     def append(self, n_tok: int, slots: int, k: int, v: int = 0, k_stride: int = 0, v_stride: int = 0) -> None:
         """cvr_kv_append: the new tokens' rows to their slots (strides of tokens in values, 0 = dense)."""
-        dense = self.config.kv_heads * self.config.head_dim
-        self._check(self._lib.cvr_kv_append(self._h, n_tok, slots, k, k_stride or dense, v, v_stride or dense))
+        st = self._append(self._h, n_tok, slots, k, k_stride or self._row, v, v_stride or self._row)
+        if st:
+            self._check(st)
 
     def attend(self, n_req: int, q: int, lens: int, table: int, scale: float, out: int, lse: int = 0,
                q_stride: int = 0, out_stride: int = 0) -> None:
         """cvr_kv_attend: one query token per request over its pages (strides of requests in values, 0 = dense)."""
-        dense = self.config.q_heads * self.config.head_dim
-        self._check(self._lib.cvr_kv_attend(self._h, n_req, q, q_stride or dense, lens, table, scale, out,
-                                            out_stride or dense, lse))
+        st = self._attend(self._h, n_req, q, q_stride or self._q_row, lens, table, scale, out, out_stride or self._q_row,
+                          lse)
+        if st:
+            self._check(st)
 
     def sync(self, check: bool = True) -> int:
         """cvr_kv_sync: waits for the stream; the status of the device-side checks."""

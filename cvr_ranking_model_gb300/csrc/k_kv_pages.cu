@@ -11,173 +11,252 @@ namespace {
 // Tables. With n_r = ceil(len_r / P), a request needs f_r = max(0, n_r - held_r) fresh pages, the free list's entries
 // from F_r = head + sum_{s<r} f_s on, and its new tokens take the slot map's entries from N_r = sum_{s<r} new_s on.
 //
-// One launch: every CTA scans all requests, 1024 at a time, and writes its own slice of each batch's table entries and
-// slots. A scan reads 12 bytes per request (from L2 in all CTAs but one); no CTA waits for another, and a slot's page
-// comes from the free list or the held entries, never from what this call writes.
-constexpr int kTabThreads = 512;
-constexpr int kTabPer = 2;                           // requests per thread and batch
-constexpr int kTabBatch = kTabThreads * kTabPer;     // 1024
-constexpr int kTabRun = 256;                         // consecutive items of one warp step, 8 per lane
+// One launch. Every CTA sums all requests (12 bytes each, from L2 in all CTAs but one) and so knows where its own slice
+// of the fresh entries and of the slots begins; it scans the slice's requests 512 at a time and writes. No CTA waits for
+// another: a slot's page comes from the free list or the held entries, never from what this call writes.
+constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
+constexpr int kTabRun = 256;  // consecutive items of a warp's step, 8 per lane, whose loads are in flight together
+
+// sums of fresh pages or new tokens; they stop at 2^31 - 1, above any list's length
+__device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); }
 
 struct TabReq {
-  int len, fresh, fresh_from, new_len, held;
+  int len, fresh, held;
+  int n_new;
 };
 
-// the last index i in [lo, hi] with start[i] <= x (start does not decrease, start[lo] <= x)
-__device__ __forceinline__ int last_at_most(const int64_t* start, int lo, int hi, int64_t x) {
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= x) lo = mid;
-    else hi = mid - 1;
+__device__ __forceinline__ TabReq tab_request(const KvTablesArgs& a, int r, int* bad) {
+  TabReq q = {0, 0, 0, 0};
+  if (r >= a.n_req) return q;
+  const int most = a.max_pages << a.page_log2;  // (at most 2^30)
+  const int len = __ldg(a.lens + r), nw = a.new_lens ? __ldg(a.new_lens + r) : 1, held = a.held ? __ldg(a.held + r) : 0;
+  q.len = min(max(len, 0), most);
+  q.n_new = a.new_lens ? min(max(nw, 0), q.len) : min(q.len, 1);
+  q.held = min(max(held, 0), a.max_pages);
+  if (q.len != len || (a.new_lens && q.n_new != nw) || q.held != held) *bad |= kKvErrLens;
+  q.fresh = max(0, ((q.len + (1 << a.page_log2) - 1) >> a.page_log2) - q.held);
+  return q;
+}
+
+// Exclusive sums of (f, w) over the block's threads, from (f_base, w_base); the totals behind the last in *_all.
+struct TabScan {
+  uint32_t f, w, f_all, w_all;
+};
+__device__ __forceinline__ TabScan tab_scan(uint32_t f, uint32_t w, uint32_t f_base, uint32_t w_base, uint32_t (*s_warp)[kTabWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t fi = f, wi = w;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, fi, d), v = __shfl_up_sync(0xffffffffu, wi, d);
+    if (lane >= d) {
+      fi = sat_add(fi, u);
+      wi = sat_add(wi, v);
+    }
   }
-  return lo;
+  __syncthreads();  // (the last scan's sums have been read)
+  if (lane == 31) {
+    s_warp[0][warp] = fi;
+    s_warp[1][warp] = wi;
+  }
+  __syncthreads();
+  // lane l < 16 takes warp l's sums; every warp scans them
+  uint32_t ft = lane < kTabWarps ? s_warp[0][lane] : 0, wt = lane < kTabWarps ? s_warp[1][lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kTabWarps; d <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, ft, d), v = __shfl_up_sync(0xffffffffu, wt, d);
+    if (lane >= d) {
+      ft = sat_add(ft, u);
+      wt = sat_add(wt, v);
+    }
+  }
+  const uint32_t fb = __shfl_sync(0xffffffffu, ft, max(warp - 1, 0)), wb = __shfl_sync(0xffffffffu, wt, max(warp - 1, 0));
+  TabScan r;
+  r.f_all = sat_add(f_base, __shfl_sync(0xffffffffu, ft, kTabWarps - 1));
+  r.w_all = sat_add(w_base, __shfl_sync(0xffffffffu, wt, kTabWarps - 1));
+  const uint32_t fx = __shfl_up_sync(0xffffffffu, fi, 1), wx = __shfl_up_sync(0xffffffffu, wi, 1);
+  r.f = sat_add(sat_add(f_base, warp ? fb : 0), lane ? fx : 0);
+  r.w = sat_add(sat_add(w_base, warp ? wb : 0), lane ? wx : 0);
+  return r;
+}
+
+// the last index i < n (at most 512) with start[i] <= x, found by a warp; start does not decrease and start[0] <= x
+__device__ __forceinline__ int warp_last_at_most(const uint32_t* start, int n, uint32_t x) {
+  const int lane = threadIdx.x & 31;
+  const int block = __popc(__ballot_sync(0xffffffffu, lane * 16 < n && start[min(lane * 16, n - 1)] <= x)) - 1;
+  const int i = block * 16 + (lane & 15);
+  return block * 16 + __popc(__ballot_sync(0xffffffffu, lane < 16 && i < n && start[min(i, n - 1)] <= x)) - 1;
 }
 
 __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesArgs a) {
-  __shared__ int s_held[kTabBatch], s_len[kTabBatch], s_new[kTabBatch];
-  __shared__ int64_t s_fresh_at[kTabBatch], s_new_at[kTabBatch];  // exclusive sums within the batch
-  __shared__ int64_t s_warp[2][kTabThreads / 32];
+  __shared__ uint32_t s_warp[2][kTabWarps];
+  __shared__ uint32_t s_run[2][kTabThreads];  // sums before each thread's run of requests
+  __shared__ uint32_t s_f[kTabThreads], s_w[kTabThreads];  // of the requests in hand: sums before each, held, first new
+  __shared__ int s_held[kTabThreads], s_first[kTabThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t cta = blockIdx.x, n_cta = gridDim.x;
+  const uint32_t cta = blockIdx.x, n_cta = gridDim.x;
   const int P = 1 << a.page_log2;
   int bad = 0;
   pdl_trigger();
   pdl_wait();
-  int64_t head = a.free_head ? *a.free_head : 0;
+  int head = a.free_head ? __ldg(a.free_head) : 0;
+  // ---- sums over every thread's run of requests (one request each for at most 512) ----
+  const int run = (a.n_req + kTabThreads - 1) / kTabThreads;
+  TabReq q = {0, 0, 0, 0};
+  uint32_t f = 0, w = 0;
+#pragma unroll 4
+  for (int i = 0; i < run; ++i) {
+    q = tab_request(a, tid * run + i, &bad);
+    f = sat_add(f, q.fresh);
+    w = sat_add(w, q.n_new);
+  }
+  const TabScan all = tab_scan(f, w, 0, 0, s_warp);
   if (head < 0 || head > a.n_free) {
     bad |= kKvErrLens;
     head = head < 0 ? 0 : a.n_free;
   }
-  int64_t fresh_base = head, new_base = 0;  // the free list's and slot map's positions at the batch's start
-  for (int r0 = 0; r0 < a.n_req; r0 += kTabBatch) {
-    const int n = min(kTabBatch, a.n_req - r0);
-    int64_t f[kTabPer], w[kTabPer], f_sum = 0, w_sum = 0;
-#pragma unroll
-    for (int i = 0; i < kTabPer; ++i) {
-      const int k = tid * kTabPer + i, r = r0 + k;
-      int len = 0, nw = 0, held = 0;
-      if (k < n) {
-        len = a.lens[r];
-        const int64_t most = (int64_t)a.max_pages << a.page_log2;
-        if (len < 0 || len > most) {
-          bad |= kKvErrLens;
-          len = len < 0 ? 0 : (int)most;
-        }
-        nw = a.new_lens ? a.new_lens[r] : min(len, 1);
-        if (nw < 0 || nw > len) {
-          bad |= kKvErrLens;
-          nw = nw < 0 ? 0 : len;
-        }
-        held = a.held ? a.held[r] : 0;
-        if (held < 0 || held > a.max_pages) {
-          bad |= kKvErrLens;
-          held = held < 0 ? 0 : a.max_pages;
-        }
-      }
-      s_len[k] = len;
-      s_new[k] = nw;
-      s_held[k] = held;
-      f[i] = max(0, ((len + P - 1) >> a.page_log2) - held);
-      w[i] = nw;
-      f_sum += f[i];
-      w_sum += w[i];
-    }
-    // exclusive sums over the batch's threads
-    int64_t f_in = f_sum, w_in = w_sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, f_in, d), v = __shfl_up_sync(0xffffffffu, w_in, d);
-      if (lane >= d) {
-        f_in += u;
-        w_in += v;
-      }
-    }
-    if (lane == 31) {
-      s_warp[0][warp] = f_in;
-      s_warp[1][warp] = w_in;
-    }
-    __syncthreads();
-    int64_t f_at = f_in - f_sum, w_at = w_in - w_sum, f_total = 0, w_total = 0;
-#pragma unroll
-    for (int i = 0; i < kTabThreads / 32; ++i) {
-      const int64_t u = s_warp[0][i], v = s_warp[1][i];
-      if (i < warp) {
-        f_at += u;
-        w_at += v;
-      }
-      f_total += u;
-      w_total += v;
-    }
-#pragma unroll
-    for (int i = 0; i < kTabPer; ++i) {
-      const int k = tid * kTabPer + i;
-      s_fresh_at[k] = f_at;
-      s_new_at[k] = w_at;
-      f_at += f[i];
-      w_at += w[i];
-    }
-    __syncthreads();
-    // the page in entry j of the batch's request k: held already, or taken from the free list; -1: none
-    auto page_of = [&](int k, int j) -> int {
-      const int held = s_held[k];
-      if (j < held) return a.table[(int64_t)(r0 + k) * a.max_pages + j];
-      const int64_t at = fresh_base + s_fresh_at[k] + (j - held);
-      if (at >= a.n_free) {
-        bad |= kKvErrPages;
-        return -1;
-      }
-      return a.free_pages[at];
-    };
-    // this CTA's slice of the batch's fresh entries, in runs that a warp takes
-    const int64_t warps = n_cta * (kTabThreads / 32), my = cta * (kTabThreads / 32) + warp;
-    for (int64_t at = my * kTabRun; at < f_total; at += warps * kTabRun) {
-      const int64_t end = min(at + kTabRun, f_total);
-      const int k0 = last_at_most(s_fresh_at, 0, n - 1, at), k1 = last_at_most(s_fresh_at, k0, n - 1, end - 1);
-#pragma unroll
-      for (int u = 0; u < kTabRun / 32; ++u) {
-        const int64_t x = at + u * 32 + lane;
-        if (x >= end) continue;
-        const int k = last_at_most(s_fresh_at, k0, k1, x), j = s_held[k] + (int)(x - s_fresh_at[k]);
-        int page = page_of(k, j);
-        if (page >= a.n_pages || (page < 0 && fresh_base + x < a.n_free)) {
-          bad |= kKvErrPage;
-          page = -1;
-        }
-        a.table[(int64_t)(r0 + k) * a.max_pages + j] = page;
-      }
-    }
-    // ... and of its slots
-    const int64_t w_end = min(w_total, a.n_slots - new_base);
-    if (w_end < w_total && a.slots) bad |= kKvErrSlots;
-    for (int64_t at = my * kTabRun; at < w_end; at += warps * kTabRun) {
-      const int64_t end = min(at + kTabRun, w_end);
-      const int k0 = last_at_most(s_new_at, 0, n - 1, at), k1 = last_at_most(s_new_at, k0, n - 1, end - 1);
-#pragma unroll
-      for (int u = 0; u < kTabRun / 32; ++u) {
-        const int64_t x = at + u * 32 + lane;
-        if (x >= end) continue;
-        const int k = last_at_most(s_new_at, k0, k1, x);
-        const int pos = s_len[k] - s_new[k] + (int)(x - s_new_at[k]);
-        const int page = page_of(k, pos >> a.page_log2);
-        const bool ok = page >= 0 && page < a.n_pages;
-        if (!ok) bad |= kKvErrPage;
-        a.slots[new_base + x] = ok ? ((int64_t)page << a.page_log2) + (pos & (P - 1)) : -1;
-      }
-    }
-    if (a.pages)
-      for (int64_t k = cta * kTabThreads + tid; k < n; k += n_cta * kTabThreads) {
-        const int64_t need = (s_len[k] + P - 1) >> a.page_log2;
-        const int64_t left = a.n_free - (fresh_base + s_fresh_at[k]);  // pages of the list from this request on
-        const int64_t got = min(max(need - s_held[k], (int64_t)0), max(left, (int64_t)0));
-        a.pages[r0 + k] = s_held[k] + (int)got;
-      }
-    fresh_base += f_total;
-    new_base += w_total;
-    __syncthreads();  // the batch's arrays have been read
+  const uint32_t left = a.n_free - head;  // pages in the free list
+  if (all.f_all > left) bad |= kKvErrPages;
+  const uint32_t n_slots = (uint32_t)min((int64_t)all.w_all, a.n_slots);
+  if (a.slots && n_slots < all.w_all) bad |= kKvErrSlots;
+  auto in_hand = [&](const TabReq& x, uint32_t f_at, uint32_t w_at) {
+    s_f[tid] = f_at;
+    s_w[tid] = w_at;
+    s_held[tid] = x.held;
+    s_first[tid] = x.len - x.n_new;
+  };
+  if (run == 1) {
+    in_hand(q, all.f, all.w);
+  } else {
+    s_run[0][tid] = all.f;
+    s_run[1][tid] = all.w;
   }
-  if (fresh_base > a.n_free) bad |= kKvErrPages;
-  for (int64_t x = new_base + cta * kTabThreads + tid; x < a.n_slots; x += n_cta * kTabThreads) a.slots[x] = -1;
-  if (cta == 0 && tid == 0 && a.free_head_out) *a.free_head_out = (int)min(fresh_base, (int64_t)a.n_free);
+  __syncthreads();
+
+  // a page id as it is written, -1 for none (kNoPage: the list has ended, which is reported above)
+  constexpr int kNoPage = INT32_MIN;
+  auto checked = [&](int page) {
+    if ((unsigned)page < (unsigned)a.n_pages) return page;
+    if (page != kNoPage) bad |= kKvErrPage;
+    return -1;
+  };
+  // Kinds of items: 0 fresh table entries, 1 slots. With all requests in hand half of the warps see to each, else all
+  // to one after the other.
+  const int n_warps = run == 1 ? kTabWarps / 2 : kTabWarps, my_warp = warp % n_warps;
+#pragma unroll 1
+  for (int kind = warp / n_warps; kind < 2; kind += run == 1 ? 2 : 1) {
+    const uint32_t total = kind ? n_slots : all.f_all;
+    const uint32_t slice = (total / n_cta + kTabRun) / kTabRun * kTabRun;
+    const uint32_t x0 = min((uint64_t)cta * slice, (uint64_t)total), x1 = min((uint64_t)x0 + slice, (uint64_t)total);
+    if (x0 >= x1) continue;
+    int r0 = 0;  // the first request in hand
+    uint32_t f_at = 0, w_at = 0;
+    if (run > 1) {
+      const int k = warp_last_at_most(s_run[kind], kTabThreads, x0);
+      r0 = k * run;
+      f_at = s_run[0][k];
+      w_at = s_run[1][k];
+    }
+    uint32_t x = x0;
+    while (x < x1 && r0 < a.n_req) {
+      uint32_t upto = x1;  // items of the requests in hand
+      int n = min(kTabThreads, a.n_req - r0);
+      if (run > 1) {
+        int ignored = 0;
+        const TabReq mine = tab_request(a, r0 + tid, &ignored);
+        const TabScan at = tab_scan(mine.fresh, mine.n_new, f_at, w_at, s_warp);
+        in_hand(mine, at.f, at.w);
+        __syncthreads();
+        f_at = at.f_all;
+        w_at = at.w_all;
+        upto = min(x1, kind ? w_at : f_at);
+      }
+      const uint32_t* s_at = kind ? s_w : s_f;
+      for (uint32_t b = x + my_warp * kTabRun; b < upto; b += n_warps * kTabRun) {
+        const uint32_t e = min(b + kTabRun, upto);
+        constexpr int U = kTabRun / 32;
+        const int k0 = warp_last_at_most(s_at, n, b), k1 = warp_last_at_most(s_at, n, e - 1);
+        int page[U], where[U], of[U];
+        if (kind == 1 && k0 == k1 && a.n_free > 0) {
+          // slots of one request, all in fresh pages: a quarter of the general case's work per slot
+          const int pos0 = s_first[k0] + (int)(b - s_w[k0]);
+          if (pos0 >> a.page_log2 >= s_held[k0]) {
+            const uint32_t at0 = (uint32_t)head + min(s_f[k0], left) - s_held[k0];  // (page j is at at0 + j: below 2^32)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              page[u] = __ldg(a.free_pages + min(at0 + ((pos0 + u * 32 + lane) >> a.page_log2), (uint32_t)a.n_free - 1));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint32_t y = b + u * 32 + lane;
+              const int pos = pos0 + u * 32 + lane;
+              if (y >= e) continue;
+              const bool none = at0 + (pos >> a.page_log2) >= (uint32_t)a.n_free;
+              const bool good = !none && (unsigned)page[u] < (unsigned)a.n_pages;
+              if (!none && !good) bad |= kKvErrPage;
+              a.slots[y] = good ? ((int64_t)page[u] << a.page_log2) + (pos & (P - 1)) : -1;
+            }
+            continue;
+          }
+        }
+        // the items' requests, by halving steps that the 8 items of a lane take together
+#pragma unroll
+        for (int u = 0; u < U; ++u) of[u] = k0;
+        for (int step = k1 > k0 ? 1 << (31 - __clz(k1 - k0)) : 0; step > 0; step >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int to = min(of[u] + step, k1);  // (past the last: the last itself, which holds if it is reached at all)
+            const uint32_t starts = s_at[to];
+            of[u] = starts <= b + u * 32 + lane ? to : of[u];
+          }
+        // one load per item, from the free list or of a held entry; without branches all are in flight together
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t y = min(b + u * 32 + lane, e - 1);
+          const int k = of[u], held = s_held[k];
+          int j;
+          int64_t at;
+          if (kind == 0) {
+            j = where[u] = held + (int)(y - s_f[k]);
+            at = (int64_t)head + y;
+          } else {
+            const int pos = s_first[k] + (int)(y - s_w[k]);
+            j = pos >> a.page_log2;
+            where[u] = pos & (P - 1);
+            at = (int64_t)head + s_f[k] + (j - held);
+          }
+          const bool fresh = kind == 0 || j >= held, none = fresh && at >= a.n_free;
+          const int32_t* from = fresh && !none ? a.free_pages + at : a.table + (int64_t)(r0 + k) * a.max_pages + min(j, a.max_pages - 1);
+          page[u] = max(*from, -1);
+          if (none) page[u] = kNoPage;
+        }
+#pragma unroll
+        for (int u = 0; u < kTabRun / 32; ++u) {
+          const uint32_t y = b + u * 32 + lane;
+          if (y >= e) continue;
+          const int p = checked(page[u]);
+          if (kind == 0) a.table[(int64_t)(r0 + of[u]) * a.max_pages + where[u]] = p;
+          else a.slots[y] = p < 0 ? -1 : ((int64_t)p << a.page_log2) + where[u];
+        }
+      }
+      x = upto;
+      r0 += kTabThreads;
+      if (run > 1) __syncthreads();  // the requests in hand have been read
+    }
+  }
+  // ---- what each request holds now: thread t's run is written by CTA t mod n_cta ----
+  if (a.pages && tid % n_cta == cta) {
+    uint32_t at = all.f;
+    for (int i = 0; i < run; ++i) {
+      const int r = tid * run + i;
+      if (r >= a.n_req) break;
+      int ignored = 0;
+      const TabReq x = run == 1 ? q : tab_request(a, r, &ignored);
+      a.pages[r] = x.held + (int)min((uint32_t)x.fresh, at < left ? left - at : 0);
+      at = sat_add(at, x.fresh);
+    }
+  }
+  if (a.slots)
+    for (int64_t y = (int64_t)n_slots + cta * kTabThreads + tid; y < a.n_slots; y += n_cta * kTabThreads) a.slots[y] = -1;
+  if (cta == 0 && tid == 0 && a.free_head_out) *a.free_head_out = head + (int)min(all.f_all, left);
   if (bad) atomicOr(a.err, bad);
 }
 
@@ -259,10 +338,11 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
 }  // namespace
 
 cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s) {
-  // one CTA per 4096 items that the call may write, at most one per SM
-  const int64_t entries = (int64_t)a.n_req * a.max_pages;
-  const int64_t items = a.n_slots + (entries < a.n_free ? entries : a.n_free);
-  const int64_t want = 1 + items / 4096;
+  // one CTA per 2048 items, at most one per SM (each sums all requests: two per SM were no faster). How many fresh entries there
+  // are only the device knows: with a slot map about one per page of new tokens, else at most what the list holds.
+  const int64_t entries = (int64_t)a.n_req * a.max_pages < a.n_free ? (int64_t)a.n_req * a.max_pages : a.n_free;
+  const int64_t per_slot = a.n_req + (a.n_slots >> a.page_log2);
+  const int64_t want = 1 + (a.n_slots + (a.slots && per_slot < entries ? per_slot : entries)) / 2048;
   return launch_kernel(kv_tables_kernel, dim3((unsigned)(want < num_sms ? want : num_sms)), dim3(kTabThreads), 0, s, true, a);
 }
 

@@ -338,7 +338,8 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
  *   pages     [n_req] int32 entries that hold pages afterwards (pass it as `held` of the next step); NULL: not written
  *   free_head_out int32, *free_head plus the pages taken; NULL: not written. `pages` and `free_head_out` must be
  *             other arrays than `held` and `free_head`: a call leaves its inputs as they were
- *   slots     [n_slots] int64: the slots of the new tokens, requests in order, tokens in order; -1 behind the last.
+ *   slots     [n_slots] int64 (n_slots < 2^31 - 1): the slots of the new tokens, requests in order, tokens in order;
+ *             -1 behind the last.
  *             NULL with n_slots = 0: none wanted
  * Errors at cvr_kv_sync: CVR_E_INPUT for a length or held count out of range (used clamped) or more new tokens than
  * n_slots (the rest is dropped); CVR_E_PAGES when the free list ends (the entries and slots without a page are -1);
