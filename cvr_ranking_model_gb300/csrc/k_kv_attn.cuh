@@ -49,7 +49,7 @@ struct Shape {
   static constexpr int kRow = D * (I8 ? 1 : 2);                 // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 ? 3 : 2) : 2;
+  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && I8 ? 3 : 2) : 2;
   static constexpr int kUnitMost = kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       };
       int P = s_start[1], r = 0, h = 0, t = 0, n_t = 1, t0 = 0, len = 0, lo = 0;  // P: tiles per head before request r
       int e0 = 0, ids = 0, more_ids = 0;  // entries e0 + lane and e0 + 32 + lane of the request's table row
+      int ids0 = 0, more0 = 0;            // the same from the request's first entry on, for its next head
       auto enter = [&]() {  // the request that was looked ahead to
         r = n_r;
         len = n_len;
@@ -338,15 +339,18 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       e0 = ((t0 + t) * TK) >> a.page_log2;  // (the run may begin anywhere in its request)
       ids = entries(r, e0);
       more_ids = entries(r, e0 + 32);
+      ids0 = n_ids;
+      more0 = entries(r, first_entry(len) + 32);
       bool ok = true;
-      const uint64_t box_bytes = (uint64_t)br * (S::kRow + (I8 ? 4 : 0));
+      const uint32_t box_bytes = br * (S::kRow + (I8 ? 4 : 0)), tile_bytes = TK * (S::kRow + (I8 ? 4 : 0));
+      const bool long_pages = a.page_log2 > log2_br;  // several tiles per page, one box per tile
       for (int at = begin; at < end && ok;) {
         // ---- a part: its query rows and description, then its tiles ----
         const int n = min(n_t - t, end - at), b = parts & 1;
         ok = wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
         if (!ok) break;
         if (lane == 0) {
-          const int fb = P * H + h * n_t;
+          const unsigned fb = P * H + h * n_t;
           Part pt;
           pt.r = r;
           pt.h = h;
@@ -354,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           pt.n_tiles = n;
           pt.lo = lo;
           pt.len = len;
-          pt.i0 = fb / per;
-          pt.n_parts = (fb + n_t - 1) / per - pt.i0 + 1;
+          pt.i0 = fb / (unsigned)per;
+          pt.n_parts = (fb + n_t - 1) / (unsigned)per - pt.i0 + 1;
           s_part[b] = pt;
           mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
         }
@@ -372,21 +376,26 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             more_ids = entries(r, e0 + 32);
           }
           // in lane b: box b of the tile, wanted if any of its tokens is seen
-          const int from = k0 + (lane << log2_br), row = from & ((1 << a.page_log2) - 1);
-          const bool need = lane < n_box_max && from < len && from + br > lo;
-          int page = __shfl_sync(0xffffffffu, ids, ((from >> a.page_log2) - e0) & 31);
-          if (need && (unsigned)page >= (unsigned)a.n_pages) {
+          const int row = long_pages ? k0 & ((1 << a.page_log2) - 1) : 0;
+          int page = __shfl_sync(0xffffffffu, ids, ((k0 >> a.page_log2) - e0 + (long_pages ? 0 : lane)) & 31);
+          unsigned want = n_box_max == 32 ? 0xffffffffu : (1u << n_box_max) - 1;
+          uint32_t bytes = tile_bytes;
+          if (k0 < lo || k0 + TK > len) {
+            const int from = k0 + (lane << log2_br);
+            want &= __ballot_sync(0xffffffffu, from < len && from + br > lo);
+            bytes = __popc(want) * box_bytes;
+          }
+          if ((want >> lane & 1) && (unsigned)page >= (unsigned)a.n_pages) {
             atomicOr(a.err, kKvErrPage);
             page = 0;
           }
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need)) * (uint32_t)box_bytes;
 #pragma unroll 1
           for (int w = 0; w < (two ? 2 : 1); ++w) {
             ok = wait_warp(empty + slot, phase ^ 1, abort_flag, a.err);
             if (!ok) break;
             if (lane == 0) mbar_expect_tx(full + slot, bytes);
             __syncwarp();
-            if (need) {
+            if (want >> lane & 1) {
               tma_load_5d(sm + slot * S::kUnit + (lane << log2_br) * S::kRow, w ? &tm_v : &tm_k, full + slot, 0, row, 0, h, page);
               if (I8)
                 bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
@@ -403,16 +412,16 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         at += n;
         if (at >= end) break;
         t = 0;
-        if (++h < H) {
-          ids = entries(r, first_entry(len));
-        } else {
+        if (++h == H) {
           h = 0;
           P += n_t;
-          ids = n_ids;
           enter();
+          ids0 = n_ids;
+          more0 = entries(r, first_entry(len) + 32);
         }
         e0 = first_entry(len);
-        more_ids = entries(r, e0 + 32);
+        ids = ids0;
+        more_ids = more0;
       }
     }
     // requests that see nothing, shared out over the grid
