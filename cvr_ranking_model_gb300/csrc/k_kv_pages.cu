@@ -15,7 +15,10 @@ namespace {
 // of the fresh entries and of the slots begins; it scans the slice's requests 512 at a time and writes. No CTA waits for
 // another: a slot's page comes from the free list or the held entries, never from what this call writes.
 constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
-constexpr int kTabRun = 256;  // consecutive items of a warp's step, 8 per lane, whose loads are in flight together
+// Consecutive items of a warp's step, whose loads are in flight together: a call of one CTA is bound by the latency of its
+// few steps (64 requests, a token each: 3.6 us with 128, 4.6 us with 256), a longer one by their number (5.5 million slots:
+// 28.5 us with 128, 23.2 us with 256).
+constexpr int kTabRunShort = 128, kTabRunLong = 256;
 
 // sums of fresh pages or new tokens; they stop at 2^31 - 1, above any list's length
 __device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); }
@@ -79,19 +82,23 @@ __device__ __forceinline__ TabScan tab_scan(uint32_t f, uint32_t w, uint32_t f_b
   return r;
 }
 
-// the last index i < n (at most 512) with start[i] <= x, found by a warp; start does not decrease and start[0] <= x
+// the last index i < n (at most kTabThreads) with start[i] <= x, found by a warp; start does not decrease, start[0] <= x
 __device__ __forceinline__ int warp_last_at_most(const uint32_t* start, int n, uint32_t x) {
+  constexpr int kStep = kTabThreads / 32;
   const int lane = threadIdx.x & 31;
-  const int block = __popc(__ballot_sync(0xffffffffu, lane * 16 < n && start[min(lane * 16, n - 1)] <= x)) - 1;
-  const int i = block * 16 + (lane & 15);
-  return block * 16 + __popc(__ballot_sync(0xffffffffu, lane < 16 && i < n && start[min(i, n - 1)] <= x)) - 1;
+  const int block = __popc(__ballot_sync(0xffffffffu, lane * kStep < n && start[min(lane * kStep, n - 1)] <= x)) - 1;
+  const int i = block * kStep + lane % kStep;
+  return block * kStep + __popc(__ballot_sync(0xffffffffu, lane < kStep && i < n && start[min(i, n - 1)] <= x)) - 1;
 }
 
+template <int kTabRun>
 __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesArgs a) {
   __shared__ uint32_t s_warp[2][kTabWarps];
   __shared__ uint32_t s_run[2][kTabThreads];  // sums before each thread's run of requests
-  __shared__ uint32_t s_f[kTabThreads], s_w[kTabThreads];  // of the requests in hand: sums before each, held, first new
-  __shared__ int s_held[kTabThreads], s_first[kTabThreads];
+  // of the requests in hand: the sums before each, its held entries, and with w and f those sums
+  __shared__ uint32_t s_f[kTabThreads], s_w[kTabThreads];
+  __shared__ int s_held[kTabThreads], s_pos[kTabThreads];  // s_pos: first new token - w, so that item y is token s_pos + y
+  __shared__ uint32_t s_at[kTabThreads];                   // head + f - held: entry j's page is s_at + j of the free list
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t cta = blockIdx.x, n_cta = gridDim.x;
   const int P = 1 << a.page_log2;
@@ -122,7 +129,8 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
     s_f[tid] = f_at;
     s_w[tid] = w_at;
     s_held[tid] = x.held;
-    s_first[tid] = x.len - x.n_new;
+    s_pos[tid] = x.len - x.n_new - (int)w_at;
+    s_at[tid] = (uint32_t)head + min(f_at, left) - x.held;  // (with j up to 2^27: below 2^32)
   };
   if (run == 1) {
     in_hand(q, all.f, all.w);
@@ -170,71 +178,63 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
         w_at = at.w_all;
         upto = min(x1, kind ? w_at : f_at);
       }
-      const uint32_t* s_at = kind ? s_w : s_f;
+      const uint32_t* starts = kind ? s_w : s_f;
       for (uint32_t b = x + my_warp * kTabRun; b < upto; b += n_warps * kTabRun) {
-        const uint32_t e = min(b + kTabRun, upto);
         constexpr int U = kTabRun / 32;
-        const int k0 = warp_last_at_most(s_at, n, b), k1 = warp_last_at_most(s_at, n, e - 1);
-        int page[U], where[U], of[U];
-        if (kind == 1 && k0 == k1 && a.n_free > 0) {
-          // slots of one request, all in fresh pages: a quarter of the general case's work per slot
-          const int pos0 = s_first[k0] + (int)(b - s_w[k0]);
-          if (pos0 >> a.page_log2 >= s_held[k0]) {
-            const uint32_t at0 = (uint32_t)head + min(s_f[k0], left) - s_held[k0];  // (page j is at at0 + j: below 2^32)
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-              page[u] = __ldg(a.free_pages + min(at0 + ((pos0 + u * 32 + lane) >> a.page_log2), (uint32_t)a.n_free - 1));
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const uint32_t y = b + u * 32 + lane;
-              const int pos = pos0 + u * 32 + lane;
-              if (y >= e) continue;
-              const bool none = at0 + (pos >> a.page_log2) >= (uint32_t)a.n_free;
-              const bool good = !none && (unsigned)page[u] < (unsigned)a.n_pages;
-              if (!none && !good) bad |= kKvErrPage;
-              a.slots[y] = good ? ((int64_t)page[u] << a.page_log2) + (pos & (P - 1)) : -1;
-            }
-            continue;
-          }
-        }
-        // the items' requests, by halving steps that the 8 items of a lane take together
+        const uint32_t e = min(b + kTabRun, upto);
+        const int k0 = warp_last_at_most(starts, n, b), k1 = warp_last_at_most(starts, n, e - 1);
+        // the items' requests, by halving steps that the items of a lane take together
+        int of[U], page[U], where[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) of[u] = k0;
         for (int step = k1 > k0 ? 1 << (31 - __clz(k1 - k0)) : 0; step > 0; step >>= 1)
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int to = min(of[u] + step, k1);  // (past the last: the last itself, which holds if it is reached at all)
-            const uint32_t starts = s_at[to];
-            of[u] = starts <= b + u * 32 + lane ? to : of[u];
+            const uint32_t start = starts[to];
+            of[u] = start <= b + u * 32 + lane ? to : of[u];
           }
-        // one load per item, from the free list or of a held entry; without branches all are in flight together
+        // where each item goes, and its page's place in the free list
+        uint32_t at[U];
+        bool held = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t y = min(b + u * 32 + lane, e - 1);
-          const int k = of[u], held = s_held[k];
-          int j;
-          int64_t at;
+          const int k = of[u];
           if (kind == 0) {
-            j = where[u] = held + (int)(y - s_f[k]);
-            at = (int64_t)head + y;
+            where[u] = s_held[k] + (int)(y - s_f[k]);
+            at[u] = (uint32_t)head + y;
           } else {
-            const int pos = s_first[k] + (int)(y - s_w[k]);
-            j = pos >> a.page_log2;
-            where[u] = pos & (P - 1);
-            at = (int64_t)head + s_f[k] + (j - held);
+            where[u] = s_pos[k] + (int)y;
+            const int j = where[u] >> a.page_log2;
+            at[u] = s_at[k] + j;
+            held |= j < s_held[k];
           }
-          const bool fresh = kind == 0 || j >= held, none = fresh && at >= a.n_free;
-          const int32_t* from = fresh && !none ? a.free_pages + at : a.table + (int64_t)(r0 + k) * a.max_pages + min(j, a.max_pages - 1);
-          page[u] = max(*from, -1);
-          if (none) page[u] = kNoPage;
+        }
+        if (__any_sync(0xffffffffu, held) || a.n_free == 0) {
+          // (some in held entries, or no list: one load each, from either; without branches all are in flight together)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int k = of[u], j = kind ? where[u] >> a.page_log2 : where[u];
+            const bool fresh = kind == 0 || j >= s_held[k], none = fresh && at[u] >= (uint32_t)a.n_free;
+            const int32_t* from = fresh && !none ? a.free_pages + at[u] : a.table + (int64_t)(r0 + k) * a.max_pages + min(j, a.max_pages - 1);
+            page[u] = max(*from, -1);
+            if (none) page[u] = kNoPage;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            page[u] = max(__ldg(a.free_pages + min(at[u], (uint32_t)a.n_free - 1)), -1);
+            if (at[u] >= (uint32_t)a.n_free) page[u] = kNoPage;
+          }
         }
 #pragma unroll
-        for (int u = 0; u < kTabRun / 32; ++u) {
+        for (int u = 0; u < U; ++u) {
           const uint32_t y = b + u * 32 + lane;
           if (y >= e) continue;
           const int p = checked(page[u]);
           if (kind == 0) a.table[(int64_t)(r0 + of[u]) * a.max_pages + where[u]] = p;
-          else a.slots[y] = p < 0 ? -1 : ((int64_t)p << a.page_log2) + where[u];
+          else a.slots[y] = p < 0 ? -1 : ((int64_t)p << a.page_log2) + (where[u] & (P - 1));
         }
       }
       x = upto;
@@ -356,7 +356,7 @@ cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s)
   const int64_t entries = (int64_t)a.n_req * a.max_pages < a.n_free ? (int64_t)a.n_req * a.max_pages : a.n_free;
   const int64_t per_slot = a.n_req + (a.n_slots >> a.page_log2);
   const int64_t want = 1 + (a.n_slots + (a.slots && per_slot < entries ? per_slot : entries)) / 2048;
-  return launch_kernel(kv_tables_kernel, dim3((unsigned)(want < num_sms ? want : num_sms)), dim3(kTabThreads), 0, s, true, a);
+  return launch_kernel(want == 1 ? kv_tables_kernel<kTabRunShort> : kv_tables_kernel<kTabRunLong>, dim3((unsigned)(want < num_sms ? want : num_sms)), dim3(kTabThreads), 0, s, true, a);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, bool int8, int num_sms, cudaStream_t s) {
