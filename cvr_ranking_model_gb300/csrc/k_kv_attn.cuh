@@ -139,10 +139,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 // two of the four bytes of x, biased signed values (q ^ 0x80 = q + 128), as an fp16 pair: SEL picks the bytes (0x4140: 0 and
-// 1, 0x4342: 2 and 3, 0x4240: 0 and 2, 0x4341: 1 and 3); the bits 0x64.. are 1024 + (q + 128). `k64` holds 0x64646464.
+// 1, 0x4342: 2 and 3, 0x4240: 0 and 2, 0x4341: 1 and 3); the bits 0x64.. are 1024 + (q + 128).
 template <int SEL>
-__device__ __forceinline__ uint32_t i8_pair(uint32_t x, uint32_t k64) {
-  const uint32_t u = __byte_perm(x, k64, SEL);
+__device__ __forceinline__ uint32_t i8_pair(uint32_t x) {
+  const uint32_t u = __byte_perm(x, 0x64646464u, SEL);
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
@@ -464,8 +464,6 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
   constexpr uint32_t kOnes = std::is_same<M, __half>::value ? 0x3c003c00u : 0x3f803f80u;
-  uint32_t k64 = 0;
-  if (I8) asm volatile("mov.b32 %0, 0x64646464;" : "=r"(k64));  // (kept in a register)
   uint32_t meets = 0;
   bool ok = true;
   auto consumer_sync = [&]() {  // a bounded barrier of the four warps
@@ -619,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               for (int e = 0; e < 4; ++e) f[e] ^= 0x80808080u;
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
-                const uint32_t e0 = i8_pair<0x4140>(f[2 * n], k64), e1 = i8_pair<0x4342>(f[2 * n], k64);
-                const uint32_t d0 = i8_pair<0x4140>(f[2 * n + 1], k64), d1 = i8_pair<0x4342>(f[2 * n + 1], k64);
+                const uint32_t e0 = i8_pair<0x4140>(f[2 * n]), e1 = i8_pair<0x4342>(f[2 * n]);
+                const uint32_t d0 = i8_pair<0x4140>(f[2 * n + 1]), d1 = i8_pair<0x4342>(f[2 * n + 1]);
                 if (k == 0) mma16816<M, true>(s[b][n], qf[k], e0, e1);
                 else mma16816<M>(s[b][n], qf[k], e0, e1);
                 mma16816<M>(s[b][n], qf[k + 1], d0, d1);
@@ -777,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               for (int e = 0; e < 4; ++e) f[e] ^= 0x80808080u;
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t e0 = i8_pair<0x4240>(f[2 * e], k64), e1 = i8_pair<0x4240>(f[2 * e + 1], k64);
-                const uint32_t d0 = i8_pair<0x4341>(f[2 * e], k64), d1 = i8_pair<0x4341>(f[2 * e + 1], k64);
+                const uint32_t e0 = i8_pair<0x4240>(f[2 * e]), e1 = i8_pair<0x4240>(f[2 * e + 1]);
+                const uint32_t d0 = i8_pair<0x4341>(f[2 * e]), d1 = i8_pair<0x4341>(f[2 * e + 1]);
                 mma16816<M>(o[4 * c + 2 * e], hi, e0, e1);
                 mma16816<M>(o[4 * c + 2 * e + 1], hi, d0, d1);
                 if (!R8) {

@@ -85,8 +85,45 @@ def test_many_short_requests():
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 40.0])
-def test_scales(scale):
-    check(Cache([1, 50, 333], 2, 64, 16, "bf16", seed=8), 4, scale=scale)
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("bf16", "i8"), ("f16", "i8")])
+def test_scales(scale, dtype, cache):
+    check(Cache([1, 50, 333], 2, 64, 16, dtype, cache, seed=8), 4, scale=scale)
+
+
+def test_twelve_thousand_requests_most_of_them_empty():
+    check(Cache([3 if i % 7 == 0 else 40 if i == 11999 else 0 for i in range(12000)], 1, 32, 8, "f16", seed=18), 1)
+
+
+def test_keys_and_values_laid_out_differently():
+    """Keys page by page and head by head, values token by token; then both in one tensor, page by page."""
+    import torch
+    c = Cache([300, 5, 64], 2, 64, 16, "bf16", seed=19)
+    v = torch.empty((c.n_pages, 16, 2, 64), dtype=c.v.dtype, device="cuda").permute(0, 2, 1, 3)
+    v.copy_(c.v)
+    c.v = v
+    check(c, 8)
+    both = torch.empty((c.n_pages, 2, 2, 16, 64), dtype=c.v.dtype, device="cuda")
+    both[:, 0], both[:, 1] = c.k, c.v
+    c.k, c.v = both[:, 0], both[:, 1]
+    check(c, 8)
+
+
+def test_a_pool_of_one_page_and_one_head():
+    """Strides of dimensions of one row are not used, whatever they are."""
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    c = Cache([13], 1, 32, 16, "f16", seed=20, spare=0)
+    cfg = cvr.make_kv_config(3, 1, 32, 16, 1, 1, c.max_pages, cvr.DTYPE_F16, k=c.k.data_ptr(), k_strides=(0, -7, 32), v=c.v.data_ptr(),
+                             v_strides=(-1, 0, 32))
+    check(c, 3, handle=cvr.KvCache(cfg))
+
+
+def test_row_scales_of_either_sign():
+    import torch
+    c = Cache([100, 7], 2, 32, 16, "bf16", "i8", seed=21)
+    for s in (c.k_scale, c.v_scale):
+        s.mul_(torch.where(torch.rand(s.shape, generator=c.gen, device="cuda") < 0.5, -1.0, 1.0))
+    check(c, 4)
 
 
 @pytest.mark.parametrize("cache", ["same", "i8"])

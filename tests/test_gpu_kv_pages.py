@@ -37,7 +37,8 @@ def run_tables(lens, new, held, free, head, table, page, n_slots, n_pages, max_p
 
 
 @pytest.mark.parametrize("n,max_len,page", [(1, 1, 8), (1, 5000, 16), (3, 40, 8), (64, 300, 16), (700, 90, 32), (1023, 20, 8), (1024, 20, 8),
-                                            (1025, 20, 8), (5000, 17, 256), (2500, 400, 64)])
+                                            (1025, 20, 8), (5000, 17, 256), (2500, 400, 64), (511, 700, 8), (512, 9, 8), (513, 9, 8),
+                                            (20000, 30, 8), (2, 150000, 32)])
 @pytest.mark.parametrize("step", ["decode", "fill", "mixed"])
 def test_tables(n, max_len, page, step):
     rng = random.Random(n * 1000 + page)
@@ -171,6 +172,38 @@ def test_append(dtype, cache, dim, layout, heads, n, page, shared):
     if layout == "gaps":  # the values between rows
         base = pools["k"]._base
         assert not bool(base[..., dim:].any()) and not bool(base[:, :, page].any())
+
+
+def test_append_of_more_tokens_than_one_round_of_indices():
+    import torch
+    n, page = 2 ** 18 + 77, 64
+    c = Cache([0], 1, 32, page, "bf16", shared=True, spare=n // page + 2)
+    c.k.zero_()
+    rows = torch.randn((n, 1, 32), device="cuda").to(torch.bfloat16)
+    slots = torch.randperm(c.n_pages * page, device="cuda")[:n]
+    want = torch.zeros_like(c.k)
+    want[slots // page, :, slots % page] = rows
+    kv = c.handle(1)
+    kv.append(n, slots.data_ptr(), rows.data_ptr())
+    kv.sync()
+    assert torch.equal(c.k, want)
+
+
+def test_append_of_tiny_rows_to_eight_bits():
+    """Rows of the smallest normal and subnormal values: their codes and scales like any others'."""
+    import torch
+    c = Cache([0], 1, 64, 16, "bf16", "i8", shared=True)
+    rows = torch.randn((6, 1, 64), device="cuda").double() * torch.tensor([2.0 ** -126, 2.0 ** -128, 2.0 ** -132, 2.0 ** -60, 2.0 ** -61, 2.0 ** 100],
+                                                                           dtype=torch.float64, device="cuda")[:, None, None]
+    rows = rows.to(torch.bfloat16)
+    slots = torch.arange(6, device="cuda")
+    kv = c.handle(1)
+    kv.append(6, slots.data_ptr(), rows.data_ptr())
+    kv.sync()
+    code, step = quantised(rows)
+    assert torch.equal(c.k[0, :, :6].transpose(0, 1).double(), code)
+    # the scale's division by 127: half a step of fp32, or of its smallest subnormal
+    assert bool(((c.k_scale[0, :, :6].T.double() - step).abs() <= step * 2.0 ** -24 + 2.0 ** -150).all())
 
 
 def test_append_reports_slots_outside_the_pool():
