@@ -132,7 +132,9 @@ bool encode_pool(CUtensorMap* m, void* base, const int64_t* stride, const cvr_kv
   const cuuint32_t box[5] = {(cuuint32_t)(line / eb), (cuuint32_t)(c->page_size < tile ? c->page_size : tile),
                              (cuuint32_t)(row / line), 1, 1};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  const CUtensorMapSwizzle swizzle = line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUtensorMapSwizzle swizzle = line == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
   // L2 fetches whole runs of rows where a head's rows are next to each other, else no more than a row
   const bool dense = stride[2] == c->head_dim;
   const CUtensorMapL2promotion l2 = dense || row >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
@@ -209,8 +211,10 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
                          const int32_t* free_pages, int32_t n_free, const int32_t* free_head, int32_t* table,
                          int32_t* pages, int32_t* free_head_out, int64_t* slots, int64_t n_slots) {
   if (!h) return CVR_E_ARG;
-  if (n_req < 0 || n_req > h->cfg.max_req) return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", h->cfg.max_req, n_req);
-  if (n_free < 0 || n_slots < 0 || n_slots >= INT32_MAX) return kv_fail(h, CVR_E_SHAPE, "need n_free >= 0 and 0 <= n_slots < 2^31 - 1");
+  if (n_req < 0 || n_req > h->cfg.max_req)
+    return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", h->cfg.max_req, n_req);
+  if (n_free < 0 || n_slots < 0 || n_slots >= INT32_MAX)
+    return kv_fail(h, CVR_E_SHAPE, "need n_free >= 0 and 0 <= n_slots < 2^31 - 1");
   if (n_req > 0 && (!lens || !table)) return kv_fail(h, CVR_E_ARG, "null lens or table");
   if ((n_free > 0 && !free_pages) || (n_slots > 0 && !slots)) return kv_fail(h, CVR_E_ARG, "null free_pages or slots");
   if ((pages && pages == held) || (free_head_out && free_head_out == free_head))
@@ -282,7 +286,8 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   if (!h) return CVR_E_ARG;
   const cvr_kv_config& c = h->cfg;
   if (!c.k) return kv_fail(h, CVR_E_ARG, "the handle was created without pools");
-  if (n_req < 0 || n_req > c.max_req) return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", c.max_req, n_req);
+  if (n_req < 0 || n_req > c.max_req)
+    return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", c.max_req, n_req);
   if (!std::isfinite(scale)) return kv_fail(h, CVR_E_ARG, "scale must be finite");
   if (n_req == 0) return CVR_OK;
   if (!q || !lens || !table || !out) return kv_fail(h, CVR_E_ARG, "null q, lens, table or out");
@@ -318,7 +323,7 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   a.n_places = h->n_places;
   a.err = h->err_host_dev;
   // one CTA per tile that there can be at most, at most as many as the SMs hold at once
-  const int64_t seen = c.window && c.window < c.max_pages * c.page_size ? c.window + h->attend.tile : (int64_t)c.max_pages * c.page_size;
+  const int64_t all = (int64_t)c.max_pages * c.page_size, seen = c.window && c.window < all ? c.window + h->attend.tile : all;
   const int64_t most = n_req * c.kv_heads * ((seen + h->attend.tile - 1) / h->attend.tile);
   const int64_t fit = (int64_t)h->num_sms * h->attend.ctas_per_sm;
   cudaLaunchConfig_t lc = {};
