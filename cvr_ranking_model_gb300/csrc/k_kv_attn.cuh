@@ -61,8 +61,9 @@ struct Shape {
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
   static constexpr int kQBytes = (MODE == 0 ? 8 : MT * 16) * kQRow;
   static constexpr int kORow = D + (I8 ? 16 : 8);               // padded fp32 rows of the joining area
-  static constexpr int kOBytes = kConsumers * 8 * kORow * 4 + 2 * kConsumers * 8 * 4;  // with its rows' m and l
-  static constexpr int kOAreas = D == 32 ? 2 : 1;              // (two spare a barrier per use, where they fit)
+  static constexpr int kORows = MODE == 0 ? 8 : 16;             // a warp's rows in the joining area
+  static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
+  static constexpr int kOAreas = D == 32 && MODE == 0 ? 2 : 1;           // (two spare a barrier per use, where they fit)
   static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     if (w < warp) before = add(before, s_sum[w]);
     all = add(all, s_sum[w]);
   }
-  const bool fits = (uint64_t)all * H <= 0x7fffffffu;
+  const bool fits = (uint64_t)all * H <= 0x7fff0000u;  // (sums with a grid's size stay below 2^31)
   if (!fits && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kKvErrSize);
   const int total = fits ? (int)all * H : 0;
   // An even share of the tiles; at least two where requests have two or more on average: a split costs a join (about 2 us at
@@ -352,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       const uint32_t box_bytes = br * (S::kRow + (I8 ? 4 : 0)), tile_bytes = TK * (S::kRow + (I8 ? 4 : 0));
       const bool long_pages = a.page_log2 > log2_br;  // several tiles per page, one box per tile
       for (int at = begin; at < end && ok;) {
-        // ---- a part: its query rows and description, then its tiles ----
+        // ---- a part: its query rows and description, and its tiles ----
         const int n = min(n_t - t, end - at), b = parts & 1;
         ok = wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
         if (!ok) break;
         if (lane == 0) {
-          const unsigned fb = P * H + h * n_t;
+          const unsigned fb = P * H + h * n_t, fe = fb + n_t - 1;  // the (request, head)'s first and last tile
           Part pt;
           pt.r = r;
           pt.h = h;
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           pt.n_tiles = n;
           pt.lo = lo;
           pt.len = len;
-          pt.i0 = fb / (unsigned)per;
-          pt.n_parts = (fb + n_t - 1) / (unsigned)per - pt.i0 + 1;
+          pt.i0 = (int)fb >= begin ? blockIdx.x : fb / (unsigned)per;
+          pt.n_parts = ((int)fe < end ? blockIdx.x : fe / (unsigned)per) - pt.i0 + 1;
           s_part[b] = pt;
           mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
         }
@@ -434,17 +435,16 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         more_ids = more0;
       }
     }
-    // requests that see nothing, shared out over the grid
-    for (int rb = blockIdx.x * 32; rb < a.n_req; rb += gridDim.x * 32) {
-      const bool none = rb + lane < a.n_req && clamped_len(a, __ldg(a.lens + rb + lane)) == 0;
-      unsigned m = __ballot_sync(0xffffffffu, none);
-      while (m) {
-        const int r = rb + __ffs(m) - 1;
-        m &= m - 1;
-        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_stride);
+    // requests that see nothing, shared out over the grid: this CTA's are blockIdx, blockIdx + grid, ..
+    for (int64_t r0 = blockIdx.x; r0 < a.n_req; r0 += 32 * (int64_t)gridDim.x) {
+      const int64_t mine = r0 + (int64_t)lane * gridDim.x;
+      unsigned none = __ballot_sync(0xffffffffu, mine < a.n_req && clamped_len(a, __ldg(a.lens + min(mine, (int64_t)a.n_req - 1))) == 0);
+      for (; none; none &= none - 1) {
+        const int64_t r = r0 + (int64_t)(__ffs(none) - 1) * gridDim.x;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + r * a.out_stride);
         for (int i = lane; i < a.q_heads * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-          for (int i = lane; i < a.q_heads; i += 32) a.lse[(int64_t)r * a.q_heads + i] = -INFINITY;
+          for (int i = lane; i < a.q_heads; i += 32) a.lse[r * a.q_heads + i] = -INFINITY;
       }
     }
     // the copies in flight land before the CTA's shared memory can go, also when a consumer's wait gave up
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       ks = v_slot + 1 == RING ? 0 : v_slot + 1;
     }
 
-    // ---- the part's end: the warps' (m, l, o) to shared memory, 8 rows of each tile at a time, and summed ----
+    // ---- the part's end: the warps' (m, l, o) to shared memory, and summed ----
     if (I8) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
@@ -844,53 +844,56 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     };
     const int part = (int)blockIdx.x - pt.i0, place = part_place(pt.i0, part);
     constexpr int kPerRow = D / 4;  // 4 values per thread
-#pragma unroll 1
-    for (int pass = 0; pass < (R8 ? 1 : 2); ++pass) {
+    {
       if (S::kOAreas == 1) {
-        consumer_sync();  // (the previous pass or part has been read; with two areas the use between has said so)
+        consumer_sync();  // (the previous part has been read; with two areas the part between has said so)
         if (!ok) return;
       }
       float* const s_o = reinterpret_cast<float*>(sm + S::oO + (S::kOAreas == 1 ? 0 : (areas & 1)) * S::kOBytes);
-      float* const s_m = s_o + kConsumers * 8 * S::kORow;
-      float* const s_l = s_m + kConsumers * 8;
+      float* const s_m = s_o + kConsumers * S::kORows * S::kORow;
+      float* const s_l = s_m + kConsumers * S::kORows;
       ++areas;
-      if (mt * 16 + pass * 8 + gid < G) {
-        float* dst = s_o + (warp * 8 + gid) * S::kORow;
+#pragma unroll
+      for (int half = 0; half < S::kORows / 8; ++half) {
+        const bool upper = half != 0;
+        if (mt * 16 + upper * 8 + gid >= G) continue;
+        const int row = warp * S::kORows + half * 8 + gid;
+        float* dst = s_o + row * S::kORow;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
-          const float x = (R8 ? o[j][0] + o[j][2] : pass ? o[j][2] : o[j][0]) * o_mul;
-          const float y = (R8 ? o[j][1] + o[j][3] : pass ? o[j][3] : o[j][1]) * o_mul;
+          const float x = (R8 ? o[j][0] + o[j][2] : upper ? o[j][2] : o[j][0]) * o_mul;
+          const float y = (R8 ? o[j][1] + o[j][3] : upper ? o[j][3] : o[j][1]) * o_mul;
           if (!I8) {
             *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
           } else if (j & 1) {
             // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)
-            const float u = (R8 ? o[j - 1][0] + o[j - 1][2] : pass ? o[j - 1][2] : o[j - 1][0]) * o_mul;
-            const float v = (R8 ? o[j - 1][1] + o[j - 1][3] : pass ? o[j - 1][3] : o[j - 1][1]) * o_mul;
+            const float u = (R8 ? o[j - 1][0] + o[j - 1][2] : upper ? o[j - 1][2] : o[j - 1][0]) * o_mul;
+            const float v = (R8 ? o[j - 1][1] + o[j - 1][3] : upper ? o[j - 1][3] : o[j - 1][1]) * o_mul;
             *reinterpret_cast<float4*>(dst + (j >> 1) * 16 + 4 * tig) = make_float4(u, x, v, y);
           }
         }
         if (tig == 0) {
-          s_m[warp * 8 + gid] = pass ? mB : mA;
-          s_l[warp * 8 + gid] = pass ? lB : lA;
+          s_m[row] = upper ? mB : mA;
+          s_l[row] = upper ? lB : lA;
         }
       }
       consumer_sync();
       if (!ok) return;
-      for (int x = tid; x < 8 * MT * kPerRow; x += kConsumers * 32) {
-        const int row8 = x / kPerRow, c = (x - row8 * kPerRow) * 4;
-        const int rt = row8 >> 3, rr = row8 & 7, g = rt * 16 + pass * 8 + rr;
+      for (int x = tid; x < S::kORows * MT * kPerRow; x += kConsumers * 32) {
+        const int rx = x / kPerRow, c = (x - rx * kPerRow) * 4;
+        const int rt = rx / S::kORows, rr = rx % S::kORows, g = rt * 16 + rr;
         if (g >= G) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * 8 + rr]);
+        for (int p = 0; p < KP; ++p) top = fmaxf(top, s_m[(p * MT + rt) * S::kORows + rr]);
         const float base = top == -INFINITY ? 0.f : top;
         float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
-          const int w = p * MT + rt;
-          const float f = ex2(s_m[w * 8 + rr] - base);
-          l += f * s_l[w * 8 + rr];
-          const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * S::kORow + c);
+          const int w = (p * MT + rt) * S::kORows + rr;
+          const float f = ex2(s_m[w] - base);
+          l += f * s_l[w];
+          const float4 v = *reinterpret_cast<const float4*>(s_o + w * S::kORow + c);
           acc[0] += f * v.x;
           acc[1] += f * v.y;
           acc[2] += f * v.z;
@@ -934,44 +937,64 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         if (!groups) --k;  // (another CTA joins this group, and sees to the groups)
         continue;
       }
-      // parts g0, g0 + every, .. (n of them): every thread joins 4 values of a row, kAtOnce parts in flight
-      constexpr int kAtOnce = D == 128 ? 16 : 8;
-      for (int x0 = warp * 32; x0 < G * kPerRow; x0 += kConsumers * 32) {
-        const int x = min(x0 + lane, G * kPerRow - 1), g = x / kPerRow, c = (x - g * kPerRow) * 4;
-        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int b = 0; b < n; b += kAtOnce) {
-          float2 ml[kAtOnce];
-          float4 v[kAtOnce];
+      // parts g0, g0 + every, .. (n of them): a thread joins 4 values of a row at a time, kInFlight loads in flight: of that
+      // many parts, or of 4 parts for several rows where there are no more
+      constexpr int kInFlight = D == 128 ? 16 : 8;
+      auto join = [&](auto parts_at_once) {
+        constexpr int NP = decltype(parts_at_once)::value, NX = kInFlight / NP;
+        for (int x0 = warp * 32; x0 < G * kPerRow; x0 += NX * kConsumers * 32) {
+          float m[NX], l[NX], acc[NX][4];
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u) {
-            const int64_t from = (int64_t)part_place(of.i0, g0 + min(b + u, n - 1) * every) * G + g;
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + from);
-            v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + c));
+          for (int i = 0; i < NX; ++i) {
+            m[i] = -INFINITY;
+            l[i] = acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
           }
-          float top = m;
+          for (int b = 0; b < n; b += NP) {
+            float2 ml[NX][NP];
+            float4 v[NX][NP];
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, ml[u].x);
-          const float base = top == -INFINITY ? 0.f : top, f = ex2(m - base);
-          l *= f;
+            for (int i = 0; i < NX; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] *= f;
+              for (int u = 0; u < NP; ++u) {
+                const int x = min(x0 + i * kConsumers * 32 + lane, G * kPerRow - 1), g = x / kPerRow;
+                const int64_t from = (int64_t)part_place(of.i0, g0 + min(b + u, n - 1) * every) * G + g;
+                ml[i][u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + from);
+                v[i][u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + (x - g * kPerRow) * 4));
+              }
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u)
-            if (b + u < n) {
-              const float w = ex2(ml[u].x - base);
-              l += w * ml[u].y;
-              acc[0] += w * v[u].x;
-              acc[1] += w * v[u].y;
-              acc[2] += w * v[u].z;
-              acc[3] += w * v[u].w;
+            for (int i = 0; i < NX; ++i) {
+              float top = m[i];
+#pragma unroll
+              for (int u = 0; u < NP; ++u) top = fmaxf(top, ml[i][u].x);
+              const float base = top == -INFINITY ? 0.f : top, f = ex2(m[i] - base);
+              l[i] *= f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+#pragma unroll
+              for (int u = 0; u < NP; ++u)
+                if (b + u < n) {
+                  const float w = ex2(ml[i][u].x - base);
+                  l[i] += w * ml[i][u].y;
+                  acc[i][0] += w * v[i][u].x;
+                  acc[i][1] += w * v[i][u].y;
+                  acc[i][2] += w * v[i][u].z;
+                  acc[i][3] += w * v[i][u].w;
+                }
+              m[i] = top;
             }
-          m = top;
+          }
+          __syncwarp();  // (a row's lanes, one warp, have read the first part, whose place the group's sum takes)
+#pragma unroll
+          for (int i = 0; i < NX; ++i) {
+            const int x = x0 + i * kConsumers * 32 + lane, g = x / kPerRow, c = (x - g * kPerRow) * 4;
+            if (x >= G * kPerRow) continue;
+            if (groups || n_groups == 1) finish(of, g, c, m[i], l[i], acc[i]);
+            else keep(part_place(of.i0, g0), g, c, m[i], l[i], acc[i]);
+          }
         }
-        __syncwarp();  // (a row's lanes, one warp, have read the first part, whose place the group's sum takes)
-        if (x0 + lane != x) continue;
-        if (groups || n_groups == 1) finish(of, g, c, m, l, acc);
-        else keep(part_place(of.i0, g0), g, c, m, l, acc);
-      }
+      };
+      if (n <= 4) join(std::integral_constant<int, 4>());
+      else join(std::integral_constant<int, kInFlight>());
     }
   }
 }

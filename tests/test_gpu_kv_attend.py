@@ -69,7 +69,8 @@ def test_one_pool_for_keys_and_values(dtype, cache, dim, group):
     check(Cache(EDGES, 4, dim, 32, dtype, cache, shared=True, seed=5), 4 * group)
 
 
-@pytest.mark.parametrize("n,heads,group,dim", [(70001, 1, 1, 32), (40000, 1, 8, 128), (20001, 8, 4, 128), (30000, 2, 64, 64)])
+@pytest.mark.parametrize("n,heads,group,dim", [(70001, 1, 1, 32), (40000, 1, 8, 128), (20001, 8, 4, 128), (30000, 2, 64, 64), (50001, 1, 16, 64),
+                                              (30000, 1, 32, 128), (40000, 1, 64, 32)])
 @pytest.mark.parametrize("cache", ["same", "i8"])
 def test_long_histories_split_over_the_gpu(n, heads, group, dim, cache):
     check(Cache([n], heads, dim, 64, "bf16", cache, seed=n), heads * group)
