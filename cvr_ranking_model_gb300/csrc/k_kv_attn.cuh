@@ -561,12 +561,12 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
             bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
           }
-          const uint32_t eA = __float_as_uint(bigA) >> 23, eB = __float_as_uint(bigB) >> 23;
-          const bool fitA = eA > 0 && eA < 254, fitB = eB > 0 && eB < 254;
-          mulA = fitA ? __uint_as_float((254u - eA) << 23) : 1.f;
-          mulB = fitB ? __uint_as_float((254u - eB) << 23) : 1.f;
-          cA = fitA ? fmaxf(c_all * __uint_as_float(eA << 23), 1.4e-45f) : c_all;
-          cB = fitB ? fmaxf(c_all * __uint_as_float(eB << 23), 1.4e-45f) : c_all;
+          // (the exponents at the type's ends, subnormals' and the highest, take the power beside theirs: both factors are normal)
+          const uint32_t eA = min(max(__float_as_uint(bigA) >> 23, 1u), 253u), eB = min(max(__float_as_uint(bigB) >> 23, 1u), 253u);
+          mulA = __uint_as_float((254u - eA) << 23);
+          mulB = __uint_as_float((254u - eB) << 23);
+          cA = fmaxf(c_all * __uint_as_float(eA << 23), 1.4e-45f);
+          cB = fmaxf(c_all * __uint_as_float(eB << 23), 1.4e-45f);
         }
         if (negate) {
           mulA = -mulA;

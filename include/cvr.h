@@ -368,10 +368,11 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  *   scale finite; with the ranking model's temperature 1 / (tau * sqrt(head_dim))
  *   lse   fp32 [n_req][q_heads] natural log of the softmax's denominator; NULL: not written
  * What lies in a page behind the history (or before the window) never reaches the output, whatever its bits. Logits,
- * softmax and sums are fp32. Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length
- * outside [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read;
- * out is not meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not written,
- * but for the empty requests), CVR_E_TIMEOUT. */
+ * softmax and sums are fp32: scale times a query value, the logits, and sums of |v| times 2^6 have to lie in its range.
+ * Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length outside
+ * [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read; out is not
+ * meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not
+ * written, but for the empty requests), CVR_E_TIMEOUT. */
 cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
                          const int32_t* table, float scale, void* out, int64_t out_stride, float* lse);
 

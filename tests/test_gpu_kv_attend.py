@@ -91,6 +91,19 @@ def test_scales(scale, dtype, cache):
     check(Cache([1, 50, 333], 2, 64, 16, dtype, cache, seed=8), 4, scale=scale)
 
 
+@pytest.mark.parametrize("cache", ["same", "i8"])
+@pytest.mark.parametrize("log2_q,log2_k,scale", [(126, -90, 2.0 ** -38), (124, -90, 2.0 ** -36), (-130, 100, 2.0 ** 28), (-126, 100, 2.0 ** 24)])
+def test_queries_at_the_ends_of_bf16(log2_q, log2_k, scale, cache):
+    c = Cache([1, 50, 333], 2, 64, 16, "bf16", cache, seed=22)
+    for r, n in enumerate(c.lens_list):
+        p = c.table[r, :-(-n // 16)].long()
+        if cache == "i8":
+            c.k_scale[p] *= 2.0 ** log2_k
+        else:
+            c.k[p] = (c.k[p].float() * 2.0 ** log2_k).to(c.k.dtype)  # (exact: powers of two, far from the type's ends)
+    check(c, 4, scale=scale, gain=0.9 * 2.0 ** log2_q)
+
+
 def test_twelve_thousand_requests_most_of_them_empty():
     check(Cache([3 if i % 7 == 0 else 40 if i == 11999 else 0 for i in range(12000)], 1, 32, 8, "f16", seed=18), 1)
 
