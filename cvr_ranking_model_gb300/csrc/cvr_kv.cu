@@ -184,6 +184,13 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
     fprintf(stderr, "cvr_kv_create: %s\n", why);
     return CVR_E_ARG;
   }
+  // (a captured clearing of the counters would run with the graph only)
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(cuda_stream), &capturing) != cudaSuccess) cudaGetLastError();
+  if (capturing != cudaStreamCaptureStatusNone) {
+    fprintf(stderr, "cvr_kv_create: the stream is capturing a graph\n");
+    return CVR_E_ARG;
+  }
   cvr_kv* h = new (std::nothrow) cvr_kv();
   if (!h) return CVR_E_OOM;
   h->cfg = *cfg;
@@ -352,7 +359,7 @@ cvr_status cvr_kv_sync(cvr_kv* h) {
   *word = 0;
   if (ew & kErrTimeout) {
     // a CTA that gave up may have left a counter part-way; the next call starts from zero
-    if (h->count) cudaMemset(h->count, 0, h->count_bytes);
+    if (h->count) cudaMemsetAsync(h->count, 0, h->count_bytes, h->stream);
     return kv_fail(h, CVR_E_TIMEOUT, "a bounded device-side wait gave up");
   }
   if (ew & kKvErrLens) return kv_fail(h, CVR_E_INPUT, "a length, new length, held count or list head is out of range");

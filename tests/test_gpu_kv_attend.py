@@ -269,6 +269,28 @@ def test_capture_and_replay():
         assert_within(lse, ref_lse, b_lse, "lse")
 
 
+def test_no_handle_is_made_while_its_stream_captures():
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    s = torch.cuda.Stream()
+    c = Cache([300, 20], 2, 64, 16, "bf16", seed=24)
+    q = torch.randn((2, 8, 64), device="cuda").to(torch.bfloat16)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    kv = c.handle(8, stream=s.cuda_stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s, capture_error_mode="relaxed"):
+        with pytest.raises(cvr.CvrError) as e:
+            c.handle(8, stream=s.cuda_stream)
+        kv.attend(2, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.1, out.data_ptr())
+    assert e.value.status == 1
+    with torch.cuda.stream(s):
+        graph.replay()
+    kv.sync()
+    ref, _, b_out, _ = c.reference(q, 0.1)
+    assert_within(out, ref, b_out, "out")
+
+
 def test_two_handles_on_two_streams_at_once():
     import torch
     c = Cache([20000, 300, 7], 2, 128, 32, "bf16", seed=17)
