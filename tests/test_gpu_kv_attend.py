@@ -309,6 +309,24 @@ def test_two_handles_on_two_streams_at_once():
         assert_within(out, ref, b_out, "out")
 
 
+def test_histories_too_long_together():
+    """More tiles than a call can number: reported, nothing written but for the empty request, and the handle stays good."""
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    k = torch.randn((1, 256, 256, 32), device="cuda").to(torch.bfloat16)
+    kv = cvr.KvCache(cvr.make_kv_config(256, 256, 32, 256, 1, 4, 2 ** 22, k=k.data_ptr()))
+    lens = torch.tensor([2 ** 30, 0, 2 ** 30, 2 ** 30], dtype=torch.int32, device="cuda")
+    table = torch.zeros((4, 2 ** 22), dtype=torch.int32, device="cuda")
+    q = torch.randn((4, 256, 32), device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    kv.attend(4, q.data_ptr(), lens.data_ptr(), table.data_ptr(), 0.1, out.data_ptr())
+    assert kv.sync(check=False) == 2 and "too long together" in kv.last_error()
+    assert bool((out[[0, 2, 3]] == 7).all()) and not bool(out[1].any())
+    lens.copy_(torch.tensor([256, 0, 1, 100], dtype=torch.int32))
+    kv.attend(4, q.data_ptr(), lens.data_ptr(), table.data_ptr(), 0.1, out.data_ptr())
+    assert kv.sync(check=False) == 0 and torch.equal(out[2], k[0, :, 0])
+
+
 def test_refusals():
     import torch
     import cvr_ranking_model_gb300 as cvr
