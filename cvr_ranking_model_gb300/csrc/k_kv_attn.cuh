@@ -4,8 +4,9 @@
 // Every K and V row is read once for all the query heads that share it, so the floor is the bytes of the seen rows.
 //
 // Work: a tile is 8 or 16 KB of one kv head's K rows (at most 256) and the V rows beside them. The tiles of all requests
-// and heads form one line (request, then head, then position); a persistent grid cuts it into equal runs, so ragged lengths,
-// few long histories and many short ones load the SMs alike. A CTA finds its run by scanning the lengths itself. What
+// and heads form one line (request, then head, then position; in long runs with a place or two in front of each head's tiles for
+// what its start and end cost); a persistent grid cuts it into equal runs, so ragged lengths, few long histories and many
+// short ones load the SMs alike. A CTA finds its run by scanning the lengths itself. What
 // a CTA leaves of a (request, head) that it shares with others goes to the workspace as (m, l, o); the last of them to
 // arrive joins the parts in order, so results do not depend on which it is.
 //
@@ -21,8 +22,8 @@
 //     the weight, whose products are kept in fp16's range by the warp's largest scale so far.
 //
 // Measured (one GB300, copy rate 6.67 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128, bf16: 113 us, 6.5 TB/s;
-// one request of 131071: 84 us, 6.4 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 79 us, 4.9 TB/s,
-// bound by issue (bytes to fp16). 512 histories of up to 2000 events, 4 heads of 32, K = V: 37 us, 3.5 TB/s, bound by issue:
+// one request of 131071: 85 us, 6.3 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 74 us, 5.2 TB/s,
+// bound by issue (bytes to fp16). 512 histories of up to 2000 events, 4 heads of 32, K = V: 34 us, 3.8 TB/s, bound by issue:
 // boxes of 1 KB in the producer, the softmax in the others. One request of 200: 4.3 us, latency.
 #pragma once
 
@@ -41,7 +42,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A part: the tiles of one (request, kv head) in a CTA's run.
 struct __align__(16) Part {
-  int r, h, k0, n_tiles;     // request, kv head, first token of the first tile
+  int r, h, k0, n_tiles;     // request, kv head, first token of the first tile; n_tiles negated: the run's last part
   int lo, len, i0, n_parts;  // tokens seen: [lo, len); the (request, head) has n_parts parts, of CTAs i0, i0 + 1, ..
 };
 constexpr int kGroup = 16;  // parts that are joined at once
@@ -65,6 +66,7 @@ struct Shape {
   static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
   static constexpr int kOAreas = D == 32 && MODE == 0 ? 2 : 1;           // (two spare a barrier per use, where they fit)
   static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
+  static constexpr int kPartCost = MT == 1 ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
   // ring units: what is left of this CTA's share of the SM's 228 KB (1 KB of it reserved, 1 KB for the ring's alignment)
@@ -254,38 +256,58 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const int r0 = min(tid * few, a.n_req), r1 = min(r0 + few, a.n_req);
   auto add = [](uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); };
   uint32_t mine = 0;
+  int nonempty = 0;
   bool bad = false;
   for (int r = r0; r < r1; ++r) {
     const int raw = __ldg(a.lens + r), len = clamped_len(a, raw);
     bad |= raw != len;
     mine = add(mine, tiles_of<TK>(a, len));
+    nonempty += len > 0;
   }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kKvErrLens);
-  uint32_t incl = mine;
+  // In runs of 8 tiles or more a (request, head) has kPartCost empty places in front of its tiles, or a run of many short
+  // requests would end last: 32 requests of 1 to 16383 tokens in 8 bits 80.5 -> 74.3 us, 48 of up to 6001 tokens, 8 x 32 heads
+  // over rows of 64, 56.9 -> 47.9 us.
+  int lead = 0;
+  uint32_t before, all;  // places per head before this thread's requests, and of all
+  bool fits = true, two_each = false;
+#pragma unroll 1
+  while (true) {  // (once without the empty places, to see whether there are any)
+    uint32_t incl = mine;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl = add(incl, u);
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  cta_sync();
-  uint32_t before = incl - mine, all = 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl = add(incl, u);
+    }
+    uint32_t* const sums = s_sum + (lead ? 8 : 0);
+    if (lane == 31) sums[warp] = incl;
+    cta_sync();
+    before = incl - mine;
+    all = 0;
 #pragma unroll
-  for (int w = 0; w <= kConsumers; ++w) {
-    if (w < warp) before = add(before, s_sum[w]);
-    all = add(all, s_sum[w]);
+    for (int w = 0; w <= kConsumers; ++w) {
+      if (w < warp) before = add(before, sums[w]);
+      all = add(all, sums[w]);
+    }
+    if (lead) break;
+    const uint64_t tiles = (uint64_t)all * H;
+    fits = tiles <= 0x7fff0000u;  // (sums with a grid's size stay below 2^31)
+    two_each = (int)all >= 2 * a.n_req;
+    if (tiles < 8 * gridDim.x || tiles > 0x7fff0000u / (1 + S::kPartCost)) break;
+    lead = S::kPartCost;
+    mine += nonempty * lead;
   }
-  const bool fits = (uint64_t)all * H <= 0x7fff0000u;  // (sums with a grid's size stay below 2^31)
   if (!fits && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kKvErrSize);
+  auto extent = [&](int n) { return n > 0 ? n + lead : 0; };  // places of a request of n tiles, per head
   const int total = fits ? (int)all * H : 0;
-  // An even share of the tiles; at least two where requests have two or more on average: a split costs a join (about 2 us at
-  // a call's end), a second tile about 0.5 us. One request of 200 tokens of 4 x 32: 4.7 us in 4 runs, 5.8 us in 8.
-  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, (int)all >= 2 * a.n_req ? 2 : 1);
+  // An even share of the line; at least two tiles where requests have two or more on average: a split costs a join (about 2 us
+  // at a call's end), a second tile about 0.5 us. One request of 200 tokens of 4 x 32: 4.7 us in 4 runs, 5.8 us in 8.
+  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, two_each ? 2 : 1);
   const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min((int64_t)begin + per, (int64_t)total);
-  const int n_tiles = end - begin;
-  if (n_tiles > 0 && begin >= (int)before * H && begin < (int)(before + mine) * H) {
+  const bool some = end > begin;  // (a run without tiles is none: the line ends with a tile, other runs are longer than kPartCost)
+  if (some && begin >= (int)before * H && begin < (int)(before + mine) * H) {
     for (int r = r0; r < r1; ++r) {
-      const int n = tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r)));
+      const int n = extent(tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r))));
       if (begin < ((int)before + n) * H) {
         s_start[0] = r;
         s_start[1] = (int)before;
@@ -303,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     int slot = 0, filled = 0;  // the ring's next unit, and the units filled so far (at most RING)
     uint32_t phase = 0;        // parity of the ring's round
     int parts = 0;             // parts begun
-    if (n_tiles > 0) {
+    if (some) {
       // Page ids come 32 entries of a table row at a time, one per lane, and ahead of their use: the row's next 32, and the
       // first 32 of the next request. A tile's entries never straddle two batches (both begin at a multiple of its count).
       auto entries = [&](int row, int e) {
@@ -329,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         n_len = some ? __shfl_sync(0xffffffffu, wl, __ffs(some) - 1) : 0;
         n_ids = some ? entries(n_r, first_entry(n_len)) : 0;
       };
-      int P = s_start[1], r = 0, h = 0, t = 0, n_t = 1, t0 = 0, len = 0, lo = 0;  // P: tiles per head before request r
+      int P = s_start[1], r = 0, h = 0, t = 0, n_t = 1, t0 = 0, len = 0, lo = 0;  // P: places per head before request r
+      int w_t = 1;  // the request's places per head
       int e0 = 0, ids = 0, more_ids = 0;  // entries e0 + lane and e0 + 32 + lane of the request's table row
       int ids0 = 0, more0 = 0;            // the same from the request's first entry on, for its next head
       auto enter = [&]() {  // the request that was looked ahead to
@@ -338,12 +361,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         lo = seen_from(a, len);
         t0 = lo / TK;
         n_t = max(1, tiles_of<TK>(a, len));
+        w_t = extent(n_t);
       };
       window(wb);
       look_ahead(wb);
       enter();
-      h = (begin - P * H) / n_t;
-      t = (begin - P * H) - h * n_t;
+      h = (begin - P * H) / w_t;
+      t = max((begin - P * H) - h * w_t - lead, 0);
       e0 = ((t0 + t) * TK) >> a.page_log2;  // (the run may begin anywhere in its request)
       ids = entries(r, e0);
       more_ids = entries(r, e0 + 32);
@@ -352,22 +376,24 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       bool ok = true;
       const uint32_t box_bytes = br * (S::kRow + (I8 ? 4 : 0)), tile_bytes = TK * (S::kRow + (I8 ? 4 : 0));
       const bool long_pages = a.page_log2 > log2_br;  // several tiles per page, one box per tile
-      for (int at = begin; at < end && ok;) {
+      while (ok) {
         // ---- a part: its query rows and description, and its tiles ----
-        const int n = min(n_t - t, end - at), b = parts & 1;
+        const int first = P * H + h * w_t + lead;  // the (request, head)'s first tile's place
+        const int n = min(n_t - t, end - first - t), b = parts & 1;
+        const bool more = n == n_t - t && first + n_t + lead < end;  // the run goes on
         ok = wait_warp(q_empty + b, ((parts >> 1) & 1) ^ 1, abort_flag, a.err);
         if (!ok) break;
         if (lane == 0) {
-          const unsigned fb = P * H + h * n_t, fe = fb + n_t - 1;  // the (request, head)'s first and last tile
+          const int last = first + n_t - 1;
           Part pt;
           pt.r = r;
           pt.h = h;
           pt.k0 = (t0 + t) * TK;
-          pt.n_tiles = n;
+          pt.n_tiles = more ? n : -n;
           pt.lo = lo;
           pt.len = len;
-          pt.i0 = (int)fb >= begin ? blockIdx.x : fb / (unsigned)per;
-          pt.n_parts = ((int)fe < end ? blockIdx.x : fe / (unsigned)per) - pt.i0 + 1;
+          pt.i0 = first >= begin ? blockIdx.x : (unsigned)first / (unsigned)per;
+          pt.n_parts = (last < end ? blockIdx.x : (unsigned)last / (unsigned)per) - pt.i0 + 1;
           s_part[b] = pt;
           mbar_expect_tx(q_full + b, (uint32_t)G * D * 2);
         }
@@ -376,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         for (int g = lane; g < G; g += 32)
           bulk_load(smem_u32(sm + S::oQ + b * S::kQBytes + g * S::kQRow), q + g * D, D * 2, q_full + b);
         ++parts;
-        if (h + 1 == H && n == n_t - t && at + n < end) look_ahead(r + 1);  // (its lengths and page ids arrive meanwhile)
+        if (more && h + 1 == H) look_ahead(r + 1);  // (its lengths and page ids arrive meanwhile)
         for (int i = 0; i < n && ok; ++i) {
           const int k0 = (t0 + t + i) * TK;
           if ((k0 >> a.page_log2) >= e0 + 32) {
@@ -420,12 +446,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           }
         }
         // on to the next head, or the next request
-        at += n;
-        if (at >= end) break;
+        if (!more) break;
         t = 0;
         if (++h == H) {
           h = 0;
-          P += n_t;
+          P += w_t;
           enter();
           ids0 = n_ids;
           more0 = entries(r, first_entry(len) + 32);
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   bool early = false;
   unsigned early_count = 0;  // (thread 0: the parts counted before it)
 
-  for (int done = 0; done < n_tiles;) {
+  for (bool last = !some; !last;) {
     // ---- a part: the tiles of one (request, head) in this CTA's run ----
     uint32_t qf[D / 16][4];
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
@@ -523,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     ok = wait_warp(q_full + qb, (parts >> 1) & 1, abort_flag, a.err);
     if (!ok) return;
     const Part pt = s_part[qb];
+    const int n_tiles = abs(pt.n_tiles);
+    last = pt.n_tiles < 0;
     {
       const uint8_t* qs = sm + S::oQ + qb * S::kQBytes + mt * 16 * S::kQRow;
       const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
@@ -585,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_empty + qb);
     ++parts;
-    done += pt.n_tiles;
 
     // One tile: its K and V units, and its tokens [j0, j1) that are seen. Whole tiles take the instance without masks.
     auto step = [&](auto masked, int k_slot, int v_slot, uint32_t v_phase, int j0, int j1) {
@@ -799,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         }
       }
     };
-    for (int i = 0; i < pt.n_tiles; ++i) {
+    for (int i = 0; i < n_tiles; ++i) {
       ok = wait_warp(full + ks, phase, abort_flag, a.err);
       if (!ok) return;
       const int v_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
@@ -906,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
 
     // ---- joining: the last of a group of 16 parts to get here joins the group, the last group's joiner the groups ----
     // A release by one thread after the warps' meeting covers what all of them wrote.
-    if (pt.n_parts > 1 && done < n_tiles) {
+    if (pt.n_parts > 1 && !last) {
       // (not the run's last part: counted now, looked at when the run is through)
       consumer_sync();
       if (!ok) return;
@@ -914,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       if (tid == 0) s_part[2] = pt;
       if (tid == 0) early_count = add_acq_rel(a.count + part_place(pt.i0, part / kGroup * kGroup));
     }
-    if (done < n_tiles) continue;
+    if (!last) continue;
     // This part and the early one; of each its group of parts, then the groups. A count is of what precedes the own.
 #pragma unroll 1
     for (int k = early ? 3 : 1; k >= 0; --k) {
@@ -927,9 +953,9 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       unsigned* const count = a.count + (groups ? a.n_places : 0) + part_place(of.i0, g0);
       consumer_sync();
       if (ok && tid == 0) {
-        const bool last = (k == 3 ? early_count : add_acq_rel(count)) == (unsigned)(n - 1);
-        if (last) *count = 0u;  // ready for the next call
-        *s_last = last;
+        const bool is_last = (k == 3 ? early_count : add_acq_rel(count)) == (unsigned)(n - 1);
+        if (is_last) *count = 0u;  // ready for the next call
+        *s_last = is_last;
       }
       consumer_sync();
       if (!ok) return;
