@@ -86,6 +86,26 @@ def test_tables_when_the_free_list_ends():
     assert want[1] == [2, 1, 0] and want[0][2] == [-1, -1, -1, 9]
 
 
+@pytest.mark.parametrize("page,left", [(8, 0), (8, 1), (8, 700), (8, 1250), (64, 90), (256, 21)])
+def test_long_histories_when_the_free_list_ends(page, left):
+    lens, held_tokens = [6000, 0, 1, 5003, 300], [100, 0, 0, 3, 300]
+    held = [-(-x // page) for x in held_tokens]
+    new = [x - y for x, y in zip(lens, held_tokens)]
+    max_pages = -(-6000 // page) + 2
+    ids = list(range(2000))
+    random.Random(page + left).shuffle(ids)
+    table, at = [], 0
+    for h in held:
+        table.append(ids[at:at + h] + [-7] * (max_pages - h))
+        at += h
+    free = ids[at:at + left]
+    want = tables_reference(lens, new, held, free, 0, table, page, sum(new) + 5)
+    got = run_tables(lens, new, held, free, 0, table, page, sum(new) + 5, 2000, max_pages)
+    assert got[4] == (8 if left < sum(max(0, -(-x // page) - h) for x, h in zip(lens, held)) else 0)
+    for g, w, what in zip(got, want, ("table", "pages", "head", "slots")):
+        assert g == w, what
+
+
 def test_tables_report_bad_inputs():
     base = dict(lens=[20, 5], new=[1, 1], held=[1, 0], free=[3, 1, 2], head=0, table=[[5, 9], [9, 9]], page=16, n_slots=4, n_pages=10, max_pages=2)
     assert run_tables(**base)[4] == 0
