@@ -80,6 +80,15 @@ def test_ragged_batch_long_and_short():
     check(Cache([5000, 1, 0, 0, 64, 12345, 3, 700] + [0] * 40 + [9] * 30, 2, 128, 16, "f16", seed=3), 8)
 
 
+@pytest.mark.parametrize("tokens", [30000, 60000, 90000, 130000, 200000, 400000])
+@pytest.mark.parametrize("dim,heads,group,cache", [(128, 2, 4, "same"), (64, 2, 16, "i8"), (32, 4, 1, "same"), (128, 1, 24, "i8")])
+def test_runs_of_every_length(tokens, dim, heads, group, cache):
+    """Uneven requests, empty ones among them, over runs from two tiles to many."""
+    share = [0, 1, 0.2, 130, 3, 2.1, 0, 0.7, 5, 63]
+    lens = [int(tokens / heads * x / sum(share)) for x in share] + [1, 129, 0]
+    check(Cache(lens, heads, dim, 64, "bf16", cache, seed=tokens), heads * group)
+
+
 def test_many_short_requests():
     lens = [(i * 37) % 23 for i in range(3000)]
     check(Cache(lens, 1, 32, 8, "bf16", seed=4), 2)
