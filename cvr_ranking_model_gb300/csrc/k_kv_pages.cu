@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
         upto = min(x1, kind ? w_at : f_at);
       }
       const uint32_t* starts = kind ? s_w : s_f;
-      // the warp's items: the same number for each warp, at least a step's
-      const uint32_t each = ((upto - min(x, upto)) / n_warps / kTabRun + 1) * kTabRun;
+      // the warp's items: whole steps, the same number for each warp
+      const uint32_t step = n_warps * kTabRun, each = (upto - min(x, upto) + step - 1) / step * kTabRun;
       uint32_t b = (uint32_t)min((uint64_t)x + (uint64_t)my_warp * each, (uint64_t)upto);
       const uint32_t mine_end = (uint32_t)min((uint64_t)b + each, (uint64_t)upto);
       while (b < mine_end) {
