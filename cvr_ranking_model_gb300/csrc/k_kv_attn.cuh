@@ -19,7 +19,9 @@
 //   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-9 in bf16) does not add to
 //     the output's. With at most 8 query rows the halves sit in the two halves of the 16-row tile, at no extra cost.
 //   - 8-bit rows become fp16 exactly (1024 + q by a byte permute, minus 1152); K's scale multiplies the logit, V's scale
-//     the weight, whose products are kept in fp16's range by the warp's largest scale so far.
+//     the weight, whose products enter as fp16 over a divisor that the first scales choose. Where scales lie farther apart
+//     than the halves' bits allow, a row's exponents get a base of their own that follows its largest product, so that a large
+//     scale without weight leaves the other tokens their bits.
 //
 // Measured (one GB300, copy rate 6.67 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128, bf16: 113 us, 6.5 TB/s;
 // one request of 131071: 85 us, 6.3 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 74 us, 5.2 TB/s,
@@ -523,9 +525,10 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   // number above it: a token that is not seen has q . k = -infinity, whose product must stay that).
   const float c_all = fmaxf(fabsf(a.scale) * kLog2e, 1.4e-45f);
   const bool negate = a.scale < 0.f;
-  // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8,
-  // with 8-bit rows times 2^8 / vmax.
-  constexpr float kGrow = 6.f, kWeight = 256.f;
+  // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8, with
+  // 8-bit rows and their V scales over a power of two (below). The two halves hold a weight to 2^-22 of it, or to 2^-25, 2^-33
+  // of a weight of 1.
+  constexpr float kGrow = 6.f;
   constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
@@ -570,7 +573,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     float cA = c_all, cB = c_all;  // logit factors of rows A (gid) and B (gid + 8)
-    float vmax = 0x1p-100f, w_mul = kWeight * 0x1p100f;  // 8 bits: the largest row scale of V so far (floored)
+    // 8 bits: weight times V scale times |w_mul| enters the second product. |w_mul| is 2^8 / hi, hi a power of two (none yet: 0),
+    // and scales in [hi / 2^11, hi] need nothing else: a row's largest weight is 1 or more, so that the halves' 2^-33 hi per
+    // token is within 2^-22 of the row's sum. The first scales set hi to 8 to 16 times their largest; one outside starts `far`
+    // below, and w_mul is negative from then on, which puts every scale outside: 32 requests of 1 to 16383 tokens 73.6 us with
+    // scales within 4 of each other, 81.6 us with scales within 2^16.
+    float w_mul = 0.f;
+    auto hi_exponent = [&]() { return 262 - (int)(__float_as_uint(fabsf(w_mul)) >> 23); };
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           ok = wait_warp(full + v_slot, v_phase, abort_flag, a.err);
           if (!ok) return;
         }
-        float nA = -INFINITY, nB = -INFINITY, big = 0.f;
+        float nA = -INFINITY, nB = -INFINITY;
         float2 sv[NBS][2];  // 8 bits: V's row scales
 #pragma unroll
         for (int b = 0; b < NBS; ++b)
@@ -726,21 +735,64 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             }
             nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
             if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
-            if (I8) big = fmaxf(big, fmaxf(fabsf(sv[b][n].x), fabsf(sv[b][n].y)));
           }
         nA *= cA;
         if (!R8) nB *= cB;
-        // The exponents' base follows the running maximum only when a logit passes it by more than kGrow, and the weights'
-        // divisor the largest V scale when a scale passes it: most steps then need neither shuffles nor a rescaling.
-        if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || (I8 && big > vmax))) {
+        // 8 bits: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
+        auto size_and = [&](uint32_t x) -> uint32_t {
+          const int key = ((sub * NBS + (NBS == 2 ? lane >> 4 : 0)) * KP + kp) * 16 + (lane & 15);
+          return !MASK || (key >= j0 && key < j1) ? (__float_as_uint(v_sc[key]) & 0x7fffffffu) + x : 0u;
+        };
+        auto is_outside = [&]() { return size_and(__float_as_uint(w_mul) - (251u << 23)) > 11u << 23; };  // (bits of hi / 2^11)
+        const bool outside = I8 && is_outside();
+        // The exponents' base follows the running maximum only when a logit passes it by more than kGrow: most steps then need
+        // neither shuffles nor a rescaling.
+        if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || outside)) {
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {
             nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
             if (!R8) nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
-            if (I8) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
           }
-          nA = fmaxf(nA, mA);
-          nB = fmaxf(nB, mB);
+          float g = 1.f;  // what a larger hi makes of the sums so far
+          if (I8) {
+            const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
+            if (w_mul == 0.f) {
+              const int e = min(max(top + 4, 12), 254);  // hi's exponent, where lo and w_mul are normal
+              w_mul = __uint_as_float((uint32_t)(262 - e) << 23);
+            }
+            if (__any_sync(0xffffffffu, is_outside())) {
+              // far: hi is above every scale so far, and a row's base follows its largest weight times V scale over hi, from
+              // above the earlier ones, but stays within 2^90 of its weights and their sum
+              const int was = hi_exponent(), e = min(max(was, top + 1), 254);
+              w_mul = -__uint_as_float((uint32_t)(262 - e) << 23);
+              g = __uint_as_float((uint32_t)max(127 + was - e, 0) << 23);
+              auto quad_max = [&](float x) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              };
+              nA = fmaxf(fmaxf(nA, mA + __log2f(quad_max(lA))) - 90.f, mA + (float)(was - e));
+              if (!R8) nB = fmaxf(fmaxf(nB, mB + __log2f(quad_max(lB))) - 90.f, mB + (float)(was - e));
+              float yA = -INFINITY, yB = -INFINITY;
+#pragma unroll
+              for (int b = 0; b < NBS; ++b)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const float v = fminf(__log2f(fabsf(i ? sv[b][n].y : sv[b][n].x)), 128.f);  // (an infinity must not move the base)
+                    yA = fmaxf(yA, fmaf(s[b][n][i], cA, v));
+                    if (!R8) yB = fmaxf(yB, fmaf(s[b][n][2 + i], cB, v));
+                  }
+              nA = fmaxf(nA, quad_max(yA) - (float)(e - 127));
+              if (!R8) nB = fmaxf(nB, quad_max(yB) - (float)(e - 127));
+            } else {
+              nA = fmaxf(nA, mA);
+              nB = fmaxf(nB, mB);
+            }
+          } else {
+            nA = fmaxf(nA, mA);
+            nB = fmaxf(nB, mB);
+          }
           const float fA = nA == mA ? 1.f : ex2(mA - nA), fB = R8 ? fA : nB == mB ? 1.f : ex2(mB - nB);
           mA = nA;
           mB = nB;
@@ -748,11 +800,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           if (I8) {
             lA *= fA;
             if (!R8) lB *= fB;
-            big = fmaxf(big, vmax);
-            gA *= vmax / big;
-            gB *= vmax / big;
-            vmax = big;
-            w_mul = kWeight / big;
+            gA *= g;
+            gB *= g;
           } else {
             ls[0] *= fA;
             ls[2] *= fB;
@@ -782,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             if (I8) {
               lA += pA0 + pA1;
               if (!R8) lB += pB0 + pB1;
-              const float w0 = sv[b][n].x * w_mul, w1 = sv[b][n].y * w_mul;
+              const float w0 = sv[b][n].x * fabsf(w_mul), w1 = sv[b][n].y * fabsf(w_mul);
               pA0 *= w0;
               pA1 *= w1;
               pB0 *= w0;
@@ -885,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       lA = R8 ? ls[0] + ls[2] : ls[0];
       lB = ls[2];
     }
-    const float o_mul = I8 ? vmax / kWeight : 1.f;
+    const float o_mul = !I8 ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(fabsf(w_mul)));  // 1 / w_mul
     // values c .. c + 3 of query row g of a (request, head), all tokens joined: the output; or so far: to a place of the
     // workspace
     auto finish = [&](const Part& of, int g, int c, float m, float l, const float* acc) {

@@ -1,0 +1,161 @@
+"""cvr_kv_attend at values where a range or a rounding inside the kernel could show. The bounds count the roundings that
+include/cvr.h states."""
+import math
+
+import pytest
+
+from kv_util import EPS, Cache, assert_within, torch_type
+
+pytestmark = pytest.mark.gpu
+
+GROUPS = [2, 12, 24, 40]  # one for each number of query rows that a tile is made for
+
+
+def call(c, q, scale, window=0):
+    import torch
+    n, heads, _ = q.shape
+    out, lse = torch.full_like(q, 7.0), torch.full((n, heads), 7.0, device="cuda")
+    kv = c.handle(heads, window)
+    kv.attend(n, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), scale, out.data_ptr(), lse.data_ptr())
+    kv.sync()
+    return out, lse
+
+
+def within(c, q, scale, out, split):
+    """Against 64 bits, the bound free of what does not scale with the values. To first order:
+      - logits: the D products' sum loses at most D 2^-23 of sum |q k| scale, the argument of the exponent 4 roundings of |s|;
+        exp2 2^-21; both enter the numerator and the denominator, relative to sum p |v|;
+      - the weights' split into two 16-bit halves: `split`, relative to sum p |v|;
+      - sums over tokens: one add per 16 tokens and 64 for the joins, 2^-23 each, in numerator and denominator;
+      - fp16 weights of 8-bit rows: per token 2^-33 of the row's largest weight times V scale, times codes of up to 127;
+      - the output's rounding: half a step of it, or of the type's smallest subnormal."""
+    import torch
+    ref, bound = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    g, step0 = q.shape[1] // c.heads, {"bf16": 2.0 ** -133, "f16": 2.0 ** -24}[c.dtype]
+    for r in range(q.shape[0]):
+        for h in range(c.heads):
+            n = c.lens_list[r]
+            k, v = c.rows(r, h, 0, n)
+            j = torch.arange(n, device="cuda")
+            v_scale = (c.k_scale if c.shared else c.v_scale)[c.table[r].long()[j // c.page], h, j % c.page].double().abs()
+            rows = slice(h * g, (h + 1) * g)
+            x = q[r, rows].double()
+            s = x @ k.T * scale
+            p = torch.softmax(s, 1)
+            o, size = p @ v, p @ v.abs()
+            ref[r, rows] = o
+            logit = (x.abs() @ k.abs().T * abs(scale)).amax(1, keepdim=True) * c.dim * 2.0 ** -23 + s.abs().amax(1, keepdim=True) * 4 * 2.0 ** -24
+            sums = (n / 16 + 64) * 2.0 ** -23
+            vanish = 2.0 ** -33 * 127 * (p * v_scale).amax(1, keepdim=True) * n
+            bound[r, rows] = EPS[c.dtype] * o.abs() + (2 * (logit + 2.0 ** -21 + sums) + split) * size + vanish + step0 / 2
+    assert_within(out, ref, bound, "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("dim,shared", [(32, False), (64, False), (128, False), (64, True)])
+@pytest.mark.parametrize("at", [[0], [2], [150, 299], [299]])
+def test_a_large_value_without_weight_leaves_the_others_their_bits(dtype, group, dim, shared, at):
+    """Tokens whose V scale is up to 2^40 times the others', which one half of the query rows gives a weight of about 2^-60 and
+    the other half nearly all of its weight."""
+    import torch
+    n = 300
+    c = Cache([n, 17], 2, dim, 16, dtype, "i8", shared=shared, seed=dim + group)
+    q = torch.full((2, 2 * group, dim), 1.0, device="cuda")
+    q[:, 1::2] = -1.0
+    q += 0.01 * torch.randn(q.shape, generator=c.gen, device="cuda")
+    q = q.to(torch_type(dtype))
+    # (fp16: what the large ones give has to be in the type's range, and so do the others')
+    small, large = {("bf16", False): (-6, 34), ("f16", False): (-19, 7), ("bf16", True): (-40, 0), ("f16", True): (-16, 0)}[dtype, shared]
+    for r in range(2):
+        p = c.table[r, :-(-c.lens_list[r] // 16)].long()
+        c.k_scale[p] = 2.0 ** small if shared else 2.0 ** -13
+        if not shared:
+            c.v_scale[p] = 2.0 ** small
+    for j in at:
+        p, i = int(c.table[0, j // 16]), j % 16
+        if shared:  # the logit and the value come from one row: -1 in every place
+            c.k[p, :, i] = -1
+            c.k_scale[p, :, i] = 1.0
+        else:
+            c.k[p, :, i] = -100
+            c.k_scale[p, :, i] = 0.01
+            c.v_scale[p, :, i] = 2.0 ** large
+    scale = 42.0 / dim
+    out, _ = call(c, q, scale)
+    within(c, q, scale, out, 2.0 ** -21)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("log2_v", [-120, -108, -95, 90, 105])
+def test_tiny_and_huge_row_scales_of_values(group, log2_v):
+    import torch
+    c = Cache([200, 3, 33], 2, 64, 16, "bf16", "i8", seed=group)
+    c.v_scale *= 2.0 ** log2_v
+    q = torch.randn((3, 2 * group, 64), generator=c.gen, device="cuda").to(torch.bfloat16)
+    out, _ = call(c, q, 0.125)
+    within(c, q, 0.125, out, 2.0 ** -21)
+
+
+def test_rising_and_falling_row_scales():
+    """V scales that grow by 2^9 from tile to tile, or fall, under weights that fall or grow."""
+    import torch
+    for sign in (1, -1):
+        c = Cache([640, 640], 1, 128, 64, "bf16", "i8", seed=5)
+        q = torch.ones((2, 2, 128), dtype=torch.bfloat16, device="cuda")
+        q[:, 1] = -1
+        for r in range(2):
+            for j in range(10):
+                p = int(c.table[r, j])
+                c.v_scale[p] = 2.0 ** (sign * 9 * (j - 5))
+                c.k[p] = 1 if r == 0 else -1
+                c.k_scale[p] = 8.0 * j / 128
+        out, _ = call(c, q, 1.0)
+        within(c, q, 1.0, out, 2.0 ** -21)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("n,dim", [(700, 32), (20001, 128), (40000, 64)])
+def test_scales_far_apart_in_histories_split_over_the_gpu(group, n, dim):
+    """V scales from 2^-60 to 2^20 and zero ones, in any order. A row's exponents may then begin up to 2^6.4 below its logits, whose
+    argument rounds to 2^-18: weights keep 2^-18.5 more."""
+    import torch
+    c = Cache([n, 5, 90], 1, dim, 64, "bf16", "i8", seed=n + group)
+    e = torch.randint(-60, 21, c.v_scale.shape, generator=c.gen, device="cuda")
+    c.v_scale *= torch.exp2(e.float())
+    c.v_scale[torch.rand(c.v_scale.shape, generator=c.gen, device="cuda") < 0.2] = 0.0
+    q = (torch.randn((3, group, dim), generator=c.gen, device="cuda") * 6).to(torch.bfloat16)
+    out, lse = call(c, q, dim ** -0.5)
+    within(c, q, dim ** -0.5, out, 2.0 ** -17)
+    _, ref, _, bound = c.reference(q, dim ** -0.5)
+    assert_within(lse, ref, bound + 2.0 ** -17, "lse")  # (its base and the sum's logarithm then are up to 90 apart)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+def test_heavy_tokens_without_a_value(group):
+    """Tokens that take nearly all the weight and whose value is zero: what the others leave keeps its bits."""
+    import torch
+    c = Cache([500, 40], 2, 64, 16, "f16", "i8", seed=group)
+    for r in range(2):
+        p = c.table[r, :-(-c.lens_list[r] // 16)].long()
+        c.k_scale[p] = 2.0 ** -12
+        for j in (0, 1, 37):
+            c.k[int(c.table[r, j // 16]), :, j % 16] = 100
+            c.k_scale[int(c.table[r, j // 16]), :, j % 16] = 0.01
+            c.v_scale[int(c.table[r, j // 16]), :, j % 16] = 0.0
+    q = torch.ones((2, 2 * group, 64), dtype=torch.float16, device="cuda")
+    c.v_scale *= 2.0 ** 12
+    out, _ = call(c, q, 18.0 / 64)
+    within(c, q, 18.0 / 64, out, 2.0 ** -20)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_a_scale_that_is_no_number_among_scales_far_apart(group, bad):
+    import torch
+    c = Cache([300, 300], 1, 32, 16, "bf16", "i8", seed=group)
+    c.v_scale *= torch.exp2(torch.randint(-30, 30, c.v_scale.shape, generator=c.gen, device="cuda").float())
+    c.v_scale[int(c.table[0, 9]), 0, 3] = bad
+    q = torch.randn((2, group, 32), generator=c.gen, device="cuda").to(torch.bfloat16)
+    out, lse = call(c, q, 0.2)
+    assert bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all()) and bool(torch.isfinite(lse).all())
