@@ -104,6 +104,20 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
+// the product of two pairs
+template <typename T>
+__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y);
+template <>
+__device__ __forceinline__ uint32_t mul2<__nv_bfloat16>(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t mul2<__half>(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // c (+)= a b; FIRST: the accumulator starts from zero
 template <typename T, bool FIRST = false>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -521,10 +535,15 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const int gid = lane >> 2, tig = lane & 3;
   const int mt = warp % MT, kp = warp / MT;  // row tile, share of the tokens
   const int log2_br = min(a.page_log2, 31 - __clz(TK));
-  // Logits in units of ln 2 are c q . k with c >= 0 (q is negated for a negative scale, and a scale of zero is the least
-  // number above it: a token that is not seen has q . k = -infinity, whose product must stay that).
-  const float c_all = fmaxf(fabsf(a.scale) * kLog2e, 1.4e-45f);
-  const bool negate = a.scale < 0.f;
+  // Logits in units of ln 2 are c q . k with c > 0 (a token that is not seen has q . k = -infinity, whose product must stay
+  // that), q times the scale's sign: -1, 0 or 1. bf16 rows enter times a power of two that brings their largest value to
+  // [1, 2), which goes back into c: q . k alone may leave fp32's range where scale times q does not.
+  const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+  auto factor = [&](uint32_t e) {  // c of rows over 2^(e - 127)
+    return a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * __uint_as_float(e << 23) * kLog2e, 1.4e-45f);
+  };
+  // (the exponents at the type's ends, subnormals' and the highest, take the power beside theirs: both factors are normal)
+  auto row_exponent = [](uint32_t e) { return min(max(e, 1u), 253u); };
   // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8, with
   // 8-bit rows and their V scales over a power of two (below). The two halves hold a weight to 2^-22 of it, or to 2^-25, 2^-33
   // of a weight of 1.
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     uint32_t qf[D / 16][4];
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-    float cA = c_all, cB = c_all;  // logit factors of rows A (gid) and B (gid + 8)
+    float cA = factor(127), cB = cA;  // logit factors of rows A (gid) and B (gid + 8)
     // 8 bits: weight times V scale times |w_mul| enters the second product. |w_mul| is 2^8 / hi, hi a power of two (none yet: 0),
     // and scales in [hi / 2^11, hi] need nothing else: a row's largest weight is 1 or more, so that the halves' 2^-33 hi per
     // token is within 2^-22 of the row's sum. The first scales set hi to 8 to 16 times their largest; one outside starts `far`
@@ -594,18 +613,43 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       const uint8_t* qs = sm + S::oQ + qb * S::kQBytes + mt * 16 * S::kQRow;
       const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
       if (!I8) {
-        const uint32_t flip = negate ? 0x80008000u : 0u;
+        uint32_t bigA = 0, bigB = 0;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 4;
-          qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) ^ flip : 0u;
-          qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) ^ flip : 0u;
-          qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) ^ flip : 0u;
-          qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) ^ flip : 0u;
+          qf[k][0] = inA ? *reinterpret_cast<const uint32_t*>(pa) : 0u;
+          qf[k][2] = inA ? *reinterpret_cast<const uint32_t*>(pa + 16) : 0u;
+          qf[k][1] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow) : 0u;
+          qf[k][3] = inB ? *reinterpret_cast<const uint32_t*>(pa + 8 * S::kQRow + 16) : 0u;
+          bigA = __vmaxu2(bigA, __vmaxu2(qf[k][0] & 0x7fff7fffu, qf[k][2] & 0x7fff7fffu));  // (magnitudes order as their bits)
+          bigB = __vmaxu2(bigB, __vmaxu2(qf[k][1] & 0x7fff7fffu, qf[k][3] & 0x7fff7fffu));
+        }
+        float mulA = sign, mulB = sign;
+        if (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            bigA = __vmaxu2(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
+            if (!R8) bigB = __vmaxu2(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
+          }
+          const uint32_t eA = row_exponent(max(bigA >> 16, bigA & 0xffffu) >> 7), eB = row_exponent(max(bigB >> 16, bigB & 0xffffu) >> 7);
+          mulA *= __uint_as_float((254u - eA) << 23);
+          mulB *= __uint_as_float((254u - eB) << 23);
+          cA = factor(eA);
+          cB = factor(eB);
+        }
+        const uint32_t mA2 = pack2<T>(mulA, mulA), mB2 = pack2<T>(mulB, mulB);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][0] = mul2<T>(qf[k][0], mA2);
+          qf[k][2] = mul2<T>(qf[k][2], mA2);
+          if (!R8) {
+            qf[k][1] = mul2<T>(qf[k][1], mB2);
+            qf[k][3] = mul2<T>(qf[k][3], mB2);
+          }
         }
       } else {
         // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
-        float mulA = 1.f, mulB = 1.f;
+        float mulA = sign, mulB = sign;
         uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -614,8 +658,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
         }
         if (std::is_same<T, __nv_bfloat16>::value) {
-          // bf16 rows enter as fp16 times a power of two that brings their largest value to [1, 2): exact down to 2^-14
-          // of it, 2^-25 of it below
+          // (as fp16: exact down to 2^-14 of the largest value, 2^-25 of it below)
           float bigA = 0.f, bigB = 0.f;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -628,16 +671,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
             bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
           }
-          // (the exponents at the type's ends, subnormals' and the highest, take the power beside theirs: both factors are normal)
-          const uint32_t eA = min(max(__float_as_uint(bigA) >> 23, 1u), 253u), eB = min(max(__float_as_uint(bigB) >> 23, 1u), 253u);
-          mulA = __uint_as_float((254u - eA) << 23);
-          mulB = __uint_as_float((254u - eB) << 23);
-          cA = fmaxf(c_all * __uint_as_float(eA << 23), 1.4e-45f);
-          cB = fmaxf(c_all * __uint_as_float(eB << 23), 1.4e-45f);
-        }
-        if (negate) {
-          mulA = -mulA;
-          mulB = -mulB;
+          const uint32_t eA = row_exponent(__float_as_uint(bigA) >> 23), eB = row_exponent(__float_as_uint(bigB) >> 23);
+          mulA *= __uint_as_float((254u - eA) << 23);
+          mulB *= __uint_as_float((254u - eB) << 23);
+          cA = factor(eA);
+          cB = factor(eB);
         }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {

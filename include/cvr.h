@@ -369,7 +369,8 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  *   scale finite; with the ranking model's temperature 1 / (tau * sqrt(head_dim))
  *   lse   fp32 [n_req][q_heads] natural log of the softmax's denominator; NULL: not written
  * What lies in a page behind the history (or before the window) never reaches the output, whatever its bits. Logits,
- * softmax and sums are fp32: scale times a query value, the logits, and sums of |v| times 2^6 have to lie in its range.
+ * softmax and sums are fp32: scale times a query value, a key value times 2^24, the logits, and sums of |v| times 2^6 have
+ * to lie in its range.
  * With 8-bit pools a weight times its V scale keeps 2^-22 of the largest such product of its query row, however much larger
  * the scales of tokens without weight are (while a row's V scales lie within 2^90 of each other; up to 2^-18 where they are
  * more than 2^11 apart).

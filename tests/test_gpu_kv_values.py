@@ -159,3 +159,41 @@ def test_a_scale_that_is_no_number_among_scales_far_apart(group, bad):
     q = torch.randn((2, group, 32), generator=c.gen, device="cuda").to(torch.bfloat16)
     out, lse = call(c, q, 0.2)
     assert bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("cache", ["same", "i8"])
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("log2_q,log2_k,scale", [(70, 70, 2.0 ** -140), (70, 70, -2.0 ** -140), (100, 100, 0.0), (120, 90, 0.0), (-100, 100, 0.0),
+                                                 (20, 100, 2.0 ** -120), (63, 63, 2.0 ** -126)])
+def test_products_beyond_fp32_before_the_scale(cache, group, log2_q, log2_k, scale):
+    """Only scale times q, the keys times 2^24 and the logits have to lie in fp32's range, not q . k."""
+    import torch
+    c = Cache([1, 50, 333], 2, 64, 16, "bf16", cache, seed=22)
+    for r, n in enumerate(c.lens_list):
+        p = c.table[r, :-(-n // 16)].long()
+        if cache == "i8":
+            c.k_scale[p] *= 2.0 ** log2_k
+        else:
+            c.k[p] = (c.k[p].float() * 2.0 ** log2_k).to(c.k.dtype)  # (exact: powers of two, far from the type's ends)
+    q = (torch.randn((3, 2 * group, 64), generator=c.gen, device="cuda").clamp(-1.9, 1.9) * 2.0 ** log2_q).to(torch.bfloat16)
+    out, lse = call(c, q, scale)
+    ref, ref_lse, b_out, b_lse = c.reference(q, scale)
+    assert_within(lse, ref_lse, b_lse, "lse")
+    assert_within(out, ref, b_out, "out")
+
+
+@pytest.mark.parametrize("cache", ["same", "i8"])
+def test_a_scale_of_zero_keeps_what_is_no_number(cache):
+    """0 times an infinity is no number: a scale of zero does not hide a bad query or key row, and spares the others."""
+    import torch
+    c = Cache([20, 20], 1, 32, 16, "bf16", cache, seed=3)
+    q = torch.ones((2, 4, 32), dtype=torch.bfloat16, device="cuda")
+    q[0, 1, 3] = math.inf
+    q[0, 2, 5] = math.nan
+    if cache == "i8":
+        c.k_scale[int(c.table[1, 0]), 0, 2] = math.inf
+    else:
+        c.k[int(c.table[1, 0]), 0, 2, 7] = math.inf
+    out, lse = call(c, q, 0.0)
+    assert bool(torch.isnan(out[0, 1:3]).all()) and bool(torch.isnan(out[1]).all()) and bool(torch.isnan(lse[1]).all())
+    assert bool(torch.isfinite(out[0, [0, 3]]).all()) and bool(torch.isfinite(lse[0, [0, 3]]).all())
