@@ -19,9 +19,9 @@
 //   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-9 in bf16) does not add to
 //     the output's. With at most 8 query rows the halves sit in the two halves of the 16-row tile, at no extra cost.
 //   - 8-bit rows become fp16 exactly (1024 + q by a byte permute, minus 1152); K's scale multiplies the logit, V's scale
-//     the weight, whose products enter as fp16 over a divisor that the first scales choose. Where scales lie farther apart
-//     than the halves' bits allow, a row's exponents get a base of their own that follows its largest product, so that a large
-//     scale without weight leaves the other tokens their bits.
+//     the weight, whose products enter as fp16 times a power of two that the first scales choose. Where scales lie farther apart
+//     than the halves' bits allow, each query row has its own, which follows the row's largest product, so that a large scale
+//     without weight leaves the other tokens their bits.
 //
 // Measured (one GB300, copy rate 6.67 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128, bf16: 113 us, 6.5 TB/s;
 // one request of 131071: 85 us, 6.3 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 74 us, 5.2 TB/s,
@@ -592,13 +592,14 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     float cA = factor(127), cB = cA;  // logit factors of rows A (gid) and B (gid + 8)
-    // 8 bits: weight times V scale times |w_mul| enters the second product. |w_mul| is 2^8 / hi, hi a power of two (none yet: 0),
-    // and scales in [hi / 2^11, hi] need nothing else: a row's largest weight is 1 or more, so that the halves' 2^-33 hi per
-    // token is within 2^-22 of the row's sum. The first scales set hi to 8 to 16 times their largest; one outside starts `far`
-    // below, and w_mul is negative from then on, which puts every scale outside: 32 requests of 1 to 16383 tokens 73.6 us with
-    // scales within 4 of each other, 81.6 us with scales within 2^16.
-    float w_mul = 0.f;
-    auto hi_exponent = [&]() { return 262 - (int)(__float_as_uint(fabsf(w_mul)) >> 23); };
+    // 8 bits: weight times V scale times |mul| enters the second product. Rows A and B have the same 2^8 / hi (none yet: 0), hi
+    // a power of two, as long as the scales lie in [hi / 2^11, hi]: a row's largest weight is 1 or more, so that the halves'
+    // 2^-33 hi per token is within 2^-22 of the row's sum. The first scales set hi to 8 to 16 times their largest; one outside
+    // makes the rows `far` below: powers of two of their own, that of A negative, which puts every scale outside. 32 requests of 1
+    // to 16383 tokens: 73.3 us with scales within 4 of each other, 80.6 us with scales within 2^16.
+    float mulA = 0.f, mulB = 0.f;
+    auto exponent = [](float x) { return (int)(__float_as_uint(x) >> 23 & 255u); };
+    auto power = [](int e) { return __uint_as_float((uint32_t)e << 23); };
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -774,14 +775,16 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
             if (!R8) nB = fmaxf(nB, fmaxf(s[b][n][2], s[b][n][3]));
           }
-        nA *= cA;
-        if (!R8) nB *= cB;
+        // (rounded before the base is taken off, as the base was: a rest of the product's bits would be far above 0 in a large one)
+        auto logit = [](float s, float c) { return __fmul_rn(s, c); };
+        nA = logit(nA, cA);
+        if (!R8) nB = logit(nB, cB);
         // 8 bits: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
         auto size_and = [&](uint32_t x) -> uint32_t {
           const int key = ((sub * NBS + (NBS == 2 ? lane >> 4 : 0)) * KP + kp) * 16 + (lane & 15);
           return !MASK || (key >= j0 && key < j1) ? (__float_as_uint(v_sc[key]) & 0x7fffffffu) + x : 0u;
         };
-        auto is_outside = [&]() { return size_and(__float_as_uint(w_mul) - (251u << 23)) > 11u << 23; };  // (bits of hi / 2^11)
+        auto is_outside = [&]() { return size_and(__float_as_uint(mulA) - (251u << 23)) > 11u << 23; };  // (less the bits of hi / 2^11)
         const bool outside = I8 && is_outside();
         // The exponents' base follows the running maximum only when a logit passes it by more than kGrow: most steps then need
         // neither shuffles nor a rescaling.
@@ -791,55 +794,45 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
             if (!R8) nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
           }
-          float g = 1.f;  // what a larger hi makes of the sums so far
-          if (I8) {
-            const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
-            if (w_mul == 0.f) {
-              const int e = min(max(top + 4, 12), 254);  // hi's exponent, where lo and w_mul are normal
-              w_mul = __uint_as_float((uint32_t)(262 - e) << 23);
-            }
-            if (__any_sync(0xffffffffu, is_outside())) {
-              // far: hi is above every scale so far, and a row's base follows its largest weight times V scale over hi, from
-              // above the earlier ones, but stays within 2^90 of its weights and their sum
-              const int was = hi_exponent(), e = min(max(was, top + 1), 254);
-              w_mul = -__uint_as_float((uint32_t)(262 - e) << 23);
-              g = __uint_as_float((uint32_t)max(127 + was - e, 0) << 23);
-              auto quad_max = [&](float x) {
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              };
-              nA = fmaxf(fmaxf(nA, mA + __log2f(quad_max(lA))) - 90.f, mA + (float)(was - e));
-              if (!R8) nB = fmaxf(fmaxf(nB, mB + __log2f(quad_max(lB))) - 90.f, mB + (float)(was - e));
-              float yA = -INFINITY, yB = -INFINITY;
-#pragma unroll
-              for (int b = 0; b < NBS; ++b)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    const float v = fminf(__log2f(fabsf(i ? sv[b][n].y : sv[b][n].x)), 128.f);  // (an infinity must not move the base)
-                    yA = fmaxf(yA, fmaf(s[b][n][i], cA, v));
-                    if (!R8) yB = fmaxf(yB, fmaf(s[b][n][2 + i], cB, v));
-                  }
-              nA = fmaxf(nA, quad_max(yA) - (float)(e - 127));
-              if (!R8) nB = fmaxf(nB, quad_max(yB) - (float)(e - 127));
-            } else {
-              nA = fmaxf(nA, mA);
-              nB = fmaxf(nB, mB);
-            }
-          } else {
-            nA = fmaxf(nA, mA);
-            nB = fmaxf(nB, mB);
-          }
+          nA = fmaxf(nA, mA);
+          nB = fmaxf(nB, mB);
           const float fA = nA == mA ? 1.f : ex2(mA - nA), fB = R8 ? fA : nB == mB ? 1.f : ex2(mB - nB);
+          const float upA = mA - nA, upB = mB - nB;
           mA = nA;
           mB = nB;
           float gA = fA, gB = fB;
           if (I8) {
             lA *= fA;
             if (!R8) lB *= fB;
-            gA *= g;
-            gB *= g;
+            const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
+            if (mulA == 0.f) mulA = mulB = power(262 - min(max(top + 4, 12), 254));
+            if (__any_sync(0xffffffffu, is_outside())) {
+              // far: the row's largest weight times V scale becomes 2^7 to 2^8, unless what was summed so far holds a larger one, and
+              // a scale times mul stays finite (its weight may be zero)
+              const float subA = mA == -INFINITY ? 0.f : mA, subB = mB == -INFINITY ? 0.f : mB;
+              float xA = 0.f, xB = 0.f;
+#pragma unroll
+              for (int b = 0; b < NBS; ++b)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const float v = i ? sv[b][n].y : sv[b][n].x;
+                    xA = fmaxf(xA, fabsf(ex2(logit(s[b][n][i], cA) - subA) * v));
+                    if (!R8) xB = fmaxf(xB, fabsf(ex2(logit(s[b][n][2 + i], cB) - subB) * v));
+                  }
+              auto follow = [&](float x, float f, float up, float& mul) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                const int was = exponent(mul), held = f == 1.f ? was : exponent(fabsf(mul) * ex2(-up));
+                const int e = min(max(min(min(held, 261 - exponent(x)), 379 - top), 8), 250);
+                mul = power(e);
+                return f == 1.f ? power(127 + max(e - was, -127)) : ex2(up + (float)(e - was));
+              };
+              gA = follow(xA, fA, upA, mulA);
+              mulA = -mulA;
+              if (!R8) gB = follow(xB, fB, upB, mulB);
+            }
           } else {
             ls[0] *= fA;
             ls[2] *= fB;
@@ -861,19 +854,20 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           uint32_t hi[4], lw[4];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float pA0 = ex2(fmaf(s[b][n][0], cA, subA)), pA1 = ex2(fmaf(s[b][n][1], cA, subA)), pB0 = 0.f, pB1 = 0.f;
+            float pA0 = ex2(logit(s[b][n][0], cA) + subA), pA1 = ex2(logit(s[b][n][1], cA) + subA), pB0 = 0.f, pB1 = 0.f;
             if (!R8) {
-              pB0 = ex2(fmaf(s[b][n][2], cB, subB));
-              pB1 = ex2(fmaf(s[b][n][3], cB, subB));
+              pB0 = ex2(logit(s[b][n][2], cB) + subB);
+              pB1 = ex2(logit(s[b][n][3], cB) + subB);
             }
             if (I8) {
               lA += pA0 + pA1;
               if (!R8) lB += pB0 + pB1;
-              const float w0 = sv[b][n].x * fabsf(w_mul), w1 = sv[b][n].y * fabsf(w_mul);
-              pA0 *= w0;
-              pA1 *= w1;
-              pB0 *= w0;
-              pB1 *= w1;
+              pA0 *= sv[b][n].x * fabsf(mulA);
+              pA1 *= sv[b][n].y * fabsf(mulA);
+              if (!R8) {
+                pB0 *= sv[b][n].x * mulB;
+                pB1 *= sv[b][n].y * mulB;
+              }
             }
             const uint32_t hA = pack2<M>(pA0, pA1);
             const float2 fA = unpack2<M>(hA);
@@ -972,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       lA = R8 ? ls[0] + ls[2] : ls[0];
       lB = ls[2];
     }
-    const float o_mul = !I8 ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(fabsf(w_mul)));  // 1 / w_mul
+    const float o_mulA = I8 ? power(254 - exponent(mulA)) : 1.f, o_mulB = I8 ? power(254 - exponent(mulB)) : 1.f;  // (1 / mul)
     // values c .. c + 3 of query row g of a (request, head), all tokens joined: the output; or so far: to a place of the
     // workspace
     auto finish = [&](const Part& of, int g, int c, float m, float l, const float* acc) {
@@ -1002,6 +996,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         const bool upper = half != 0;
         if (mt * 16 + upper * 8 + gid >= G) continue;
         const int row = warp * S::kORows + half * 8 + gid;
+        const float o_mul = upper ? o_mulB : o_mulA;
         float* dst = s_o + row * S::kORow;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {

@@ -372,8 +372,7 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  * softmax and sums are fp32: scale times a query value, a key value times 2^24, the logits, and sums of |v| times 2^6 have
  * to lie in its range.
  * With 8-bit pools a weight times its V scale keeps 2^-22 of the largest such product of its query row, however much larger
- * the scales of tokens without weight are (while a row's V scales lie within 2^90 of each other; up to 2^-18 where they are
- * more than 2^11 apart).
+ * the scales of tokens without weight are.
  * Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length outside
  * [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read; out is not
  * meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not
