@@ -551,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
-  constexpr uint32_t kOnes = std::is_same<M, __half>::value ? 0x3c003c00u : 0x3f803f80u;
+  // fp16 weights are summed by a product of their halves, 2^-22 of each, with ones; others as they are (bf16's halves hold 2^-17)
+  constexpr bool kOnesSum = kF16;
+  constexpr uint32_t kOnes = 0x3c003c00u;  // 1, 1
   uint32_t meets = 0;
   bool ok = true;
   auto consumer_sync = [&]() {  // a bounded barrier of the four warps
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   for (bool last = !some; !last;) {
     // ---- a part: the tiles of one (request, head) in this CTA's run ----
     uint32_t qf[D / 16][4];
-    float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: 16 bits: sums of the weights, a product with ones
+    float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: sums of the weights by products
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     float cA = factor(127), cB = cA;  // logit factors of rows A (gid) and B (gid + 8)
     // 8 bits: weight times V scale times |mul| enters the second product. Rows A and B have the same 2^8 / hi (none yet: 0), hi
@@ -801,9 +803,14 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           mA = nA;
           mB = nB;
           float gA = fA, gB = fB;
-          if (I8) {
+          if (kOnesSum) {
+            ls[0] *= fA;
+            ls[2] *= fB;
+          } else {
             lA *= fA;
             if (!R8) lB *= fB;
+          }
+          if (I8) {
             const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
             if (mulA == 0.f) mulA = mulB = power(262 - min(max(top + 4, 12), 254));
             if (__any_sync(0xffffffffu, is_outside())) {
@@ -833,9 +840,6 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               mulA = -mulA;
               if (!R8) gB = follow(xB, fB, upB, mulB);
             }
-          } else {
-            ls[0] *= fA;
-            ls[2] *= fB;
           }
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
@@ -859,9 +863,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               pB0 = ex2(logit(s[b][n][2], cB) + subB);
               pB1 = ex2(logit(s[b][n][3], cB) + subB);
             }
-            if (I8) {
+            if (!kOnesSum) {
               lA += pA0 + pA1;
               if (!R8) lB += pB0 + pB1;
+            }
+            if (I8) {
               pA0 *= sv[b][n].x * fabsf(mulA);
               pA1 *= sv[b][n].y * fabsf(mulA);
               if (!R8) {
@@ -883,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               lw[2 * n + 1] = pack2<M>(pB0 - fB.x, pB1 - fB.y);
             }
           }
-          if (!I8) {
+          if (kOnesSum) {
             mma16816<M>(ls, hi, kOnes, kOnes);
             if (!R8) mma16816<M>(ls, lw, kOnes, kOnes);
           }
@@ -956,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     }
 
     // ---- the part's end: the warps' (m, l, o) to shared memory, and summed ----
-    if (I8) {
+    if (!kOnesSum) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
         lA += __shfl_xor_sync(0xffffffffu, lA, d);
@@ -974,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       T* dst = static_cast<T*>(a.out) + (int64_t)of.r * a.out_stride + (int64_t)qh * D + c;
       const float inv = 1.f / l;
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv));
-      if (c == 0 && a.lse) a.lse[(int64_t)of.r * a.q_heads + qh] = ((m == -INFINITY ? 0.f : m) - kShift) * kLn2 + logf(l);
+      if (c == 0 && a.lse) a.lse[(int64_t)of.r * a.q_heads + qh] = (m == -INFINITY ? 0.f : m) * kLn2 + logf(l * (kF16 ? 0x1p-8f : 1.f));
     };
     auto keep = [&](int to, int g, int c, float m, float l, const float* acc) {
       __stcg(reinterpret_cast<float4*>(a.part_o + ((int64_t)to * G + g) * D + c), make_float4(acc[0], acc[1], acc[2], acc[3]));

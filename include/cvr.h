@@ -371,8 +371,10 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  * What lies in a page behind the history (or before the window) never reaches the output, whatever its bits. Logits,
  * softmax and sums are fp32: scale times a query value, a key value times 2^24, the logits, and sums of |v| times 2^6 have
  * to lie in its range.
- * With 8-bit pools a weight times its V scale keeps 2^-22 of the largest such product of its query row, however much larger
- * the scales of tokens without weight are.
+ * Weights enter the sum over v as two 16-bit halves: with bf16 pools to 2^-16 of a weight, with fp16 pools to 2^-22 of it or
+ * 2^-33 of its query row's largest, with 8-bit pools, times the V scale, to 2^-22 of it or of the row's largest such product,
+ * however much larger the scales of tokens without weight are. bf16 queries on 8-bit pools are held in fp16 relative to their
+ * row's largest value: exact down to 2^-14 of it, to 2^-25 of it below.
  * Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length outside
  * [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read; out is not
  * meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not

@@ -229,3 +229,28 @@ def test_logits_of_any_size_pick_the_largest(dtype, cache, group, apart, log2):
             bound = EPS[dtype] * want.abs() + 2.0 ** -20 * want.abs().amax() + {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}[dtype]
             assert bool(((out[0, h * group + i].double() - want).abs() <= bound).all())
             assert abs(float(lse[0, h * group + i]) - logit) <= abs(logit) * 2.0 ** -21
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "i8"), ("f16", "i8")])
+@pytest.mark.parametrize("group", [1, 3, 16, 40])
+def test_the_sum_of_few_weights_is_fp32(dtype, cache, group):
+    """Two tokens, the first logit 0, the second s in (-0.7, 0): lse = ln(1 + e^s). Each logit is one exact product. What
+    rounds: the exponent's factor and argument (3 half steps of |s| log2 e <= 1.01 at 2^-24, and with fp16 weights, whose
+    exponents begin at 8, 2^-22) times ln 2, exp2 (2^-22 relative) and fp16's split (2^-22), all three times
+    e^s / (1 + e^s) <= 1/2; the sum (2^-23 of it); ln and its scalings (4 half steps of 0.7). In all
+    (3 * 2^-24 * 1.01 + 2^-22) ln 2 / 2 + 2^-23 + 2^-23 + 2^-23 + 0.7 * 4 * 2^-24 < 2^-20.5."""
+    import torch
+    n = 400
+    c = Cache([2] * n, 1, 32, 8, dtype, cache, seed=group)
+    p = c.table[:, 0].long()
+    c.k[p, :, :2] = 0
+    step = 64 if cache == "i8" else 1
+    c.k[p, 0, 1, 5] = -step
+    if cache == "i8":
+        c.k_scale[p] = 1.0 / step
+    q = torch.zeros((n, group, 32), device="cuda")
+    q[:, :, 5] = torch.rand((n, group), generator=c.gen, device="cuda") * 0.69
+    q = q.to(torch_type(dtype))
+    _, lse = call(c, q, 1.0)
+    want = torch.log1p(torch.exp(-q[:, :, 5].double()))
+    assert float((lse.double() - want).abs().max()) <= 2.0 ** -20.5
