@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     if (two) tma_prefetch_desc(&tm_v);
   }
   pdl_trigger();
-  pdl_wait();
+  pdl_wait();  // (lengths and page ids are read with plain loads: an earlier call may have written them while this one started)
 
   // ---- this CTA's run of the line of tiles: every thread sums a few requests' tiles, saturating ----
   const int few = (a.n_req + kThreads - 1) / kThreads;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   int nonempty = 0;
   bool bad = false;
   for (int r = r0; r < r1; ++r) {
-    const int raw = __ldg(a.lens + r), len = clamped_len(a, raw);
+    const int raw = a.lens[r], len = clamped_len(a, raw);
     bad |= raw != len;
     mine = add(mine, tiles_of<TK>(a, len));
     nonempty += len > 0;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   } else if (__builtin_expect(per > 1 && per < 8 && a.n_req * H <= grid && (a.n_req > 1 || (int)line.all > per), 0)) {
     uint32_t filled_up = 0;
 #pragma unroll 1
-    for (int r = r0; r < r1; ++r) filled_up += whole_runs(tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r))), per);
+    for (int r = r0; r < r1; ++r) filled_up += whole_runs(tiles_of<TK>(a, clamped_len(a, a.lens[r])), per);
     const Scanned l = scan_block_again(filled_up, s_sum + 8);
     if ((uint64_t)l.all * H <= (uint64_t)grid * per) {
       pad = per;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   if (some && begin >= (int)before * H && begin < (int)(before + mine) * H) {
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      const int n = r1 - r0 == 1 ? (int)mine : extent(tiles_of<TK>(a, clamped_len(a, __ldg(a.lens + r))));
+      const int n = r1 - r0 == 1 ? (int)mine : extent(tiles_of<TK>(a, clamped_len(a, a.lens[r])));
       if (begin < ((int)before + n) * H) {
         s_start[0] = r;
         s_start[1] = (int)before;
@@ -375,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       // Page ids come 32 entries of a table row at a time, one per lane, and ahead of their use: the row's next 32, and the
       // first 32 of the next request. A tile's entries never straddle two batches (both begin at a multiple of its count).
       auto entries = [&](int row, int e) {
-        return e + lane < a.max_pages ? __ldg(a.table + (int64_t)row * a.max_pages + e + lane) : 0;
+        return e + lane < a.max_pages ? a.table[(int64_t)row * a.max_pages + e + lane] : 0;
       };
       int wb = s_start[0], wl = 0;  // lengths of the 32 requests from wb on, one per lane
       auto window = [&](int from) {
         wb = from;
-        wl = wb + lane < a.n_req ? clamped_len(a, __ldg(a.lens + wb + lane)) : 0;
+        wl = wb + lane < a.n_req ? clamped_len(a, a.lens[wb + lane]) : 0;
       };
       auto first_entry = [&](int length) { return (seen_from(a, length) / TK * TK) >> a.page_log2; };
       // the next request with a tile from `from` on (n_req: none), its length and first page ids
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     // requests that see nothing, shared out over the grid: this CTA's are blockIdx, blockIdx + grid, ..
     for (int64_t r0 = blockIdx.x; r0 < a.n_req; r0 += 32 * (int64_t)gridDim.x) {
       const int64_t mine = r0 + (int64_t)lane * gridDim.x;
-      unsigned none = __ballot_sync(0xffffffffu, mine < a.n_req && clamped_len(a, __ldg(a.lens + min(mine, (int64_t)a.n_req - 1))) == 0);
+      unsigned none = __ballot_sync(0xffffffffu, mine < a.n_req && clamped_len(a, a.lens[min(mine, (int64_t)a.n_req - 1)]) == 0);
       for (; none; none &= none - 1) {
         const int64_t r = r0 + (int64_t)(__ffs(none) - 1) * gridDim.x;
         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + r * a.out_stride);

@@ -33,8 +33,9 @@ struct TabReq {
 __device__ __forceinline__ TabReq tab_request(const KvTablesArgs& a, int r, int* bad) {
   TabReq q = {0, 0, 0, 0};
   if (r >= a.n_req) return q;
+  // (plain loads, here and below: an earlier call of the stream may have written these arrays while this one started)
   const int most = a.max_pages << a.page_log2;  // (at most 2^30)
-  const int len = __ldg(a.lens + r), nw = a.new_lens ? __ldg(a.new_lens + r) : 1, held = a.held ? __ldg(a.held + r) : 0;
+  const int len = a.lens[r], nw = a.new_lens ? a.new_lens[r] : 1, held = a.held ? a.held[r] : 0;
   q.len = min(max(len, 0), most);
   q.n_new = a.new_lens ? min(max(nw, 0), q.len) : min(q.len, 1);
   q.held = min(max(held, 0), a.max_pages);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
   int bad = 0;
   pdl_trigger();
   pdl_wait();
-  int head = a.free_head ? __ldg(a.free_head) : 0;
+  int head = a.free_head ? *a.free_head : 0;
   // ---- sums over every thread's run of requests (one request each for at most 512) ----
   const int run = (a.n_req + kTabThreads - 1) / kTabThreads;
   TabReq q = {0, 0, 0, 0};
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
           auto id_of = [&](int j) {
             const bool fresh = j >= held;
             if (j > j_end || (fresh && at0 + j >= (uint32_t)a.n_free)) return kNoPage;
-            return max(fresh ? __ldg(a.free_pages + (at0 + j)) : row[j], -1);
+            return max(fresh ? a.free_pages[at0 + j] : row[j], -1);
           };
           int j = (pos0 + (int)b) >> a.page_log2, next = id_of(j + lane);
           for (uint32_t y0 = b; y0 < stop; j += 32) {
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
         } else {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            page[u] = max(__ldg(a.free_pages + min(at[u], (uint32_t)a.n_free - 1)), -1);
+            page[u] = max(a.free_pages[min(at[u], (uint32_t)a.n_free - 1)], -1);
             if (at[u] >= (uint32_t)a.n_free) page[u] = kNoPage;
           }
         }
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
       uint4 row[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        row[w] = ok && a.src[w] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.src[w]) + tok * a.src_stride[w]) + c)
+        row[w] = ok && a.src[w] ? *(reinterpret_cast<const uint4*>(static_cast<const T*>(a.src[w]) + tok * a.src_stride[w]) + c)
                                 : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {

@@ -1,0 +1,58 @@
+"""Calls of the paged history cache as a program may make them: without waits between them, while streams capture, with
+arrays that overlap or are not aligned, with very many requests."""
+import math
+
+import pytest
+
+from kv_util import Cache, assert_within, torch_type
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(x, kind="int32"):
+    import torch
+    return torch.tensor(x, dtype=getattr(torch, kind), device="cuda")
+
+
+@pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("i8", "f16")])
+def test_a_chain_of_calls_without_a_wait(cache, dtype):
+    """Steps of tables, append and attend directly behind one another, each step with arrays of its own: every kernel starts
+    while the ones before it still write what it reads."""
+    import torch
+    n, heads, group, dim, page, steps = 9, 2, 2, 64, 8, 40
+    c = Cache([0] * n, heads, dim, page, dtype, cache, max_pages=16, spare=n * 16, seed=5)
+    for x in (c.k_scale, c.v_scale):
+        if x is not None:
+            x.fill_(math.nan)
+    lens = [[r + s * (r + 1) // 9 for r in range(n)] for s in range(steps)]
+    new = [[b if s == 0 else b - a for a, b in zip(lens[s - 1], lens[s])] for s in range(steps)]
+    most = max(sum(x) for x in new)
+    t_lens, t_new = dev(lens), dev(new)
+    rows = torch.randn((steps, 2, most, heads, dim), generator=c.gen, device="cuda").to(torch_type(dtype))
+    q = torch.randn((steps, n, heads * group, dim), generator=c.gen, device="cuda").to(torch_type(dtype))
+    free = torch.randperm(c.n_pages, device="cuda").to(torch.int32)
+    results = []
+    for waits in (False, True, False):
+        held, head = torch.zeros((steps + 1, n), dtype=torch.int32, device="cuda"), torch.zeros(steps + 1, dtype=torch.int32, device="cuda")
+        slots, out = torch.zeros((steps, most), dtype=torch.int64, device="cuda"), torch.zeros_like(q)
+        c.table.fill_(-1)
+        torch.cuda.synchronize()
+        kv = c.handle(heads * group)
+        for s in range(steps):
+            kv.tables(n, t_lens[s].data_ptr(), c.table.data_ptr(), t_new[s].data_ptr(), held[s].data_ptr(), free.data_ptr(), c.n_pages,
+                      head[s:].data_ptr(), held[s + 1].data_ptr(), head[s + 1:].data_ptr(), slots[s].data_ptr(), most)
+            if waits:
+                kv.sync()
+            kv.append(most, slots[s].data_ptr(), rows[s, 0].data_ptr(), rows[s, 1].data_ptr())
+            if waits:
+                kv.sync()
+            kv.attend(n, q[s].data_ptr(), t_lens[s].data_ptr(), c.table.data_ptr(), 0.125, out[s].data_ptr())
+            if waits:
+                kv.sync()
+        kv.sync()
+        results.append((held, head, slots, out, c.table.clone()))
+    for other in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(results[0], other))
+    c.lens_list = lens[-1]
+    ref, _, bound, _ = c.reference(q[-1], 0.125)
+    assert_within(results[0][3][-1], ref, bound, "out")
