@@ -58,6 +58,24 @@ struct OnDevice {
   }
 };
 
+// Lets a call allocate, free and wait while a stream other than its own captures a graph in the calling thread's or the
+// global mode, which would end that capture: none of them touches it.
+struct BesideCaptures {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Whether the stream captures, or is the legacy stream while a blocking one does (whose capture any use of it would end).
+cudaError_t captures(cudaStream_t s, bool* yes) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &status);
+  *yes = e == cudaErrorStreamCaptureImplicit || (e == cudaSuccess && status != cudaStreamCaptureStatusNone);
+  if (e == cudaSuccess) return e;
+  cudaGetLastError();
+  return *yes ? cudaSuccess : e;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int elt_bytes(int dtype) { return dtype == CVR_DTYPE_I8 ? 1 : 2; }
@@ -185,18 +203,18 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
     return CVR_E_ARG;
   }
   // (a captured clearing of the counters would run with the graph only)
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(cuda_stream), &capturing) != cudaSuccess) cudaGetLastError();
-  if (capturing != cudaStreamCaptureStatusNone) {
-    fprintf(stderr, "cvr_kv_create: the stream is capturing a graph\n");
-    return CVR_E_ARG;
-  }
+  bool capturing = false;
+  cudaError_t e = captures(static_cast<cudaStream_t>(cuda_stream), &capturing);
+  if (capturing) fprintf(stderr, "cvr_kv_create: the stream is capturing a graph, or another one that it would wait for\n");
+  else if (e != cudaSuccess) fprintf(stderr, "cvr_kv_create: %s\n", cudaGetErrorString(e));
+  if (capturing || e != cudaSuccess) return capturing ? CVR_E_ARG : CVR_E_CUDA;
+  BesideCaptures beside;
   cvr_kv* h = new (std::nothrow) cvr_kv();
   if (!h) return CVR_E_OOM;
   h->cfg = *cfg;
   h->stream = static_cast<cudaStream_t>(cuda_stream);
   while ((1 << h->page_log2) < cfg->page_size) ++h->page_log2;
-  cudaError_t e = cudaGetDevice(&h->device);
+  e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) e = cudaHostAlloc(reinterpret_cast<void**>(&h->err_host), 64, cudaHostAllocMapped);
   if (e == cudaSuccess) {
@@ -378,6 +396,7 @@ void cvr_kv_destroy(cvr_kv* h) {
   if (!h) return;
   {
     OnDevice on(h->device);
+    BesideCaptures beside;
     if (h->err_host) {  // (a handle whose creation failed has nothing in flight)
       cudaStreamSynchronize(h->stream);
       cudaFreeHost(h->err_host);

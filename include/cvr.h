@@ -325,8 +325,9 @@ typedef struct {
 } cvr_kv_config;
 
 /* Creates a handle on the current CUDA device, working on `cuda_stream` (NULL = the legacy default stream).
- * CVR_E_ARG for a bad configuration or a stream that is capturing (reason on stderr), CVR_E_OOM / CVR_E_CUDA on device
- * failures. */
+ * CVR_E_ARG for a bad configuration, a stream that is capturing, or the legacy stream while a blocking stream captures (reason
+ * on stderr), CVR_E_OOM / CVR_E_CUDA on device failures. Captures of other streams are left as they are, here and in
+ * cvr_kv_destroy. */
 cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** out);
 
 /* Block tables and slot maps for n_req requests (0 <= n_req <= max_req), all arrays DEVICE:

@@ -56,3 +56,70 @@ def test_a_chain_of_calls_without_a_wait(cache, dtype):
     c.lens_list = lens[-1]
     ref, _, bound, _ = c.reference(q[-1], 0.125)
     assert_within(results[0][3][-1], ref, bound, "out")
+
+
+def small(seed, q_heads=8):
+    import torch
+    c = Cache([300, 20], 2, 64, 16, "bf16", seed=seed)
+    q = torch.randn((2, q_heads, 64), generator=c.gen, device="cuda").to(torch.bfloat16)
+    return c, q, torch.zeros_like(q)
+
+
+def attend(kv, c, q, out):
+    kv.attend(2, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.1, out.data_ptr())
+
+
+def check(c, q, out):
+    ref, _, bound, _ = c.reference(q, 0.1)
+    assert_within(out, ref, bound, "out")
+
+
+def test_a_handle_of_another_stream_while_a_stream_captures():
+    """A handle may be made, used and destroyed on a stream of its own while another stream captures in the default
+    (global) mode, and the capture goes on."""
+    import torch
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    c, q, out = small(1)
+    out2 = torch.zeros_like(out)
+    kv = c.handle(8, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        attend(kv, c, q, out)
+        kv2 = c.handle(8, stream=other.cuda_stream)
+        attend(kv2, c, q, out2)
+        kv2.close()
+        attend(kv, c, q, out)
+    check(c, q, out2)
+    with torch.cuda.stream(s):
+        graph.replay()
+    kv.sync()
+    check(c, q, out)
+
+
+def test_the_legacy_stream_is_refused_while_a_blocking_stream_captures():
+    """A blocking stream's capture makes the legacy default stream unusable: a handle is not made on it, and the capture goes
+    on."""
+    import ctypes
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    raw = ctypes.c_void_p()
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(raw))) == 0
+    s = torch.cuda.ExternalStream(raw.value)
+    c, q, out = small(3)
+    kv = c.handle(8, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s, capture_error_mode="relaxed"):
+        with pytest.raises(cvr.CvrError) as made:
+            c.handle(8)
+        attend(kv, c, q, out)
+    assert made.value.status == 1
+    with torch.cuda.stream(s):
+        graph.replay()
+    kv.sync()
+    check(c, q, out)
+    kv.close()
+    torch.cuda.synchronize()
+    del graph
+    assert int(torch.cuda.cudart().cudaStreamDestroy(raw.value)) == 0
