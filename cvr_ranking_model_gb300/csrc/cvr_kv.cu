@@ -370,7 +370,11 @@ cvr_status cvr_kv_sync(cvr_kv* h) {
   if (!h) return CVR_E_ARG;
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
-  const cudaError_t e = cudaStreamSynchronize(h->stream);
+  bool capturing = false;
+  cudaError_t e = captures(h->stream, &capturing);
+  if (capturing) return kv_fail(h, CVR_E_ARG, "the stream is capturing a graph, or another one that it would wait for");
+  BesideCaptures beside;
+  if (e == cudaSuccess) e = cudaStreamSynchronize(h->stream);
   if (e != cudaSuccess) return kv_cuda_fail(h, e, "cvr_kv_sync");
   volatile int* word = h->err_host;
   const int ew = *word;

@@ -383,7 +383,8 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
 cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
                          const int32_t* table, float scale, void* out, int64_t out_stride, float* lse);
 
-/* Waits for the handle's stream; the status of the device-side checks since the previous cvr_kv_sync. */
+/* Waits for the handle's stream; the status of the device-side checks since the previous cvr_kv_sync. CVR_E_ARG while the
+ * stream captures (or, for the legacy stream, a blocking stream does): nothing is waited for and the capture goes on. */
 cvr_status cvr_kv_sync(cvr_kv* h);
 const char* cvr_kv_last_error(const cvr_kv* h);
 /* Waits for the stream and frees the handle's memory (not the pools). NULL is ignored. */

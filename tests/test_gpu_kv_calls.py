@@ -75,7 +75,7 @@ def check(c, q, out):
 
 
 def test_a_handle_of_another_stream_while_a_stream_captures():
-    """A handle may be made, used and destroyed on a stream of its own while another stream captures in the default
+    """A handle may be made, used, waited for and destroyed on a stream of its own while another stream captures in the default
     (global) mode, and the capture goes on."""
     import torch
     s, other = torch.cuda.Stream(), torch.cuda.Stream()
@@ -88,6 +88,7 @@ def test_a_handle_of_another_stream_while_a_stream_captures():
         attend(kv, c, q, out)
         kv2 = c.handle(8, stream=other.cuda_stream)
         attend(kv2, c, q, out2)
+        kv2.sync()
         kv2.close()
         attend(kv, c, q, out)
     check(c, q, out2)
@@ -97,9 +98,28 @@ def test_a_handle_of_another_stream_while_a_stream_captures():
     check(c, q, out)
 
 
+def test_sync_of_a_stream_that_captures_is_refused():
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    s = torch.cuda.Stream()
+    c, q, out = small(2)
+    kv = c.handle(8, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        attend(kv, c, q, out)
+        with pytest.raises(cvr.CvrError) as e:
+            kv.sync()
+    assert e.value.status == 1 and "captur" in str(e.value)
+    with torch.cuda.stream(s):
+        graph.replay()
+    kv.sync()
+    check(c, q, out)
+
+
 def test_the_legacy_stream_is_refused_while_a_blocking_stream_captures():
-    """A blocking stream's capture makes the legacy default stream unusable: a handle is not made on it, and the capture goes
-    on."""
+    """A blocking stream's capture makes the legacy default stream unusable: a handle is not made on it or waited for, and the
+    capture goes on."""
     import ctypes
     import torch
     import cvr_ranking_model_gb300 as cvr
@@ -107,14 +127,16 @@ def test_the_legacy_stream_is_refused_while_a_blocking_stream_captures():
     assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(raw))) == 0
     s = torch.cuda.ExternalStream(raw.value)
     c, q, out = small(3)
-    kv = c.handle(8, stream=s.cuda_stream)
+    kv, legacy = c.handle(8, stream=s.cuda_stream), c.handle(8)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=s, capture_error_mode="relaxed"):
         with pytest.raises(cvr.CvrError) as made:
             c.handle(8)
+        with pytest.raises(cvr.CvrError) as waited:
+            legacy.sync()
         attend(kv, c, q, out)
-    assert made.value.status == 1
+    assert made.value.status == 1 and waited.value.status == 1
     with torch.cuda.stream(s):
         graph.replay()
     kv.sync()
