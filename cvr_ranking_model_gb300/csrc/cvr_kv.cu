@@ -76,7 +76,8 @@ cudaError_t captures(cudaStream_t s, bool* yes) {
   return *yes ? cudaSuccess : e;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 int elt_bytes(int dtype) { return dtype == CVR_DTYPE_I8 ? 1 : 2; }
 
@@ -242,6 +243,10 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
     return kv_fail(h, CVR_E_SHAPE, "need n_free >= 0 and 0 <= n_slots < 2^31 - 1");
   if (n_req > 0 && (!lens || !table)) return kv_fail(h, CVR_E_ARG, "null lens or table");
   if ((n_free > 0 && !free_pages) || (n_slots > 0 && !slots)) return kv_fail(h, CVR_E_ARG, "null free_pages or slots");
+  for (const void* p : {(const void*)lens, (const void*)new_lens, (const void*)held, (const void*)free_pages, (const void*)free_head,
+                        (const void*)table, (const void*)pages, (const void*)free_head_out})
+    if (!aligned(p, 4)) return kv_fail(h, CVR_E_ARG, "int32 arrays must be 4-byte aligned");
+  if (!aligned(slots, 8)) return kv_fail(h, CVR_E_ARG, "slots must be 8-byte aligned");
   if ((pages && pages == held) || (free_head_out && free_head_out == free_head))
     return kv_fail(h, CVR_E_ARG, "pages and free_head_out must be other arrays than held and free_head");
   OnDevice on(h->device);
@@ -280,6 +285,7 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
   if (k_stride < row || k_stride % 8 != 0 || (v && (v_stride < row || v_stride % 8 != 0)))
     return kv_fail(h, CVR_E_ARG, "row strides must be multiples of 8 and >= kv_heads * head_dim");
   if (!aligned16(k) || !aligned16(v)) return kv_fail(h, CVR_E_ARG, "rows must be 16-byte aligned");
+  if (!aligned(slots, 8)) return kv_fail(h, CVR_E_ARG, "slots must be 8-byte aligned");
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
   KvAppendArgs a;
@@ -320,6 +326,8 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   if (q_stride < row || q_stride % 8 != 0 || out_stride < row || out_stride % 8 != 0)
     return kv_fail(h, CVR_E_ARG, "q and out strides must be multiples of 8 and >= q_heads * head_dim");
   if (!aligned16(q) || !aligned16(out)) return kv_fail(h, CVR_E_ARG, "q and out must be 16-byte aligned");
+  if (!aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4))
+    return kv_fail(h, CVR_E_ARG, "lens, table and lse must be 4-byte aligned");
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
   KvAttendArgs a;

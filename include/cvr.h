@@ -295,6 +295,7 @@ void cvr_destroy(cvr_handle* h);
  * encoded states serve as both) a cache has one pool.
  * The three calls only enqueue (like cvr_score_async) and may be captured into a CUDA graph of the handle's
  * stream; cvr_kv_sync waits and returns the status of the device-side checks. Calls never allocate.
+ * Arrays are aligned to their elements, where no more is said; other pointers are refused (CVR_E_ARG).
  * A handle is not thread-safe, and its calls and the graphs captured from it share its workspace: run them one
  * after another, and use one handle per stream (handles may share pools). Pools are BORROWED and must stay
  * valid while calls or graphs use them. */

@@ -145,3 +145,33 @@ def test_the_legacy_stream_is_refused_while_a_blocking_stream_captures():
     torch.cuda.synchronize()
     del graph
     assert int(torch.cuda.cudart().cudaStreamDestroy(raw.value)) == 0
+
+
+def refused(call, **args):
+    import cvr_ranking_model_gb300 as cvr
+    with pytest.raises(cvr.CvrError) as e:
+        call(**args)
+    assert e.value.status == 1, args
+
+
+def test_arrays_that_are_not_aligned_are_refused():
+    import torch
+    c, q, out = small(4)
+    kv = c.handle(8)
+    x = torch.zeros(4096, dtype=torch.int64, device="cuda")
+    p = x.data_ptr()
+    ok = dict(n_req=2, lens=p, table=p + 256, new_lens=p + 512, held=p + 768, free_pages=p + 1024, n_free=8, free_head=p + 1280, pages=p + 1536,
+              free_head_out=p + 1792, slots=p + 2048, n_slots=4)
+    for name in ("lens", "table", "new_lens", "held", "free_pages", "free_head", "pages", "free_head_out"):
+        for by in (1, 2, 3):
+            refused(kv.tables, **{**ok, name: ok[name] + by})
+    for by in (1, 2, 4):
+        refused(kv.tables, **{**ok, "slots": ok["slots"] + by})
+        refused(kv.append, n_tok=1, slots=p + by, k=q.data_ptr(), v=q.data_ptr())
+    ok = dict(n_req=2, q=q.data_ptr(), lens=c.lens.data_ptr(), table=c.table.data_ptr(), scale=0.1, out=out.data_ptr(), lse=p)
+    for name in ("lens", "table", "lse"):
+        for by in (1, 2, 3):
+            refused(kv.attend, **{**ok, name: ok[name] + by})
+    kv.attend(**ok)
+    kv.sync()
+    check(c, q, out)
