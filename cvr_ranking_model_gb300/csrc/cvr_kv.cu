@@ -81,6 +81,15 @@ bool aligned16(const void* p) { return aligned(p, 16); }
 
 int elt_bytes(int dtype) { return dtype == CVR_DTYPE_I8 ? 1 : 2; }
 
+struct Array {
+  const void* p;  // (null: none)
+  int64_t bytes;
+};
+bool overlap(const Array& a, const Array& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && (x < y ? y - x < (uint64_t)a.bytes && b.bytes > 0 : x - y < (uint64_t)b.bytes && a.bytes > 0);
+}
+
 // The strides (page, head, token) of a pool, in values: multiples of 16 bytes below 2^40 bytes, and each of them, in
 // rising order, steps over everything that the smaller ones span, so that no two rows overlap.
 const char* bad_strides(const int64_t* stride, const cvr_kv_config* c) {
@@ -243,12 +252,20 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
     return kv_fail(h, CVR_E_SHAPE, "need n_free >= 0 and 0 <= n_slots < 2^31 - 1");
   if (n_req > 0 && (!lens || !table)) return kv_fail(h, CVR_E_ARG, "null lens or table");
   if ((n_free > 0 && !free_pages) || (n_slots > 0 && !slots)) return kv_fail(h, CVR_E_ARG, "null free_pages or slots");
-  for (const void* p : {(const void*)lens, (const void*)new_lens, (const void*)held, (const void*)free_pages, (const void*)free_head,
-                        (const void*)table, (const void*)pages, (const void*)free_head_out})
-    if (!aligned(p, 4)) return kv_fail(h, CVR_E_ARG, "int32 arrays must be 4-byte aligned");
+  // No CTA waits for another: what one writes, another may still have to read. The written arrays come last.
+  const int64_t n = n_req;
+  const Array arrays[] = {{lens, n * 4},  {new_lens, n * 4},
+                          {held, n * 4},  {free_pages, (int64_t)n_free * 4},
+                          {free_head, 4}, {table, n * h->cfg.max_pages * 4},
+                          {pages, n * 4}, {free_head_out, 4},
+                          {slots, n_slots * 8}};
+  constexpr int kArrays = sizeof(arrays) / sizeof(arrays[0]), kRead = 5;
+  for (int i = 0; i < kArrays - 1; ++i)
+    if (!aligned(arrays[i].p, 4)) return kv_fail(h, CVR_E_ARG, "int32 arrays must be 4-byte aligned");
   if (!aligned(slots, 8)) return kv_fail(h, CVR_E_ARG, "slots must be 8-byte aligned");
-  if ((pages && pages == held) || (free_head_out && free_head_out == free_head))
-    return kv_fail(h, CVR_E_ARG, "pages and free_head_out must be other arrays than held and free_head");
+  for (int i = kRead; i < kArrays; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(arrays[i], arrays[j])) return kv_fail(h, CVR_E_ARG, "an array that the call writes overlaps another one");
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
   KvTablesArgs a;

@@ -339,11 +339,12 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
  *   table     [n_req][max_pages] int32, in place: a request of n = ceil(lens / page_size) > held pages gets free pages
  *             in entries held .. n - 1; no other entry is touched
  *   pages     [n_req] int32 entries that hold pages afterwards (pass it as `held` of the next step); NULL: not written
- *   free_head_out int32, *free_head plus the pages taken; NULL: not written. `pages` and `free_head_out` must be
- *             other arrays than `held` and `free_head`: a call leaves its inputs as they were
+ *   free_head_out int32, *free_head plus the pages taken; NULL: not written
  *   slots     [n_slots] int64 (n_slots < 2^31 - 1): the slots of the new tokens, requests in order, tokens in order;
  *             -1 behind the last.
  *             NULL with n_slots = 0: none wanted
+ * An array that the call writes (table, pages, free_head_out, slots) must not overlap any other of its arrays (CVR_E_ARG): a
+ * call leaves its inputs as they were.
  * Errors at cvr_kv_sync: CVR_E_INPUT for a length or held count out of range (used clamped) or more new tokens than
  * n_slots (the rest is dropped); CVR_E_PAGES when the free list ends (the entries and slots without a page are -1);
  * CVR_E_ID_RANGE for a page id outside the pool (its slots are -1). */
@@ -354,7 +355,7 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
 /* Writes n_tok tokens' rows (0 <= n_tok <= 2^31 - 1) to their slots:
  *   slots [n_tok] int64; a negative slot skips its token (padding); a slot outside the pool is skipped and reported
  *         (CVR_E_ID_RANGE). Of tokens with the same slot any may stay, in parts: give each its own
- *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned; consecutive tokens k_stride / v_stride
+ *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned, not among the rows that the call writes; consecutive tokens k_stride / v_stride
  *         values apart (a multiple of 8, at least kv_heads * head_dim). With K = V pass v = NULL.
  * CVR_DTYPE_I8 pools: per row scale = max|x| / 127 and q = round-half-even(127 x / max|x|); a zero row has q = 0 and
  * scale 0; a row with an infinity or NaN gets a scale that is not finite, so that it reads as no number. */

@@ -175,3 +175,37 @@ def test_arrays_that_are_not_aligned_are_refused():
     kv.attend(**ok)
     kv.sync()
     check(c, q, out)
+
+
+def test_arrays_that_overlap_are_refused():
+    """Whatever a call writes lies apart from all that it reads or writes, wholly and in part; neighbours are fine."""
+    import torch
+    c, _, _ = small(5)
+    kv = c.handle(8)
+    n, cols = 2, c.max_pages
+    x = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    p = x.data_ptr()
+    size = dict(lens=n, new_lens=n, held=n, free_pages=7, free_head=1, table=n * cols, pages=n, free_head_out=1, slots=2 * 4)
+    at, ok = 0, dict(n_req=n, n_free=7, n_slots=4)
+    for name, words in size.items():
+        if name == "slots":
+            at += at % 2
+        ok[name] = p + 4 * at
+        at += words
+    written = ("table", "pages", "free_head_out", "slots")
+    for one in written:
+        for other in size:
+            if other == one:
+                continue
+            first, last = ok[other], ok[other] + 4 * (size[other] - 1)
+            starts = {first, last, first - 4 * (size[one] - 1), last - 4 * (size[one] - 1)}
+            for s in starts:
+                if one != "slots" or s % 8 == 0:
+                    refused(kv.tables, **{**ok, one: s})
+    x[0:2] = dev([4, 0])
+    x[2:4] = dev([4, 0])
+    x[6:13] = dev([3, 4, 5, 6, 7, 8, 9])
+    kv.tables(**ok)
+    kv.sync()
+    assert x[:4].tolist() == [4, 0, 4, 0] and x[14:16].tolist() == [3, 0] and x[(ok["pages"] - p) // 4:][:3].tolist() == [1, 0, 1]
+    assert x[(ok["slots"] - p) // 4:][:10:2].tolist() == [48, 49, 50, 51, 0]
