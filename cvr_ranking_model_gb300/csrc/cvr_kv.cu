@@ -248,8 +248,8 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
   if (!h) return CVR_E_ARG;
   if (n_req < 0 || n_req > h->cfg.max_req)
     return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", h->cfg.max_req, n_req);
-  if (n_free < 0 || n_slots < 0 || n_slots >= INT32_MAX)
-    return kv_fail(h, CVR_E_SHAPE, "need n_free >= 0 and 0 <= n_slots < 2^31 - 1");
+  if (n_free < 0 || n_free == INT32_MAX || n_slots < 0 || n_slots >= INT32_MAX)
+    return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_free < 2^31 - 1 and 0 <= n_slots < 2^31 - 1");
   if (n_req > 0 && (!lens || !table)) return kv_fail(h, CVR_E_ARG, "null lens or table");
   if ((n_free > 0 && !free_pages) || (n_slots > 0 && !slots)) return kv_fail(h, CVR_E_ARG, "null free_pages or slots");
   // No CTA waits for another: what one writes, another may still have to read. The written arrays come last.

@@ -22,8 +22,9 @@ constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
 // 28.5 us with 128, 23.2 us with 256).
 constexpr int kTabRunShort = 128, kTabRunLong = 256;
 
-// sums of fresh pages or new tokens; they stop at 2^31 - 1, above any list's length
-__device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); }
+// sums of fresh pages or new tokens; they stop at 2^31 - 1, above any list's or slot map's length
+constexpr uint32_t kTabMost = 0x7fffffffu;
+__device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, kTabMost); }
 
 struct TabReq {
   int len, fresh, held;
@@ -95,8 +96,26 @@ __device__ __forceinline__ int warp_last_at_most(const uint32_t* start, int n, u
   return block * kStep + __popc(__ballot_sync(0xffffffffu, lane < kStep && i < n && start[min(i, n - 1)] <= x)) - 1;
 }
 
+// Fresh entries from the kTabMost-th on, of which no sum knows the place: no list reaches them, they are -1. start: a sum per
+// thread's run of requests. (Out of line: a table above 8 GB.)
+static __device__ __noinline__ void tab_behind(const KvTablesArgs& a, int run, uint32_t before, uint32_t* start) {
+  __syncthreads();
+  start[threadIdx.x] = before;
+  __syncthreads();
+  for (int t = blockIdx.x; t < kTabThreads; t += gridDim.x) {
+    uint32_t at = start[t];
+    for (int r = t * run; r < min((t + 1) * run, a.n_req); ++r) {
+      int ignored = 0;
+      const TabReq x = tab_request(a, r, &ignored);
+      for (uint32_t j = min((uint32_t)x.fresh, kTabMost - at) + threadIdx.x; j < (uint32_t)x.fresh; j += kTabThreads)
+        a.table[(int64_t)r * a.max_pages + x.held + j] = -1;
+      at = sat_add(at, x.fresh);
+    }
+  }
+}
+
 template <int kTabRun>
-__global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesArgs a) {
+__global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const __grid_constant__ KvTablesArgs a) {
   __shared__ uint32_t s_warp[2][kTabWarps];
   __shared__ uint32_t s_run[2][kTabThreads];  // sums before each thread's run of requests
   // of the requests in hand: the sums before each, its held entries, and with w and f those sums
@@ -292,6 +311,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesAr
       at = sat_add(at, x.fresh);
     }
   }
+  if (all.f_all == kTabMost) tab_behind(a, run, all.f, s_run[0]);
   if (a.slots)
     for (int64_t y = (int64_t)n_slots + cta * kTabThreads + tid; y < a.n_slots; y += n_cta * kTabThreads) a.slots[y] = -1;
   if (cta == 0 && tid == 0 && a.free_head_out) *a.free_head_out = head + (int)min(all.f_all, left);

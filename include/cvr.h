@@ -335,7 +335,7 @@ cvr_status cvr_kv_create(const cvr_kv_config* cfg, void* cuda_stream, cvr_kv** o
  *   lens      [n_req] int32 tokens of each request's history, the new ones included
  *   new_lens  [n_req] int32 how many of them, the last ones, are new; NULL: one of each request that is not empty
  *   held      [n_req] int32 leading entries of the request's table row that hold pages already; NULL: none
- *   free_pages [n_free] int32 page ids; taken from position *free_head on (NULL: from 0), in request order
+ *   free_pages [n_free] int32 page ids (n_free < 2^31 - 1); taken from position *free_head on (NULL: from 0), in request order
  *   table     [n_req][max_pages] int32, in place: a request of n = ceil(lens / page_size) > held pages gets free pages
  *             in entries held .. n - 1; no other entry is touched
  *   pages     [n_req] int32 entries that hold pages afterwards (pass it as `held` of the next step); NULL: not written

@@ -209,3 +209,30 @@ def test_arrays_that_overlap_are_refused():
     kv.sync()
     assert x[:4].tolist() == [4, 0, 4, 0] and x[14:16].tolist() == [3, 0] and x[(ok["pages"] - p) // 4:][:3].tolist() == [1, 0, 1]
     assert x[(ok["slots"] - p) // 4:][:10:2].tolist() == [48, 49, 50, 51, 0]
+
+
+@pytest.mark.parametrize("n,cols", [(42000, 65536), (500, 2 ** 23)])
+def test_more_fresh_entries_than_32_bit_sums_hold(n, cols):
+    """A table above 8 GB of which nearly every entry is fresh: those behind the free list's end are -1 to the last one."""
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    n_free, page = 600_001, 8
+    kv = cvr.KvCache(cvr.make_kv_config(1, 1, 32, page, n_free, n, cols))
+    lens = torch.full((n,), cols * page, dtype=torch.int32, device="cuda")
+    held = (torch.arange(n, device="cuda") % 3 == 0).to(torch.int32)
+    table = torch.full((n, cols), 77, dtype=torch.int32, device="cuda")
+    free = torch.randperm(n_free, device="cuda").to(torch.int32)
+    pages, head, none = torch.empty_like(held), dev([0]), torch.zeros_like(held)
+    kv.tables(n, lens.data_ptr(), table.data_ptr(), new_lens=none.data_ptr(), held=held.data_ptr(), free_pages=free.data_ptr(),
+              n_free=n_free, pages=pages.data_ptr(), free_head_out=head.data_ptr())
+    assert kv.sync(check=False) == 8 and int(head) == n_free and int(pages.sum()) == n_free + int(held.sum())
+    assert bool((table[::3, 0] == 77).all())
+    table[::3, 0] = -1
+    rows = 3 + n_free // cols  # the rows that hold pages
+    flat = table[:rows].flatten()
+    assert torch.equal(flat[flat != -1], free) and int(flat.max()) == n_free - 1
+    for a in range(rows, n, 2000):
+        assert int(table[a:a + 2000].max()) == -1 and int(table[a:a + 2000].min()) == -1
+    with pytest.raises(cvr.CvrError) as e:
+        kv.tables(n, lens.data_ptr(), table.data_ptr(), free_pages=free.data_ptr(), n_free=2 ** 31 - 1)
+    assert e.value.status == 2
