@@ -236,3 +236,64 @@ def test_more_fresh_entries_than_32_bit_sums_hold(n, cols):
     with pytest.raises(cvr.CvrError) as e:
         kv.tables(n, lens.data_ptr(), table.data_ptr(), free_pages=free.data_ptr(), n_free=2 ** 31 - 1)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("cache", ["same", "i8"])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 161, 2 ** 31 - 1])
+def test_a_length_out_of_range_is_reported_and_used_clamped(cache, bad):
+    import torch
+    c = Cache([160, 30], 2, 64, 16, "bf16", cache, seed=6, max_pages=10)
+    kv = c.handle(8)
+    q = torch.randn((2, 8, 64), generator=c.gen, device="cuda").to(torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 8), 7.0, device="cuda")
+    c.lens[0] = c.lens_list[0] = bad
+    kv.attend(2, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.1, out.data_ptr(), lse.data_ptr())
+    assert kv.sync(check=False) == 6 and "length" in kv.last_error()
+    ref, ref_lse, bound, b_lse = c.reference(q, 0.1)  # (of no token, or of max_pages * page_size)
+    assert_within(out, ref, bound, "out")
+    assert_within(lse, ref_lse, b_lse, "lse")
+
+
+@pytest.mark.parametrize("n", [20000, 65535])
+@pytest.mark.parametrize("dtype,cache,heads,group,dim,window", [("bf16", "same", 1, 2, 32, 0), ("f16", "i8", 2, 1, 64, 9), ("bf16", "i8", 1, 17, 32, 0)])
+def test_very_many_requests_with_histories(n, dtype, cache, heads, group, dim, window):
+    """Tens of thousands of requests of 0 to 24 tokens; the bounds as in Cache.reference, for all requests at once."""
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    from kv_util import EPS, cvr_type
+    page, cols = 8, 3
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n + dim)
+    lens = torch.randint(0, page * cols + 1, (n,), generator=gen, device="cuda").to(torch.int32)
+    table = torch.randperm(n * cols, generator=gen, device="cuda").to(torch.int32).view(n, cols)
+    x = [torch.randn((n * cols, heads, page, dim), generator=gen, device="cuda") for _ in range(2)]
+    scale = [None, None]
+    if cache == "i8":
+        x = [(t * 40).round().clamp(-127, 127).to(torch.int8) for t in x]
+        scale = [torch.rand((n * cols, heads, page), generator=gen, device="cuda") * 0.05 for _ in range(2)]
+    else:
+        x = [t.to(torch_type(dtype)) for t in x]
+    q = torch.randn((n, heads * group, dim), generator=gen, device="cuda").to(torch_type(dtype))
+    out, lse = torch.full_like(q, 7.0), torch.full((n, heads * group), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    kv = cvr.KvCache(cvr.make_kv_config(heads * group, heads, dim, page, n * cols, n, cols, cvr_type(dtype), cvr_type("i8" if cache == "i8" else dtype),
+                                        window, x[0].data_ptr(), k_scale=scale[0].data_ptr() if scale[0] is not None else 0,
+                                        v=x[1].data_ptr(), v_scale=scale[1].data_ptr() if scale[1] is not None else 0))
+    kv.attend(n, q.data_ptr(), lens.data_ptr(), table.data_ptr(), dim ** -0.5, out.data_ptr(), lse.data_ptr())
+    kv.sync()
+    for a in range(0, n, 8192):
+        r = slice(a, min(a + 8192, n))
+        k, v = ((t[table[r].long()].double() * (1.0 if s is None else s[table[r].long()].double()[..., None])).transpose(1, 2).flatten(2, 3)
+                for t, s in zip(x, scale))  # [request, head, token, dim]
+        j, m = torch.arange(page * cols, device="cuda"), lens[r].long()[:, None]
+        seen = ((j < m) & (j >= (m - window if window else 0)))[:, None, None, :]
+        y = q[r].double().unflatten(1, (heads, group))
+        s = torch.where(seen, y @ k.transpose(2, 3) * dim ** -0.5, -math.inf)
+        p = torch.nan_to_num(torch.softmax(s, 3), nan=0.0)
+        o, size = p @ v, p @ v.abs()
+        top = torch.where(seen, (y.abs() @ k.abs().transpose(2, 3)) * dim ** -0.5, 0.0).amax(3, keepdim=True)
+        rel = top * dim * 2.0 ** -23 + torch.where(seen, s.abs(), 0.0).amax(3, keepdim=True) * 2.0 ** -22 + 2.0 ** -21
+        sums = (page * cols / 16 + 64) * 2.0 ** -23
+        assert_within(out[r], o.flatten(1, 2), (EPS[dtype] * o.abs() + (2 * (rel + 2.0 ** -15) + 2 * sums) * size + 2.0 ** -25).flatten(1, 2), "out")
+        want = torch.logsumexp(s, 3)
+        assert_within(lse[r], want.flatten(1, 2), (rel[..., 0] + sums + torch.where(torch.isinf(want), 0.0, want.abs()) * 2.0 ** -22).flatten(1, 2), "lse")

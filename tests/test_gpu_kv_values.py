@@ -254,3 +254,32 @@ def test_the_sum_of_few_weights_is_fp32(dtype, cache, group):
     _, lse = call(c, q, 1.0)
     want = torch.log1p(torch.exp(-q[:, :, 5].double()))
     assert float((lse.double() - want).abs().max()) <= 2.0 ** -20.5
+
+
+@pytest.mark.parametrize("dtype,cache,split", [("bf16", "same", 2.0 ** -16), ("f16", "same", 2.0 ** -22), ("bf16", "i8", 2.0 ** -22), ("f16", "i8", 2.0 ** -22)])
+@pytest.mark.parametrize("group", GROUPS)
+def test_weights_keep_both_halves(dtype, cache, split, group):
+    """Eight tokens with exact logits in (-1, 0], values 1 and -1 in turn, so that the output is far below its sum p |v| = 1 and
+    does not hide the weights' errors: the exponent's argument (2^-22 where exponents begin at 8, and 3 roundings of 2^-24) times
+    ln 2 and exp2 (2^-22), below 2^-21 and twice, for numerator and denominator; the split; 8 adds of 2^-24, twice."""
+    import torch
+    n = 300
+    c = Cache([8] * n, 1, 32, 8, dtype, cache, seed=group)
+    p = c.table[:, 0].long()
+    one = 64 if cache == "i8" else 1
+    c.k[p] = 0
+    c.k[p, 0, :, 5] = -torch.arange(1, 9, device="cuda").to(c.k.dtype) * (one // 8 if cache == "i8" else 0.125)
+    c.v[p] = one
+    c.v[p, 0, 1::2] = -one
+    if cache == "i8":
+        c.k_scale[p] = c.v_scale[p] = 1.0 / one
+    q = torch.zeros((n, group, 32), device="cuda")
+    q[:, :, 5] = torch.rand((n, group), generator=c.gen, device="cuda") * 0.02
+    q = q.to(torch_type(dtype))
+    out, _ = call(c, q, 1.0)
+    s = -q[:, :, 5].double()[..., None] * torch.arange(1, 9, device="cuda") / 8
+    w = torch.softmax(s, 2)
+    want = (w[..., 0::2] - w[..., 1::2]).sum(2)[..., None]
+    assert float(want.abs().max()) < 2.0 ** -8
+    bound = EPS[dtype] * want.abs() + 2 * 2.0 ** -21 + split + 2 * 8 * 2.0 ** -24 + 2.0 ** -25
+    assert bool(((out.double() - want).abs() <= bound).all())
