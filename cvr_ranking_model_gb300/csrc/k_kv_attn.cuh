@@ -16,7 +16,7 @@
 // 16 of the heads): S = Q K^T and O += P V on mma.sync m16n8k16 with the running maximum, sum and O in registers.
 //   - mma.sync, not tcgen05: with at most 64 query rows a tile has 4 to 64 operations per byte read, an M = 128 MMA would
 //     be almost all padding, and P stays in registers between the two products. The tensor pipe is idle most of the time.
-//   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-9 in bf16) does not add to
+//   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-8 in bf16) does not add to
 //     the output's. With at most 8 query rows the halves sit in the two halves of the 16-row tile, at no extra cost.
 //   - 8-bit rows become fp16 exactly (1024 + q by a byte permute, minus 1152); K's scale multiplies the logit, V's scale
 //     the weight, whose products enter as fp16 times a power of two that the first scales choose. Where scales lie farther apart
@@ -536,14 +536,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   const int mt = warp % MT, kp = warp / MT;  // row tile, share of the tokens
   const int log2_br = min(a.page_log2, 31 - __clz(TK));
   // Logits in units of ln 2 are c q . k with c > 0 (a token that is not seen has q . k = -infinity, whose product must stay
-  // that), q times the scale's sign: -1, 0 or 1. bf16 rows enter times a power of two that brings their largest value to
-  // [1, 2), which goes back into c: q . k alone may leave fp32's range where scale times q does not.
+  // that), q times the scale's sign: -1, 0 or 1. bf16 rows may enter times a power of two, which goes back into c: q . k alone may
+  // leave fp32's range where scale times q does not. On 16-bit pools rows whose largest value is 2^16 or more are brought to
+  // [2^15, 2^16) (128 products with keys up to 2^104 then stay below 2^127), others stay as they are.
   const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
-  auto factor = [&](uint32_t e) {  // c of rows over 2^(e - 127)
+  auto factor = [&](uint32_t e) {  // c of rows over 2^(e - 127), at least the least number above 0
     return a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * __uint_as_float(e << 23) * kLog2e, 1.4e-45f);
   };
-  // (the exponents at the type's ends, subnormals' and the highest, take the power beside theirs: both factors are normal)
-  auto row_exponent = [](uint32_t e) { return min(max(e, 1u), 253u); };
   // In fp16 weights are kept times a power of two (p is at most 2^kGrow), so that small ones keep their bits: times 2^8, with
   // 8-bit rows and their V scales over a power of two (below). The two halves hold a weight to 2^-22 of it, or to 2^-25, 2^-33
   // of a weight of 1.
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
   typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
-  // fp16 weights are summed by a product of their halves, 2^-22 of each, with ones; others as they are (bf16's halves hold 2^-17)
+  // fp16 weights are summed by a product of their halves, 2^-22 of each, with ones; others as they are (bf16's halves hold 2^-16)
   constexpr bool kOnesSum = kF16;
   constexpr uint32_t kOnes = 0x3c003c00u;  // 1, 1
   uint32_t meets = 0;
@@ -627,32 +626,33 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           bigA = __vmaxu2(bigA, __vmaxu2(qf[k][0] & 0x7fff7fffu, qf[k][2] & 0x7fff7fffu));  // (magnitudes order as their bits)
           bigB = __vmaxu2(bigB, __vmaxu2(qf[k][1] & 0x7fff7fffu, qf[k][3] & 0x7fff7fffu));
         }
-        float mulA = sign, mulB = sign;
+        float upA = sign, upB = sign;
         if (std::is_same<T, __nv_bfloat16>::value) {
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {
             bigA = __vmaxu2(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
             if (!R8) bigB = __vmaxu2(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
           }
-          const uint32_t eA = row_exponent(max(bigA >> 16, bigA & 0xffffu) >> 7), eB = row_exponent(max(bigB >> 16, bigB & 0xffffu) >> 7);
-          mulA *= __uint_as_float((254u - eA) << 23);
-          mulB *= __uint_as_float((254u - eB) << 23);
+          auto row_exponent = [](uint32_t big) { return min(max(max(big >> 16, big & 0xffffu) >> 7, 142u), 254u) - 15; };
+          const uint32_t eA = row_exponent(bigA), eB = row_exponent(bigB);
+          upA *= __uint_as_float((254u - eA) << 23);
+          upB *= __uint_as_float((254u - eB) << 23);
           cA = factor(eA);
           cB = factor(eB);
         }
-        const uint32_t mA2 = pack2<T>(mulA, mulA), mB2 = pack2<T>(mulB, mulB);
+        const uint32_t upA2 = pack2<T>(upA, upA), upB2 = pack2<T>(upB, upB);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          qf[k][0] = mul2<T>(qf[k][0], mA2);
-          qf[k][2] = mul2<T>(qf[k][2], mA2);
+          qf[k][0] = mul2<T>(qf[k][0], upA2);
+          qf[k][2] = mul2<T>(qf[k][2], upA2);
           if (!R8) {
-            qf[k][1] = mul2<T>(qf[k][1], mB2);
-            qf[k][3] = mul2<T>(qf[k][3], mB2);
+            qf[k][1] = mul2<T>(qf[k][1], upB2);
+            qf[k][3] = mul2<T>(qf[k][3], upB2);
           }
         }
       } else {
         // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
-        float mulA = sign, mulB = sign;
+        float upA = sign, upB = sign;
         uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
         }
         if (std::is_same<T, __nv_bfloat16>::value) {
-          // (as fp16: exact down to 2^-14 of the largest value, 2^-25 of it below)
+          // in fp16, the largest value brought to [1, 2): exact down to 2^-14 of it, 2^-25 of it below
           float bigA = 0.f, bigB = 0.f;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -674,19 +674,21 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             bigA = fmaxf(bigA, __shfl_xor_sync(0xffffffffu, bigA, d));
             bigB = fmaxf(bigB, __shfl_xor_sync(0xffffffffu, bigB, d));
           }
-          const uint32_t eA = row_exponent(__float_as_uint(bigA) >> 23), eB = row_exponent(__float_as_uint(bigB) >> 23);
-          mulA *= __uint_as_float((254u - eA) << 23);
-          mulB *= __uint_as_float((254u - eB) << 23);
+          // (the exponents at the type's ends, subnormals' and the highest, take the power beside theirs: both factors are normal)
+          auto row_exponent = [](float big) { return min(max(__float_as_uint(big) >> 23, 1u), 253u); };
+          const uint32_t eA = row_exponent(bigA), eB = row_exponent(bigB);
+          upA *= __uint_as_float((254u - eA) << 23);
+          upB *= __uint_as_float((254u - eB) << 23);
           cA = factor(eA);
           cB = factor(eB);
         }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const float2 u = unpack2<T>(xa[k].x), v = unpack2<T>(xa[k].y), w = unpack2<T>(xb[k].x), z = unpack2<T>(xb[k].y);
-          qf[k][0] = pack2<__half>(u.x * mulA, u.y * mulA);
-          qf[k][2] = pack2<__half>(v.x * mulA, v.y * mulA);
-          qf[k][1] = pack2<__half>(w.x * mulB, w.y * mulB);
-          qf[k][3] = pack2<__half>(z.x * mulB, z.y * mulB);
+          qf[k][0] = pack2<__half>(u.x * upA, u.y * upA);
+          qf[k][2] = pack2<__half>(v.x * upA, v.y * upA);
+          qf[k][1] = pack2<__half>(w.x * upB, w.y * upB);
+          qf[k][3] = pack2<__half>(z.x * upB, z.y * upB);
         }
       }
     }

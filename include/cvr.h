@@ -377,7 +377,8 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  * Weights enter the sum over v as two 16-bit halves: with bf16 pools to 2^-16 of a weight, with fp16 pools to 2^-22 of it or
  * 2^-33 of its query row's largest, with 8-bit pools, times the V scale, to 2^-22 of it or of the row's largest such product,
  * however much larger the scales of tokens without weight are. bf16 queries on 8-bit pools are held in fp16 relative to their
- * row's largest value: exact down to 2^-14 of it, to 2^-25 of it below.
+ * row's largest value: exact down to 2^-14 of it, to 2^-25 of it below; on bf16 pools exact but for values below 2^-141 of a
+ * largest value above 2^16.
  * Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length outside
  * [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read; out is not
  * meaningful), CVR_E_SHAPE when the histories of a call, times kv heads, hold more than about 2^36 tokens (out is not

@@ -181,6 +181,23 @@ def test_products_beyond_fp32_before_the_scale(cache, group, log2_q, log2_k, sca
     assert_within(out, ref, b_out, "out")
 
 
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("log2", [10, 15, 16, 17, 40, 100, 127])
+def test_one_huge_query_value_leaves_the_others_theirs(group, log2):
+    """A query value that meets only zero keys: the logits are the other values', however much larger it is."""
+    import torch
+    c = Cache([3, 80], 2, 64, 16, "bf16", seed=log2)
+    c.k[..., 11] = 0
+    q = torch.randn((2, 2 * group, 64), generator=c.gen, device="cuda").to(torch.bfloat16)
+    small = q.clone()
+    small[..., 11] = 0
+    q[..., 11] = 2.0 ** log2
+    out, lse = call(c, q, 0.125)
+    ref, ref_lse, b_out, b_lse = c.reference(small, 0.125)
+    assert_within(lse, ref_lse, b_lse, "lse")
+    assert_within(out, ref, b_out, "out")
+
+
 @pytest.mark.parametrize("cache", ["same", "i8"])
 def test_a_scale_of_zero_keeps_what_is_no_number(cache):
     """0 times an infinity is no number: a scale of zero does not hide a bad query or key row, and spares the others."""
