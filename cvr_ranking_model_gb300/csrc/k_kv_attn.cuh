@@ -14,8 +14,10 @@
 // into a ring of units, K and V in turn, swizzled so that ldmatrix reads without bank conflicts, and runs ahead across
 // requests. A consumer warp takes every fourth block of 16 tokens of a tile (or, for more than 16 query heads per kv head,
 // 16 of the heads): S = Q K^T and O += P V on mma.sync m16n8k16 with the running maximum, sum and O in registers.
-//   - mma.sync, not tcgen05: with at most 64 query rows a tile has 4 to 64 operations per byte read, an M = 128 MMA would
-//     be almost all padding, and P stays in registers between the two products. The tensor pipe is idle most of the time.
+//   - mma.sync, not tcgen05: a tile has 1 (one head, 16 bits) to 256 (64 heads, int8, K = V) operations per byte read, and P
+//     stays in registers between the two products. For up to 8 heads the tensor pipe is active less than 30% of the time. With the
+//     heads on M an M = 128 MMA would be mostly padding; with the tokens on M it would not, which is not built: the forms for 32
+//     and 64 heads, whose warps load and convert the same rows for 16 heads each, stand far from their bytes.
 //   - P enters the second product as two 16-bit halves (p = hi + lo), so that its rounding (2^-8 in bf16) does not add to
 //     the output's. With at most 8 query rows the halves sit in the two halves of the 16-row tile, at no extra cost.
 //   - 8-bit rows become fp16 exactly (1024 + q by a byte permute, minus 1152); K's scale multiplies the logit, V's scale
@@ -24,9 +26,9 @@
 //     without weight leaves the other tokens their bits.
 //
 // Measured (one GB300, copy rate 6.67 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128, bf16: 113 us, 6.5 TB/s;
-// one request of 131071: 85 us, 6.3 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 74 us, 5.2 TB/s,
-// bound by issue (bytes to fp16). 512 histories of up to 2000 events, 4 heads of 32, K = V: 34 us, 3.8 TB/s, bound by issue:
-// boxes of 1 KB in the producer, the softmax in the others. One request of 200: 4.3 us, latency.
+// one request of 131071: 85 us, 6.3 TB/s; both bound by HBM. 32 requests on int8 rows, 64 / 8 heads of 128: 74 us, 5.2 TB/s: 2.4
+// warps per scheduler, which issue 49% of the time, and no registers for more. 512 histories of up to 2000 events, 4 heads of 32,
+// K = V: 35 us, 3.7 TB/s: softmax, masks and copies of 1 KB once per head, issued 53% of the time. One request of 200: 4.6 us, latency.
 #pragma once
 
 #include <type_traits>

@@ -14,8 +14,8 @@ namespace {
 // One launch. Every CTA sums all requests (12 bytes each, from L2 in all CTAs but one) and so knows where its own slice
 // of the fresh entries and of the slots begins; it scans the slice's requests 512 at a time and writes. No CTA waits for
 // another: a slot's page comes from the free list or the held entries, never from what this call writes.
-// Bound by latency: 64 requests, a token each, 3.6 us (two dependent loads, a scan); 4095 requests and 5.5 million slots
-// 20.7 us, where writing 46 MB takes 7: 5.7 until the slots' requests are known, 3 of them for the table's entries.
+// Bound by latency: 64 requests, a token each, 3.7 us (two dependent loads, a scan); 4095 requests and 5.5 million slots
+// 20.1 us, where writing 46 MB takes 7: 5.7 until the slots' requests are known, 3 of them for the table's entries.
 constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
 // Consecutive items of a warp's step, whose loads are in flight together: a call of one CTA is bound by the latency of its
 // few steps (64 requests, a token each: 3.6 us with 128, 4.6 us with 256), a longer one by their number (5.5 million slots:

@@ -390,7 +390,8 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
  * stream captures (or, for the legacy stream, a blocking stream does): nothing is waited for and the capture goes on. */
 cvr_status cvr_kv_sync(cvr_kv* h);
 const char* cvr_kv_last_error(const cvr_kv* h);
-/* Waits for the stream and frees the handle's memory (not the pools). NULL is ignored. */
+/* Waits for the stream and frees the handle's memory (not the pools). Graphs captured from the handle must not run afterwards, and
+ * its stream must not be capturing (the capture would end with an error). NULL is ignored. */
 void cvr_kv_destroy(cvr_kv* h);
 
 #ifdef __cplusplus
