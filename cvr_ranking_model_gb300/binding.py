@@ -25,7 +25,7 @@ TIMELINE_KERNELS = ["sparse", "seq_mlp", "seq_colsum", "tokenizer", "query", "at
 STATUS = {0: "CVR_OK", 1: "CVR_E_ARG", 2: "CVR_E_SHAPE", 3: "CVR_E_ID_RANGE", 4: "CVR_E_OOM", 5: "CVR_E_CUDA",
           6: "CVR_E_INPUT", 7: "CVR_E_TIMEOUT", 8: "CVR_E_PAGES"}
 
-DTYPE_BF16, DTYPE_F16, DTYPE_I8 = 0, 1, 2  # cvr_dtype
+DTYPE_BF16, DTYPE_F16, DTYPE_I8, DTYPE_FP4 = 0, 1, 2, 3  # cvr_dtype
 
 _F = ctypes.POINTER(ctypes.c_float)
 
@@ -123,6 +123,12 @@ def lib() -> ctypes.CDLL:
         L.cvr_kv_append.restype = ctypes.c_int
         L.cvr_kv_attend.argtypes = [V, i32, V, i64, V, V, f32, V, i64, V]
         L.cvr_kv_attend.restype = ctypes.c_int
+        L.cvr_kv_read.argtypes = [V, i64, V, V, i64, V, i64]
+        L.cvr_kv_read.restype = ctypes.c_int
+        L.cvr_kv_weigh.argtypes = [V, i32, V, i64, V, V, V, f32, V, f32, V]
+        L.cvr_kv_weigh.restype = ctypes.c_int
+        L.cvr_kv_evict.argtypes = [V, i32, V, i32, i32, i32, i32, V, V, V, V, V, V, V, i32, V, V]
+        L.cvr_kv_evict.restype = ctypes.c_int
         L.cvr_kv_sync.argtypes = [V]
         L.cvr_kv_sync.restype = ctypes.c_int
         L.cvr_kv_last_error.argtypes = [V]
@@ -333,7 +339,8 @@ def make_kv_config(q_heads: int, kv_heads: int, head_dim: int, page_size: int, n
                    max_pages: int, dtype: int = DTYPE_BF16, cache_dtype: Optional[int] = None, window: int = 0,
                    k: int = 0, k_strides: Sequence[int] = (), k_scale: int = 0, v: int = 0,
                    v_strides: Sequence[int] = (), v_scale: int = 0) -> KvConfig:
-    """k, v, k_scale, v_scale: device pointers of the pools and their row scales (0 = none; v = 0 with k: K = V).
+    """k, v, k_scale, v_scale: device pointers of the pools and their scales (0 = none; v = 0 with k: K = V): of 8-bit pools a
+    float per row, of 4-bit pools (cache_dtype DTYPE_FP4) a record per page and kv head (include/cvr.h).
     Strides (page, kv head, token) are in values; by default a pool is [page][kv head][token][head_dim]."""
     c = KvConfig(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, max_req=max_req,
                  max_pages=max_pages, dtype=dtype, cache_dtype=dtype if cache_dtype is None else cache_dtype,
@@ -363,6 +370,7 @@ class KvCache:
         # (a decode step's calls are short: their entry points are looked up once)
         self._tables, self._append, self._attend = (self._lib.cvr_kv_tables, self._lib.cvr_kv_append,
                                                     self._lib.cvr_kv_attend)
+        self._read, self._weigh, self._evict = self._lib.cvr_kv_read, self._lib.cvr_kv_weigh, self._lib.cvr_kv_evict
 
     def _check(self, st: int) -> int:
         if st != 0:
@@ -389,6 +397,28 @@ class KvCache:
         """cvr_kv_attend: one query token per request over its pages (strides of requests in values, 0 = dense)."""
         st = self._attend(self._h, n_req, q, q_stride or self._q_row, lens, table, scale, out, out_stride or self._q_row,
                           lse)
+        if st:
+            self._check(st)
+
+    def read(self, n_tok: int, slots: int, k: int, v: int = 0, k_stride: int = 0, v_stride: int = 0) -> None:
+        """cvr_kv_read: rows of slots back as values of 16 bits (strides of tokens in values, 0 = dense)."""
+        st = self._read(self._h, n_tok, slots, k, k_stride or self._row, v, v_stride or self._row)
+        if st:
+            self._check(st)
+
+    def weigh(self, n_req: int, q: int, lens: int, table: int, scale: float, lse: int, weight: int, decay: float = 1.0,
+              new_lens: int = 0, q_stride: int = 0) -> None:
+        """cvr_kv_weigh: the attention weights of one query token per request, added up per cached token and kv head."""
+        st = self._weigh(self._h, n_req, q, q_stride or self._q_row, lens, new_lens, table, scale, lse, decay, weight)
+        if st:
+            self._check(st)
+
+    def evict(self, n_req: int, lens: int, limit: int, keep: int, table: int, weight: int, kept: int, lens_out: int,
+              first: int = 0, last: int = 0, held: int = 0, pages: int = 0, free_pages: int = 0, n_free: int = 0,
+              free_head: int = 0, free_head_out: int = 0) -> None:
+        """cvr_kv_evict: requests of more than `limit` tokens cut to their `keep` heaviest, pages back to the free list."""
+        st = self._evict(self._h, n_req, lens, limit, keep, first, last, held, table, weight, kept, lens_out, pages,
+                         free_pages, n_free, free_head, free_head_out)
         if st:
             self._check(st)
 

@@ -79,7 +79,11 @@ cudaError_t captures(cudaStream_t s, bool* yes) {
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
 
-int elt_bytes(int dtype) { return dtype == CVR_DTYPE_I8 ? 1 : 2; }
+// the form of a configuration's pools, and bytes of n of their values (of whole rows)
+int code_of(const cvr_kv_config& c) {
+  return c.cache_dtype == CVR_DTYPE_I8 ? kKv8 : c.cache_dtype == CVR_DTYPE_FP4 ? kKv4 : kKv16;
+}
+int64_t value_bytes(int code, int64_t n) { return code == kKv16 ? n * 2 : code == kKv8 ? n : n / 2; }
 
 struct Array {
   const void* p;  // (null: none)
@@ -90,16 +94,21 @@ bool overlap(const Array& a, const Array& b) {
   return x && y && (x < y ? y - x < (uint64_t)a.bytes && b.bytes > 0 : x - y < (uint64_t)b.bytes && a.bytes > 0);
 }
 
+// Bytes that n > 0 rows of 16-bit values take, `stride` values apart (more than an address space holds: the largest number).
+int64_t span(int64_t n, int64_t stride, int64_t row) {
+  return n > 1 && stride > (INT64_MAX / 4 - row) / (n - 1) ? INT64_MAX : ((n - 1) * stride + row) * 2;
+}
+
 // The strides (page, head, token) of a pool, in values: multiples of 16 bytes below 2^40 bytes, and each of them, in
 // rising order, steps over everything that the smaller ones span, so that no two rows overlap.
 const char* bad_strides(const int64_t* stride, const cvr_kv_config* c) {
   const int64_t size[3] = {c->n_pages, c->kv_heads, c->page_size};
-  const int eb = elt_bytes(c->cache_dtype);
+  const int code = code_of(*c), whole = code == kKv16 ? 8 : code == kKv8 ? 16 : 32;  // values of 16 bytes
   int order[3] = {2, 1, 0};
   for (int i = 0; i < 3; ++i) {
     if (size[i] == 1) continue;  // (a dimension of one row: its stride is never used)
-    if (stride[i] <= 0 || stride[i] >= (int64_t(1) << 40) / eb) return "a pool stride is not in (0, 2^40) bytes";
-    if (stride[i] * eb % 16 != 0) return "a pool stride is not a multiple of 16 bytes";
+    if (stride[i] <= 0 || stride[i] >= (int64_t(1) << 36) * whole) return "a pool stride is not in (0, 2^40) bytes";
+    if (stride[i] % whole != 0) return "a pool stride is not a multiple of 16 bytes";
   }
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2 - i; ++j)
@@ -131,17 +140,18 @@ const char* bad_config(const cvr_kv_config* c) {
     return "max_pages must be >= 1 and max_pages * page_size <= 2^30";
   if (c->n_pages < 1 || c->n_pages > INT32_MAX) return "n_pages must be in [1, 2^31 - 1]";
   if (c->dtype != CVR_DTYPE_BF16 && c->dtype != CVR_DTYPE_F16) return "dtype must be CVR_DTYPE_BF16 or CVR_DTYPE_F16";
-  if (c->cache_dtype != c->dtype && c->cache_dtype != CVR_DTYPE_I8) return "cache_dtype must be dtype or CVR_DTYPE_I8";
+  if (c->cache_dtype != c->dtype && c->cache_dtype != CVR_DTYPE_I8 && c->cache_dtype != CVR_DTYPE_FP4)
+    return "cache_dtype must be dtype, CVR_DTYPE_I8 or CVR_DTYPE_FP4";
   if (c->window < 0) return "window must be >= 0";
   if (c->reserved != 0) return "reserved must be 0";
   if (!c->k) return c->v || c->k_scale || c->v_scale ? "v, k_scale and v_scale need k" : nullptr;
-  const bool i8 = c->cache_dtype == CVR_DTYPE_I8;
+  const bool scaled = code_of(*c) != kKv16;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
     return "pools and scales must be 16-byte aligned";
   if (c->k == c->v) return "k and v are the same pool (pass v = NULL for K = V)";
-  if (i8 != (c->k_scale != nullptr) || (c->v && i8 != (c->v_scale != nullptr)))
-    return "an 8-bit pool needs its scales, a 16-bit pool has none";
-  if (i8 && c->v && c->k_scale == c->v_scale) return "k and v need scales of their own";
+  if (scaled != (c->k_scale != nullptr) || (c->v && scaled != (c->v_scale != nullptr)))
+    return "an 8- or 4-bit pool needs its scales, a 16-bit pool has none";
+  if (scaled && c->v && c->k_scale == c->v_scale) return "k and v need scales of their own";
   if (const char* why = bad_strides(c->k_stride, c)) return why;
   return c->v ? bad_strides(c->v_stride, c) : nullptr;
 }
@@ -151,9 +161,9 @@ const char* bad_config(const cvr_kv_config* c) {
 bool encode_pool(CUtensorMap* m, void* base, const int64_t* stride, const cvr_kv_config* c, int tile) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return false;
-  const int eb = elt_bytes(c->cache_dtype), row = c->head_dim * eb, line = row < 128 ? row : 128;
+  const int code = code_of(*c), eb = code == kKv16 ? 2 : 1, row = kv_row_bytes(code, c->head_dim), line = row < 128 ? row : 128;
   // (the stride of a dimension of one row is never used, but has to be a valid one)
-  auto bytes = [&](int d, int64_t size) { return (cuuint64_t)(size == 1 ? 256 : stride[d] * eb); };
+  auto bytes = [&](int d, int64_t size) { return (cuuint64_t)(size == 1 ? 256 : value_bytes(code, stride[d])); };
   const cuuint64_t dims[5] = {(cuuint64_t)(line / eb), (cuuint64_t)c->page_size, (cuuint64_t)(row / line),
                               (cuuint64_t)c->kv_heads, (cuuint64_t)c->n_pages};
   const cuuint64_t strides[4] = {bytes(2, c->page_size), 128, bytes(1, c->kv_heads), bytes(0, c->n_pages)};
@@ -162,7 +172,8 @@ bool encode_pool(CUtensorMap* m, void* base, const int64_t* stride, const cvr_kv
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   const CUtensorMapSwizzle swizzle = line == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                      : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
+                                     : line == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                  : CU_TENSOR_MAP_SWIZZLE_NONE;
   // L2 fetches whole runs of rows where a head's rows are next to each other, else no more than a row
   const bool dense = stride[2] == c->head_dim;
   const CUtensorMapL2promotion l2 = dense || row >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
@@ -178,7 +189,8 @@ cudaError_t prepare_attend(cvr_kv* h) {
   const cvr_kv_config* c = &h->cfg;
   const bool i8 = c->cache_dtype == CVR_DTYPE_I8;
   const int group = c->q_heads / c->kv_heads;
-  h->attend = c->head_dim == 32   ? kv_attend_kernel_32(c->dtype, i8, group)
+  h->attend = code_of(*c) == kKv4 ? kv_attend_kernel_fp4(c->dtype, c->head_dim, group)
+              : c->head_dim == 32 ? kv_attend_kernel_32(c->dtype, i8, group)
               : c->head_dim == 64 ? kv_attend_kernel_64(c->dtype, i8, group)
                                   : kv_attend_kernel_128(c->dtype, i8, group);
   if (!encode_pool(&h->tm_k, c->k, c->k_stride, c, h->attend.tile)) return cudaErrorInvalidValue;
@@ -325,7 +337,7 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
   a.head_dim = c.head_dim;
   a.page_log2 = h->page_log2;
   a.err = h->err_host_dev;
-  const cudaError_t e = launch_kv_append(a, c.dtype, c.cache_dtype == CVR_DTYPE_I8, h->num_sms, h->stream);
+  const cudaError_t e = launch_kv_append(a, c.dtype, code_of(c), h->num_sms, h->stream);
   return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_append launch");
 }
 
@@ -391,6 +403,174 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
   return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_attend launch");
 }
 
+cvr_status cvr_kv_read(cvr_kv* h, int64_t n_tok, const int64_t* slots, void* k, int64_t k_stride, void* v, int64_t v_stride) {
+  if (!h) return CVR_E_ARG;
+  const cvr_kv_config& c = h->cfg;
+  if (!c.k) return kv_fail(h, CVR_E_ARG, "the handle was created without pools");
+  if (n_tok < 0 || n_tok > INT32_MAX) return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_tok <= 2^31 - 1");
+  if (n_tok == 0) return CVR_OK;
+  if (!slots || (!k && !v)) return kv_fail(h, CVR_E_ARG, "null slots, or no rows wanted");
+  if (!c.v && v) return kv_fail(h, CVR_E_ARG, "the cache has K = V: pass v = NULL");
+  const int64_t row = (int64_t)c.kv_heads * c.head_dim;
+  for (const int64_t stride : {k ? k_stride : row, v ? v_stride : row})
+    if (stride < row || stride % 8 != 0)
+      return kv_fail(h, CVR_E_ARG, "row strides must be multiples of 8 and >= kv_heads * head_dim");
+  if (!aligned16(k) || !aligned16(v)) return kv_fail(h, CVR_E_ARG, "rows must be 16-byte aligned");
+  if (!aligned(slots, 8)) return kv_fail(h, CVR_E_ARG, "slots must be 8-byte aligned");
+  // (rows of k and v may interleave: whether they overlap shows within one stride where the strides are the same)
+  const Array whole[3] = {{slots, n_tok * 8}, {k, span(n_tok, k_stride, row)}, {v, span(n_tok, v_stride, row)}};
+  if (overlap(whole[0], whole[1]) || overlap(whole[0], whole[2])) return kv_fail(h, CVR_E_ARG, "the rows overlap the slots");
+  if (overlap(whole[1], whole[2])) {
+    bool apart = n_tok > 1 && k_stride == v_stride && k_stride < INT64_MAX / 4;
+    if (apart) {
+      const int64_t step = k_stride * 2, d = (static_cast<char*>(v) - static_cast<char*>(k)) % step;
+      const int64_t at = d < 0 ? d + step : d;  // where a v row begins after a k row
+      apart = at >= row * 2 && step - at >= row * 2;
+    }
+    if (!apart) return kv_fail(h, CVR_E_ARG, "the rows of k and v overlap");
+  }
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
+  KvReadArgs a;
+  a.slots = slots;
+  a.dst[0] = k;
+  a.dst[1] = v;
+  a.dst_stride[0] = k_stride;
+  a.dst_stride[1] = v_stride;
+  a.pool[0] = c.k;
+  a.pool[1] = c.v;
+  for (int i = 0; i < 3; ++i) {
+    a.stride[0][i] = c.k_stride[i];
+    a.stride[1][i] = c.v_stride[i];
+  }
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v_scale;
+  a.n_tok = n_tok;
+  a.n_pages = c.n_pages;
+  a.kv_heads = c.kv_heads;
+  a.head_dim = c.head_dim;
+  a.page_log2 = h->page_log2;
+  a.err = h->err_host_dev;
+  const cudaError_t e = launch_kv_read(a, c.dtype, code_of(c), h->num_sms, h->stream);
+  return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_read launch");
+}
+
+cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
+                        const int32_t* new_lens, const int32_t* table, float scale, const float* lse, float decay,
+                        float* weight) {
+  if (!h) return CVR_E_ARG;
+  const cvr_kv_config& c = h->cfg;
+  if (!c.k) return kv_fail(h, CVR_E_ARG, "the handle was created without pools");
+  if (c.window) return kv_fail(h, CVR_E_ARG, "weights are not kept for handles with a window");
+  if (n_req < 0 || n_req > c.max_req)
+    return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", c.max_req, n_req);
+  if (!std::isfinite(scale) || !std::isfinite(decay) || decay < 0.f)
+    return kv_fail(h, CVR_E_ARG, "scale and decay must be finite, decay >= 0");
+  if (n_req == 0) return CVR_OK;
+  if (!q || !lens || !table || !lse || !weight) return kv_fail(h, CVR_E_ARG, "null q, lens, table, lse or weight");
+  const int64_t row = (int64_t)c.q_heads * c.head_dim;
+  if (q_stride < row || q_stride % 8 != 0) return kv_fail(h, CVR_E_ARG, "the q stride must be a multiple of 8 and >= q_heads * head_dim");
+  if (!aligned16(q)) return kv_fail(h, CVR_E_ARG, "q must be 16-byte aligned");
+  if (!aligned(lens, 4) || !aligned(new_lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(weight, 4))
+    return kv_fail(h, CVR_E_ARG, "lens, new_lens, table, lse and weight must be 4-byte aligned");
+  const int64_t n = n_req;
+  const Array out = {weight, c.n_pages * c.kv_heads * c.page_size * 4};
+  for (const Array& in : {Array{q, span(n, q_stride, row)}, Array{lens, n * 4}, Array{new_lens, n * 4},
+                          Array{table, n * c.max_pages * 4}, Array{lse, n * c.q_heads * 4}})
+    if (overlap(out, in)) return kv_fail(h, CVR_E_ARG, "weight overlaps another array");
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
+  KvWeighArgs a;
+  a.q = q;
+  a.k = c.k;
+  a.lens = lens;
+  a.new_lens = new_lens;
+  a.table = table;
+  a.lse = lse;
+  a.k_scale = c.k_scale;
+  a.weight = weight;
+  a.q_stride = q_stride;
+  a.n_pages = c.n_pages;
+  for (int i = 0; i < 3; ++i) a.k_stride[i] = c.k_stride[i];
+  a.scale = scale;
+  a.decay = decay;
+  a.n_req = n_req;
+  a.kv_heads = c.kv_heads;
+  a.group = c.q_heads / c.kv_heads;
+  a.page_log2 = h->page_log2;
+  a.max_pages = c.max_pages;
+  a.err = h->err_host_dev;
+  const cudaError_t e = launch_kv_weigh(a, c.dtype, code_of(c), c.head_dim, h->num_sms, h->stream);
+  return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_weigh launch");
+}
+
+cvr_status cvr_kv_evict(cvr_kv* h, int32_t n_req, const int32_t* lens, int32_t limit, int32_t keep, int32_t first,
+                        int32_t last, const int32_t* held, const int32_t* table, float* weight, int32_t* kept,
+                        int32_t* lens_out, int32_t* pages, int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                        int32_t* free_head_out) {
+  if (!h) return CVR_E_ARG;
+  const cvr_kv_config& c = h->cfg;
+  if (!c.k) return kv_fail(h, CVR_E_ARG, "the handle was created without pools");
+  if (c.window) return kv_fail(h, CVR_E_ARG, "tokens are not evicted by weight from handles with a window");
+  if (n_req < 0 || n_req > c.max_req)
+    return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_req <= max_req (%d); got %d", c.max_req, n_req);
+  if (keep < 1 || keep > limit || limit > (1 << 30) || first < 0 || last < 0 || (int64_t)first + last > keep)
+    return kv_fail(h, CVR_E_SHAPE, "need 1 <= keep <= limit <= 2^30, first >= 0, last >= 0 and first + last <= keep");
+  if (n_free < 0 || n_free == INT32_MAX) return kv_fail(h, CVR_E_SHAPE, "need 0 <= n_free < 2^31 - 1");
+  if ((free_pages != nullptr) != (n_free > 0)) return kv_fail(h, CVR_E_ARG, "free_pages and n_free belong together");
+  if (free_pages && (!free_head || !free_head_out)) return kv_fail(h, CVR_E_ARG, "a free list needs free_head and free_head_out");
+  if (!free_pages && (free_head || free_head_out)) return kv_fail(h, CVR_E_ARG, "free_head and free_head_out need a free list");
+  if (n_req > 0 && (!lens || !table || !weight || !kept || !lens_out))
+    return kv_fail(h, CVR_E_ARG, "null lens, table, weight, kept or lens_out");
+  // No CTA waits for those of other requests: what one writes, another may still have to read. The written arrays come last.
+  const int64_t n = n_req;
+  const Array arrays[] = {{lens, n * 4}, {held, n * 4}, {table, n * c.max_pages * 4}, {free_head, 4},
+                          {weight, c.n_pages * c.kv_heads * c.page_size * 4}, {kept, n * c.kv_heads * keep * 4},
+                          {lens_out, n * 4}, {pages, n * 4}, {free_pages, (int64_t)n_free * 4}, {free_head_out, 4}};
+  constexpr int kArrays = sizeof(arrays) / sizeof(arrays[0]), kRead = 4;
+  for (int i = 0; i < kArrays; ++i)
+    if (!aligned(arrays[i].p, 4)) return kv_fail(h, CVR_E_ARG, "int32 arrays and weight must be 4-byte aligned");
+  for (int i = kRead; i < kArrays; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(arrays[i], arrays[j])) return kv_fail(h, CVR_E_ARG, "an array that the call writes overlaps another one");
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return kv_cuda_fail(h, on.status, "cudaSetDevice");
+  const int code = code_of(c);
+  KvEvictArgs a;
+  a.lens = lens;
+  a.held = held;
+  a.table = table;
+  a.free_head = free_head;
+  a.weight = weight;
+  a.kept = kept;
+  a.lens_out = lens_out;
+  a.pages = pages;
+  a.free_pages = free_pages;
+  a.free_head_out = free_head_out;
+  a.pool[0] = c.k;
+  a.pool[1] = c.v;
+  for (int i = 0; i < 3; ++i) {
+    a.stride[0][i] = value_bytes(code, c.k_stride[i]);
+    a.stride[1][i] = value_bytes(code, c.v_stride[i]);
+  }
+  a.scale[0] = c.k_scale;
+  a.scale[1] = c.v ? c.v_scale : nullptr;
+  a.n_pages = c.n_pages;
+  a.limit = limit;
+  a.keep = keep;
+  a.first = first;
+  a.last = last;
+  a.n_req = n_req;
+  a.n_free = n_free;
+  a.kv_heads = c.kv_heads;
+  a.head_dim = c.head_dim;
+  a.page_log2 = h->page_log2;
+  a.max_pages = c.max_pages;
+  a.err = h->err_host_dev;
+  const cudaError_t e = launch_kv_evict(a, code, h->num_sms, h->stream);
+  return e == cudaSuccess ? CVR_OK : kv_cuda_fail(h, e, "cvr_kv_evict launch");
+}
+
 cvr_status cvr_kv_sync(cvr_kv* h) {
   if (!h) return CVR_E_ARG;
   OnDevice on(h->device);
@@ -410,7 +590,7 @@ cvr_status cvr_kv_sync(cvr_kv* h) {
     return kv_fail(h, CVR_E_TIMEOUT, "a bounded device-side wait gave up");
   }
   if (ew & kKvErrLens) return kv_fail(h, CVR_E_INPUT, "a length, new length, held count or list head is out of range");
-  if (ew & kKvErrPages) return kv_fail(h, CVR_E_PAGES, "the free list ran out of pages");
+  if (ew & kKvErrPages) return kv_fail(h, CVR_E_PAGES, "the free list ran out of pages, or has no room in front of its head");
   if (ew & kKvErrSlots) return kv_fail(h, CVR_E_INPUT, "more new tokens than the slot map holds");
   if (ew & kKvErrSize) return kv_fail(h, CVR_E_SHAPE, "the histories of one call are too long together");
   if (ew & kKvErrPage) return kv_fail(h, CVR_E_ID_RANGE, "a page id is outside the pool");

@@ -31,10 +31,8 @@
 // K = V: 35 us, 3.7 TB/s: softmax, masks and copies of 1 KB once per head, issued 53% of the time. One request of 200: 4.6 us, latency.
 #pragma once
 
-#include <type_traits>
-
 #include "../../include/cvr.h"
-#include "cvr_kv.cuh"
+#include "cvr_kv_rows.cuh"
 
 namespace cvr {
 namespace kv {
@@ -42,7 +40,6 @@ namespace kv {
 constexpr int kConsumers = 4;                       // consumer warps
 constexpr int kThreads = (kConsumers + 1) * 32;     // and the producer
 static_assert(kThreads == kKvAttendThreads, "the launch's block");
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A part: the tiles of one (request, kv head) in a CTA's run.
 struct __align__(16) Part {
@@ -52,24 +49,25 @@ struct __align__(16) Part {
 constexpr int kGroup = 16;  // parts that are joined at once
 
 // MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64
-template <bool I8, int D, int MODE>
+template <int CODE, int D, int MODE>
 struct Shape {
+  static constexpr bool I8 = CODE == kKv8, F4 = CODE == kKv4;
   static constexpr int MT = MODE == 3 ? 4 : MODE == 2 ? 2 : 1;  // 16-row tiles of query heads
   static constexpr int KP = kConsumers / MT;                    // consumer warps that share a row tile's tokens
-  static constexpr int kRow = D * (I8 ? 1 : 2);                 // bytes of a row
+  static constexpr int kRow = kv_row_bytes(CODE, D);            // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && I8 ? 3 : 2) : 2;
-  static constexpr int kUnitMost = kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
+  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
+  static constexpr int kUnitMost = kCtasPerSm == 2 && ((MT == 1 && !(F4 && MODE == 1)) || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
   static constexpr int kQBytes = (MODE == 0 ? 8 : MT * 16) * kQRow;
-  static constexpr int kORow = D + (I8 ? 16 : 8);               // padded fp32 rows of the joining area
+  static constexpr int kORow = D + (F4 ? 4 : I8 ? 16 : 8);      // padded fp32 rows of the joining area
   static constexpr int kORows = MODE == 0 ? 8 : 16;             // a warp's rows in the joining area
   static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
   static constexpr int kOAreas = D == 32 && MODE == 0 ? 2 : 1;           // (two spare a barrier per use, where they fit)
-  static constexpr int kScaleBytes = I8 ? TK * 4 : 0;
+  static constexpr int kScaleBytes = TK * kv_scale_bytes(CODE, D);  // the row scales, then the block scales
   static constexpr int kPartCost = MT == 1 ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
@@ -88,89 +86,23 @@ struct Shape {
 };
 
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) { return pack_bf16(a, b); }
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t x);
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
-  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
-
-// the product of two pairs
-template <typename T>
-__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y);
-template <>
-__device__ __forceinline__ uint32_t mul2<__nv_bfloat16>(uint32_t x, uint32_t y) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-template <>
-__device__ __forceinline__ uint32_t mul2<__half>(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// c (+)= a b; FIRST: the accumulator starts from zero
-template <typename T, bool FIRST = false>
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (FIRST) {
-    if (std::is_same<T, __half>::value)
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-    else
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-  } else {
-    if (std::is_same<T, __half>::value)
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-}
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void ldsm2(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm2_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void ldsm4_trans(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// two of the four bytes of x, biased signed values (q ^ 0x80 = q + 128), as an fp16 pair: SEL picks the bytes (0x4140: 0 and
-// 1, 0x4342: 2 and 3, 0x4240: 0 and 2, 0x4341: 1 and 3); the bits 0x64.. are 1024 + (q + 128).
-template <int SEL>
-__device__ __forceinline__ uint32_t i8_pair(uint32_t x) {
-  const uint32_t u = __byte_perm(x, 0x64646464u, SEL);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // A wait of a whole warp, bounded like mbar_wait: the hardware may hold a polling warp for up to 1 ms at a time, so that
 // waiting warps do not take the others' issue slots.
@@ -256,11 +188,12 @@ __device__ __forceinline__ unsigned add_acq_rel(unsigned* p) {
   return v;
 }
 
-template <typename T, bool I8, int D, int MODE>
-__global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
+template <typename T, int CODE, int D, int MODE>
+__global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     attend_kernel(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v) {
-  typedef Shape<I8, D, MODE> S;
+  typedef Shape<CODE, D, MODE> S;
+  constexpr bool I8 = S::I8, F4 = S::F4, SCALED = I8 || F4;  // (row scales)
   constexpr int MT = S::MT, KP = S::KP, TK = S::TK, NB = S::NB, NBS = S::NBS, RING = S::kRing;
   constexpr bool R8 = MODE == 0;
   extern __shared__ uint8_t smem_raw[];
@@ -423,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       ids0 = n_ids;
       more0 = entries(r, first_entry(len) + 32);
       bool ok = true;
-      const uint32_t box_bytes = br * (S::kRow + (I8 ? 4 : 0)), tile_bytes = TK * (S::kRow + (I8 ? 4 : 0));
+      constexpr int kTokBytes = S::kRow + kv_scale_bytes(CODE, D);
+      const uint32_t box_bytes = br * kTokBytes, tile_bytes = TK * kTokBytes;
       const bool long_pages = a.page_log2 > log2_br;  // several tiles per page, one box per tile
       while (ok) {
         // ---- a part: its query rows and description, and its tiles ----
@@ -484,8 +418,15 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
                           page);
               if (I8)
                 bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
-                          (w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row), 4 << log2_br,
-                          full + slot);
+                          static_cast<const float*>(w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row),
+                          4 << log2_br, full + slot);
+              if (F4) {
+                const uint8_t* const record = kv4_record(w ? a.v_scale : a.k_scale, (int64_t)page * H + h, a.page_log2, D);
+                const uint32_t to = smem_u32(sm + S::oScale + slot * S::kScaleBytes);
+                bulk_load(to + (lane << log2_br) * 4, record + row * 4, 4 << log2_br, full + slot);
+                bulk_load(to + TK * 4 + (lane << log2_br) * (D / 16), record + (4 << a.page_log2) + row * (D / 16),
+                          (D / 16) << log2_br, full + slot);
+              }
             }
             filled = min(filled + 1, RING);
             if (++slot == RING) {
@@ -549,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   // 8-bit rows and their V scales over a power of two (below). The two halves hold a weight to 2^-22 of it, or to 2^-25, 2^-33
   // of a weight of 1.
   constexpr float kGrow = 6.f;
-  constexpr bool kF16 = !I8 && std::is_same<T, __half>::value;
+  constexpr bool kF16 = !SCALED && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
-  typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
+  typedef typename std::conditional<SCALED, __half, T>::type M;  // operand type of the products
   // fp16 weights are summed by a product of their halves, 2^-22 of each, with ones; others as they are (bf16's halves hold 2^-16)
   constexpr bool kOnesSum = kF16;
   constexpr uint32_t kOnes = 0x3c003c00u;  // 1, 1
@@ -569,12 +510,14 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
   // rows is an exclusive or (lines are 128-byte aligned, or the bits above the swizzle's belong to the row).
   const uint32_t half_step = (uint32_t)S::kLine << log2_br;
   const int l7 = lane & 7, up8 = (lane >> 3) & 1, up16 = lane >> 4;
-  const uint32_t swz = (S::kLine == 128 ? l7 : S::kLine == 64 ? (l7 >> 1) & 3 : (l7 >> 2) & 1) << 4;
+  const uint32_t swz = (S::kLine == 128 ? l7 : S::kLine == 64 ? (l7 >> 1) & 3 : S::kLine == 32 ? (l7 >> 2) & 1 : 0) << 4;
   auto row_off = [&](int upper) -> uint32_t {
     return l7 * S::kLine + upper * (log2_br >= 4 ? 8 * S::kLine : S::kHalves * 8 * S::kLine);
   };
   const uint32_t ring = smem_u32(sm);
-  const uint32_t lane_k = ring + row_off(up16) + ((up8 << 4) ^ swz), lane_v = ring + row_off(up8) + ((up16 << 4) ^ swz);
+  // (lines of 16 bytes have one piece: matrices 0 and 1 are rows 0-7 and 8-15)
+  const uint32_t lane_k = S::kLine == 16 ? ring + row_off(up8) : ring + row_off(up16) + ((up8 << 4) ^ swz);
+  const uint32_t lane_v = S::kLine == 16 ? lane_k : ring + row_off(up8) + ((up16 << 4) ^ swz);
   auto block_at = [&](int key) -> uint32_t {
     return (uint32_t)(((key >> log2_br) * S::kHalves << log2_br) + (key & ((1 << log2_br) - 1))) * S::kLine;
   };
@@ -616,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
     {
       const uint8_t* qs = sm + S::oQ + qb * S::kQBytes + mt * 16 * S::kQRow;
       const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
-      if (!I8) {
+      if (!SCALED) {
         uint32_t bigA = 0, bigB = 0;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -653,12 +596,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           }
         }
       } else {
-        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
+        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's (values 4 tig .. of 16, or 8 tig .. of 32): the products' k
+        // index is permuted to match
         float upA = sign, upB = sign;
         uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
+          const uint8_t* pa = qs + gid * S::kQRow + (F4 ? (k >> 1) * 64 + tig * 16 + (k & 1) * 8 : k * 32 + tig * 8);
           xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
           xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
         }
@@ -703,6 +647,8 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       constexpr bool MASK = decltype(masked)::value;
       const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + k_slot * S::kScaleBytes);
       const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + v_slot * S::kScaleBytes);
+      const uint8_t* const k_blocks = reinterpret_cast<const uint8_t*>(k_sc + TK);  // 4 bits: block scales
+      const uint8_t* const v_blocks = reinterpret_cast<const uint8_t*>(v_sc + TK);
 #pragma unroll 1
       for (int sub = 0; sub < NB / NBS; ++sub) {
         // S = Q K^T
@@ -718,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             continue;
           }
           const uint32_t base = lane_k + k_slot * S::kUnit + block_at(key);
-          if (!I8) {
+          if (!SCALED) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               uint32_t f[4];
@@ -728,6 +674,34 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
                 if (k == 0) mma16816<M, true>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
                 else mma16816<M>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
               }
+            }
+          } else if (F4) {
+            uint2 bs[2];  // block scales of tokens gid and 8 + gid
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint8_t* at = k_blocks + (key + n * 8 + gid) * (D / 16);
+              if (D == 128) bs[n] = *reinterpret_cast<const uint2*>(at);
+              else bs[n].x = D == 64 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; k += D == 32 ? 2 : 4) {
+              uint32_t f[4];
+              if (D == 32) ldsm2(f, base);
+              else ldsm4(f, piece(base, k / 4));
+              constexpr int kPieces = D == 32 ? 1 : 2;  // of 32 values
+#pragma unroll
+              for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  const uint32_t x = f[kPieces * n + p];
+                  const int g = k / 2 + p;  // the row's piece, whose block of this thread is 2 g + tig / 2
+                  const uint32_t sc = e4m3_f16x2(__byte_perm(g < 2 ? bs[n].x : bs[n].y, 0, (g & 1) * 0x22 + (tig >> 1) * 0x11));
+                  const uint32_t e0 = mul2<M>(e2m1_f16x2<0>(x), sc), e1 = mul2<M>(e2m1_f16x2<1>(x), sc);
+                  const uint32_t d0 = mul2<M>(e2m1_f16x2<2>(x), sc), d1 = mul2<M>(e2m1_f16x2<3>(x), sc);
+                  if (g == 0) mma16816<M, true>(s[b][n], qf[0], e0, e1);
+                  else mma16816<M>(s[b][n], qf[2 * g], e0, e1);
+                  mma16816<M>(s[b][n], qf[2 * g + 1], d0, d1);
+                }
             }
           } else {
 #pragma unroll
@@ -752,13 +726,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           if (!ok) return;
         }
         float nA = -INFINITY, nB = -INFINITY;
-        float2 sv[NBS][2];  // 8 bits: V's row scales
+        float2 sv[NBS][2];  // V's row scales
 #pragma unroll
         for (int b = 0; b < NBS; ++b)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
-            if (I8) {
+            if (SCALED) {
               const float2 sk = *reinterpret_cast<const float2*>(k_sc + key);
               sv[b][n] = *reinterpret_cast<const float2*>(v_sc + key);
               s[b][n][0] *= sk.x;
@@ -771,11 +745,11 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             if (MASK) {  // tokens that are not seen are out
               if (key < j0 || key >= j1) {
                 s[b][n][0] = s[b][n][2] = -INFINITY;
-                if (I8) sv[b][n].x = 0.f;
+                if (SCALED) sv[b][n].x = 0.f;
               }
               if (key + 1 < j0 || key + 1 >= j1) {
                 s[b][n][1] = s[b][n][3] = -INFINITY;
-                if (I8) sv[b][n].y = 0.f;
+                if (SCALED) sv[b][n].y = 0.f;
               }
             }
             nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
@@ -785,13 +759,13 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         auto logit = [](float s, float c) { return __fmul_rn(s, c); };
         nA = logit(nA, cA);
         if (!R8) nB = logit(nB, cB);
-        // 8 bits: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
+        // Row scales: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
         auto size_and = [&](uint32_t x) -> uint32_t {
           const int key = ((sub * NBS + (NBS == 2 ? lane >> 4 : 0)) * KP + kp) * 16 + (lane & 15);
           return !MASK || (key >= j0 && key < j1) ? (__float_as_uint(v_sc[key]) & 0x7fffffffu) + x : 0u;
         };
         auto is_outside = [&]() { return size_and(__float_as_uint(mulA) - (251u << 23)) > 11u << 23; };  // (less the bits of hi / 2^11)
-        const bool outside = I8 && is_outside();
+        const bool outside = SCALED && is_outside();
         // The exponents' base follows the running maximum only when a logit passes it by more than kGrow: most steps then need
         // neither shuffles nor a rescaling.
         if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || outside)) {
@@ -814,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
             lA *= fA;
             if (!R8) lB *= fB;
           }
-          if (I8) {
+          if (SCALED) {
             const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
             if (mulA == 0.f) mulA = mulB = power(262 - min(max(top + 4, 12), 254));
             if (__any_sync(0xffffffffu, is_outside())) {
@@ -871,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
               lA += pA0 + pA1;
               if (!R8) lB += pB0 + pB1;
             }
-            if (I8) {
+            if (SCALED) {
               pA0 *= sv[b][n].x * fabsf(mulA);
               pA1 *= sv[b][n].y * fabsf(mulA);
               if (!R8) {
@@ -901,11 +875,58 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (!I8 && MASK) {
             const int key = key0 + 2 * tig;
-            keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
-            keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
+            constexpr uint32_t kFirst = F4 ? 0xffu : 0xffffu, kSecond = F4 ? 0xff00u : 0xffff0000u;
+            keep0 = (key >= j0 && key < j1 ? kFirst : 0u) | (key + 1 >= j0 && key + 1 < j1 ? kSecond : 0u);
+            keep1 = (key + 8 >= j0 && key + 8 < j1 ? kFirst : 0u) | (key + 9 >= j0 && key + 9 < j1 ? kSecond : 0u);
           }
           const uint32_t base = lane_v + v_slot * S::kUnit + block_at(key0);
-          if (!I8) {
+          if (F4) {
+            // A loaded register holds 4 values of two tokens. Block scales of tokens 2 tig, 2 tig + 1 and 8 further, those that are not
+            // seen cleared (they may be no numbers).
+            uint4 bs[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint8_t* at = v_blocks + (key0 + t * 8 + 2 * tig) * (D / 16);
+              if (D == 128) {
+                bs[t] = *reinterpret_cast<const uint4*>(at);
+              } else if (D == 64) {
+                const uint2 x = *reinterpret_cast<const uint2*>(at);
+                bs[t] = make_uint4(x.x, 0, x.y, 0);
+              } else {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(at);
+                bs[t] = make_uint4(x, 0, x >> 16, 0);
+              }
+            }
+            const uint32_t pick = (gid >> 2) * 0x11 + 0x40;  // block gid / 4 of a piece's two, of either token
+#pragma unroll
+            for (int c = 0; c < (D + 63) / 64; ++c) {
+              uint32_t f[4];
+              if (D == 32) ldsm2_trans(f, base);
+              else ldsm4_trans(f, piece(base, c));
+#pragma unroll
+              for (int p = 0; p < (D == 32 ? 1 : 2); ++p) {
+                const int g = 2 * c + p;
+                uint32_t v[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  const uint32_t x = f[2 * p + t];
+                  uint32_t both = __byte_perm(g < 2 ? bs[t].x : bs[t].y, g < 2 ? bs[t].z : bs[t].w, pick + (g & 1) * 0x22);
+                  if (MASK) both &= t ? keep1 : keep0;
+                  const uint32_t sc = e4m3_f16x2(both);
+                  const uint32_t y0 = e2m1_f16x2<0>(x), y1 = e2m1_f16x2<1>(x), y2 = e2m1_f16x2<2>(x), y3 = e2m1_f16x2<3>(x);
+                  v[t][0] = mul2<M>(__byte_perm(y0, y2, 0x5410), sc);
+                  v[t][1] = mul2<M>(__byte_perm(y0, y2, 0x7632), sc);
+                  v[t][2] = mul2<M>(__byte_perm(y1, y3, 0x5410), sc);
+                  v[t][3] = mul2<M>(__byte_perm(y1, y3, 0x7632), sc);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // values 4 gid + e of the piece's 32 form an n-tile
+                  mma16816<M>(o[4 * g + e], hi, v[0][e], v[1][e]);
+                  if (!R8) mma16816<M>(o[4 * g + e], lw, v[0][e], v[1][e]);
+                }
+              }
+            }
+          } else if (!I8) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t f[4];
@@ -976,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
       lA = R8 ? ls[0] + ls[2] : ls[0];
       lB = ls[2];
     }
-    const float o_mulA = I8 ? power(254 - exponent(mulA)) : 1.f, o_mulB = I8 ? power(254 - exponent(mulB)) : 1.f;  // (1 / mul)
+    const float o_mulA = SCALED ? power(254 - exponent(mulA)) : 1.f, o_mulB = SCALED ? power(254 - exponent(mulB)) : 1.f;  // (1 / mul)
     // values c .. c + 3 of query row g of a (request, head), all tokens joined: the output; or so far: to a place of the
     // workspace
     auto finish = [&](const Part& of, int g, int c, float m, float l, const float* acc) {
@@ -1012,7 +1033,18 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
         for (int j = 0; j < D / 8; ++j) {
           const float x = (R8 ? o[j][0] + o[j][2] : upper ? o[j][2] : o[j][0]) * o_mul;
           const float y = (R8 ? o[j][1] + o[j][3] : upper ? o[j][3] : o[j][1]) * o_mul;
-          if (!I8) {
+          if (F4) {
+            // (column 2 tig of an n-tile is dim 4 (2 tig) + j mod 4 of its piece, the next column 4 further)
+            if (j & 3) continue;
+            float u[4], v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u[e] = (R8 ? o[j + e][0] + o[j + e][2] : upper ? o[j + e][2] : o[j + e][0]) * o_mul;
+              v[e] = (R8 ? o[j + e][1] + o[j + e][3] : upper ? o[j + e][3] : o[j + e][1]) * o_mul;
+            }
+            *reinterpret_cast<float4*>(dst + j * 8 + 8 * tig) = make_float4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<float4*>(dst + j * 8 + 8 * tig + 4) = make_float4(v[0], v[1], v[2], v[3]);
+          } else if (!I8) {
             *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
           } else if (j & 1) {
             // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)
@@ -1154,23 +1186,21 @@ __global__ void __launch_bounds__(kThreads, Shape<I8, D, MODE>::kCtasPerSm)
 }
 
 // The instance for a configuration: its kernel, shared memory, CTAs per SM and tile.
-template <int D>
-KvAttendKernel instance(int dtype, bool int8, int group) {
+template <int D, int CODE>
+KvAttendKernel instance(int dtype, int group) {
   const int mode = group <= 8 ? 0 : group <= 16 ? 1 : group <= 32 ? 2 : 3;
-  auto of = [&](auto t, auto i8, auto m) {
+  auto of = [&](auto t, auto m) {
     typedef decltype(t) T;
-    typedef Shape<decltype(i8)::value, D, decltype(m)::value> S;
-    return KvAttendKernel{reinterpret_cast<const void*>(&attend_kernel<T, decltype(i8)::value, D, decltype(m)::value>), S::kSmem,
-                          S::kCtasPerSm, S::TK};
+    typedef Shape<CODE, D, decltype(m)::value> S;
+    return KvAttendKernel{reinterpret_cast<const void*>(&attend_kernel<T, CODE, D, decltype(m)::value>), S::kSmem, S::kCtasPerSm, S::TK};
   };
-  auto by_mode = [&](auto t, auto i8) {
-    if (mode == 0) return of(t, i8, std::integral_constant<int, 0>());
-    if (mode == 1) return of(t, i8, std::integral_constant<int, 1>());
-    if (mode == 2) return of(t, i8, std::integral_constant<int, 2>());
-    return of(t, i8, std::integral_constant<int, 3>());
+  auto by_mode = [&](auto t) {
+    if (mode == 0) return of(t, std::integral_constant<int, 0>());
+    if (mode == 1) return of(t, std::integral_constant<int, 1>());
+    if (mode == 2) return of(t, std::integral_constant<int, 2>());
+    return of(t, std::integral_constant<int, 3>());
   };
-  if (dtype == CVR_DTYPE_BF16) return int8 ? by_mode(__nv_bfloat16(), std::true_type()) : by_mode(__nv_bfloat16(), std::false_type());
-  return int8 ? by_mode(__half(), std::true_type()) : by_mode(__half(), std::false_type());
+  return dtype == CVR_DTYPE_BF16 ? by_mode(__nv_bfloat16()) : by_mode(__half());
 }
 
 }  // namespace kv

@@ -2,5 +2,7 @@
 #include "k_kv_attn.cuh"
 
 namespace cvr {
-KvAttendKernel kv_attend_kernel_128(int dtype, bool int8, int group) { return kv::instance<128>(dtype, int8, group); }
+KvAttendKernel kv_attend_kernel_128(int dtype, bool int8, int group) {
+  return int8 ? kv::instance<128, kKv8>(dtype, group) : kv::instance<128, kKv16>(dtype, group);
+}
 }  // namespace cvr

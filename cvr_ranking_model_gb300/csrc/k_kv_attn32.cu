@@ -2,5 +2,7 @@
 #include "k_kv_attn.cuh"
 
 namespace cvr {
-KvAttendKernel kv_attend_kernel_32(int dtype, bool int8, int group) { return kv::instance<32>(dtype, int8, group); }
+KvAttendKernel kv_attend_kernel_32(int dtype, bool int8, int group) {
+  return int8 ? kv::instance<32, kKv8>(dtype, group) : kv::instance<32, kKv16>(dtype, group);
+}
 }  // namespace cvr

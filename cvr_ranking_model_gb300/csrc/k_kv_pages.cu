@@ -1,7 +1,7 @@
-// Pages of the history cache: block tables and slot maps from request lengths, and the new tokens' rows to their
-// slots (cvr_kv_tables and cvr_kv_append of include/cvr.h).
+// Pages of the history cache: block tables and slot maps from request lengths, the new tokens' rows to their slots, and
+// rows back from theirs (cvr_kv_tables, cvr_kv_append and cvr_kv_read of include/cvr.h).
 #include "../../include/cvr.h"
-#include "cvr_kv.cuh"
+#include "cvr_kv_rows.cuh"
 
 namespace cvr {
 
@@ -321,15 +321,6 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const __grid_con
 // ------------------------------------------------------------------------------------------
 // Append: 16 bytes (8 values) of a row per thread, the key's and the value's loads in flight together. Bound by HBM:
 // 16383 tokens of 8 heads of 128 move 134 MB in 22.9 us (88% of the measured copy rate).
-template <typename T>
-__device__ __forceinline__ float2 to_f32x2(uint32_t x);
-template <>
-__device__ __forceinline__ float2 to_f32x2<__nv_bfloat16>(uint32_t x) {
-  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 to_f32x2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
-
 // 8-bit codes of 8 values of a row whose largest magnitude is `big`, finite: q = round-half-even(y), y = 127 x / big, as in
 // exact arithmetic. r = x (127 / big) is within 2^-23 |y| of y. A y that is no half lies at least 2^-19 |y| from one: 127 x
 // and big are whole numbers of at most 18 and 11 bits times powers of two, so y - (k + 1/2) is a multiple of
@@ -343,7 +334,7 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, float big) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float2 v = to_f32x2<T>(w[j >> 1]);
+    const float2 v = kv::unpack2<T>(w[j >> 1]);
     const float r2 = (j & 1 ? v.y : v.x) * up * c2;
     const float whole = __fadd_rn(__fadd_rn(r2, kMagic), -kMagic);  // 2 y to the nearest half of y
     const float y2 = fabsf(r2 - whole) <= fabsf(r2) * 0x1p-20f ? whole : r2;
@@ -355,9 +346,36 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, float big) {
   return make_uint2(four(code), four(code + 4));
 }
 
+// 4-bit codes of 8 values x of a block and the block's scale, of a row whose largest magnitude is `big`, finite, the block's `top`:
+// the quotients of the definition are rounded as in exact arithmetic.
+//   - scale: 448 top is exact and the quotient rounded once to 24 bits. It is no tie of two e4m3 values by that: a quotient of
+//     numbers of 11 and 3 by 11 bits that is not a tie (of 5 bits) lies 2^-16 of it from one.
+//   - codes: y = 2688 x / (big scale) has 16 bits over 15 (2688 = 21 * 2^7), a tie of two codes at most 3: one that is no tie lies
+//     at least 2^-18 of it from one. x (2688 / (big scale)) is within 2^-22 of y, and rounded to 20 bits it is the tie where y is.
+template <typename T>
+__device__ __forceinline__ uint32_t codes4(const uint4& x, float big, float top, uint32_t& scale) {
+  // (a power of two brings rows at the type's ends to where nothing below leaves fp32)
+  const float up = big < 0x1p-60f ? 0x1p64f : big > 0x1p60f ? 0x1p-64f : 1.f;
+  big *= up;
+  const float ratio = big > 0.f ? __fdiv_rn(top * up * 448.f, big) : 0.f;
+  uint16_t s8;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(ratio));
+  scale = s8;
+  const float den = big * kv::unpack2<__half>(kv::e4m3_f16x2(scale)).x, c = den > 0.f ? __fdiv_rn(2688.f, den) : 0.f;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t code = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = kv::unpack2<T>(w[j]);
+    auto to_20_bits = [](float y) { return __uint_as_float((__float_as_uint(y) + 8u) & ~15u); };
+    code |= kv::e2m1_pair(to_20_bits(v.x * up * c), to_20_bits(v.y * up * c)) << (8 * j);
+  }
+  return code;
+}
+
 constexpr int kAppThreads = 256;
 
-template <typename T, bool I8>
+template <typename T, int CODE>
 __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendArgs a) {
   const unsigned vec_row = a.head_dim >> 3;  // vectors of 8 values per row: 4, 8 or 16, within one warp
   const unsigned vec_tok = a.kv_heads * vec_row;
@@ -387,7 +405,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
         if (!a.src[w]) continue;
         const uint4 x = row[w];
         const int64_t at = page * a.stride[w][0] + head * a.stride[w][1] + pos * a.stride[w][2] + piece * 8;
-        if (!I8) {
+        if (CODE == kKv16) {
           if (ok) *reinterpret_cast<uint4*>(static_cast<T*>(a.pool[w]) + at) = x;
           continue;
         }
@@ -395,14 +413,82 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
         // infinities and NaN last
         uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                               __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-        for (unsigned d = vec_row >> 1; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float2 m2 = to_f32x2<T>(max(m & 0xffffu, m >> 16));
-        const float big = m2.x;
-        const bool finite = big < INFINITY;  // (not for NaN either)
-        if (ok) {
-          *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.pool[w]) + at) = finite ? codes8<T>(x, big) : make_uint2(0, 0);
-          if (piece == 0) a.scale[w][((page * a.kv_heads + head) << a.page_log2) + pos] = __fdiv_rn(big, 127.f);
+        auto largest = [](uint32_t m) { return kv::unpack2<T>(max(m & 0xffffu, m >> 16)).x; };
+        float top = 0.f;  // 4 bits: of the block of 16, two threads'
+        if (CODE == kKv4) {
+          m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          top = largest(m);
         }
+        for (unsigned d = vec_row >> 1; d > (CODE == kKv4); d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float big = largest(m);
+        const bool finite = big < INFINITY;  // (not for NaN either)
+        if (ok && CODE == kKv8) {
+          *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.pool[w]) + at) = finite ? codes8<T>(x, big) : make_uint2(0, 0);
+          if (piece == 0) static_cast<float*>(a.scale[w])[((page * a.kv_heads + head) << a.page_log2) + pos] = __fdiv_rn(big, 127.f);
+        }
+        if (ok && CODE == kKv4) {
+          uint8_t* const record = kv4_record(a.scale[w], page * a.kv_heads + head, a.page_log2, a.head_dim);
+          uint32_t code = 0, scale = 0;
+          if (finite) code = codes4<T>(x, big, top, scale);
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.pool[w]) + (at >> 1)) = code;
+          if (!(piece & 1)) record[(4 << a.page_log2) + pos * (a.head_dim >> 4) + (piece >> 1)] = (uint8_t)scale;
+          if (piece == 0) reinterpret_cast<float*>(record)[pos] = __fdiv_rn(big, 2688.f);
+        }
+      }
+    }
+  }
+  if (bad) atomicOr(a.err, bad);
+}
+
+// ------------------------------------------------------------------------------------------
+// Read: append's threads the other way round.
+template <typename T, int CODE>
+__global__ void __launch_bounds__(kAppThreads) kv_read_kernel(const KvReadArgs a) {
+  const unsigned vec_row = a.head_dim >> 3, vec_tok = a.kv_heads * vec_row;
+  const int64_t n_slots = a.n_pages << a.page_log2;
+  int bad = 0;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t t0 = 0; t0 < a.n_tok; t0 += 1 << 18) {
+    const unsigned total = (unsigned)min(a.n_tok - t0, (int64_t)1 << 18) * vec_tok;
+    for (unsigned i = blockIdx.x * kAppThreads + threadIdx.x; i < total; i += gridDim.x * kAppThreads) {
+      const unsigned at_tok = i / vec_tok, c = i - at_tok * vec_tok;
+      const unsigned head = c / vec_row, piece = c - head * vec_row;
+      const int64_t tok = t0 + at_tok, slot = a.slots[tok];
+      if (slot >= n_slots) bad |= kKvErrSlot;
+      if (slot < 0 || slot >= n_slots) continue;
+      const int64_t page = slot >> a.page_log2, pos = slot & ((1 << a.page_log2) - 1);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!a.dst[w]) continue;
+        const int64_t at = page * a.stride[w][0] + head * a.stride[w][1] + pos * a.stride[w][2] + piece * 8;
+        uint4 x;
+        if (CODE == kKv16) x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.pool[w]) + at);
+        if (CODE == kKv8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.pool[w]) + at);
+          const float s = static_cast<const float*>(a.scale[w])[((page * a.kv_heads + head) << a.page_log2) + pos];
+          const uint32_t b[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+          auto two = [&](uint32_t y) {
+            const float2 f = kv::unpack2<__half>(y);
+            return kv::pack2<T>(f.x * s, f.y * s);
+          };
+          x = make_uint4(two(kv::i8_pair<0x4140>(b[0])), two(kv::i8_pair<0x4342>(b[0])), two(kv::i8_pair<0x4140>(b[1])),
+                         two(kv::i8_pair<0x4342>(b[1])));
+        }
+        if (CODE == kKv4) {
+          const uint8_t* const record = kv4_record(a.scale[w], page * a.kv_heads + head, a.page_log2, a.head_dim);
+          const uint32_t q = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.pool[w]) + (at >> 1));
+          const float s = reinterpret_cast<const float*>(record)[pos];
+          const uint32_t b = record[(4 << a.page_log2) + pos * (a.head_dim >> 4) + (piece >> 1)];
+          const uint32_t b2 = kv::e4m3_f16x2(b | b << 8);
+          auto two = [&](uint32_t y) {  // (code times block scale is exact in fp16)
+            const float2 f = kv::unpack2<__half>(kv::mul2<__half>(y, b2));
+            return kv::pack2<T>(f.x * s, f.y * s);
+          };
+          x = make_uint4(two(kv::e2m1_f16x2<0>(q)), two(kv::e2m1_f16x2<1>(q)), two(kv::e2m1_f16x2<2>(q)),
+                         two(kv::e2m1_f16x2<3>(q)));
+        }
+        *(reinterpret_cast<uint4*>(static_cast<T*>(a.dst[w]) + tok * a.dst_stride[w]) + c) = x;
       }
     }
   }
@@ -421,14 +507,28 @@ cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s)
                        dim3((unsigned)(want < num_sms ? want : num_sms)), dim3(kTabThreads), 0, s, true, a);
 }
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, bool int8, int num_sms, cudaStream_t s) {
+cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, int code, int num_sms, cudaStream_t s) {
   const int64_t total = a.n_tok * a.kv_heads * (a.head_dim / 8);
   const int64_t want = (total + kAppThreads - 1) / kAppThreads, most = (int64_t)num_sms * 8;
   const dim3 grid((unsigned)(want < most ? want : most));
   auto run = [&](auto kern) { return launch_kernel(kern, grid, dim3(kAppThreads), 0, s, true, a); };
-  if (dtype == CVR_DTYPE_BF16)
-    return int8 ? run(kv_append_kernel<__nv_bfloat16, true>) : run(kv_append_kernel<__nv_bfloat16, false>);
-  return int8 ? run(kv_append_kernel<__half, true>) : run(kv_append_kernel<__half, false>);
+  auto of = [&](auto t) {
+    typedef decltype(t) T;
+    return code == kKv16 ? run(kv_append_kernel<T, kKv16>) : code == kKv8 ? run(kv_append_kernel<T, kKv8>) : run(kv_append_kernel<T, kKv4>);
+  };
+  return dtype == CVR_DTYPE_BF16 ? of(__nv_bfloat16()) : of(__half());
+}
+
+cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, int code, int num_sms, cudaStream_t s) {
+  const int64_t total = a.n_tok * a.kv_heads * (a.head_dim / 8);
+  const int64_t want = (total + kAppThreads - 1) / kAppThreads, most = (int64_t)num_sms * 8;
+  const dim3 grid((unsigned)(want < most ? want : most));
+  auto run = [&](auto kern) { return launch_kernel(kern, grid, dim3(kAppThreads), 0, s, true, a); };
+  auto of = [&](auto t) {
+    typedef decltype(t) T;
+    return code == kKv16 ? run(kv_read_kernel<T, kKv16>) : code == kKv8 ? run(kv_read_kernel<T, kKv8>) : run(kv_read_kernel<T, kKv4>);
+  };
+  return dtype == CVR_DTYPE_BF16 ? of(__nv_bfloat16()) : of(__half());
 }
 
 }  // namespace cvr

@@ -52,7 +52,7 @@ typedef enum {
   CVR_E_CUDA = 5,     /* a CUDA call failed (message in cvr_last_error) */
   CVR_E_INPUT = 6,    /* bag offsets decreasing, or request ids out of range / decreasing */
   CVR_E_TIMEOUT = 7,  /* a bounded device-side wait gave up (reported instead of hanging) */
-  CVR_E_PAGES = 8     /* cvr_kv_tables: the free list ran out of pages */
+  CVR_E_PAGES = 8     /* cvr_kv_tables: the free list ran out of pages; cvr_kv_evict: it has no room for them */
 } cvr_status;
 
 typedef struct cvr_handle cvr_handle;
@@ -287,13 +287,16 @@ void cvr_destroy(cvr_handle* h);
 /* ---------------------------------------------------------------------------------------------------------
  * Paged history cache. cvr_score encodes a user's whole history on every call; a server that keeps histories
  * (or any sequence's keys and values) resident in HBM stores them in pages of `page_size` tokens and touches
- * only what is new. Three operators work on the caller's pools, on the handle's stream:
+ * only what is new. Six operators work on the caller's pools, on the handle's stream:
  *   cvr_kv_tables  block tables and slot maps from request lengths, pages taken from a free list
- *   cvr_kv_append  new key and value rows to their slots, in 16 bits or as 8-bit integers with a scale per row
+ *   cvr_kv_append  new key and value rows to their slots, in 16 bits, as 8-bit integers with a scale per row, or in 4 bits
  *   cvr_kv_attend  one query token per request and head over that request's pages
+ *   cvr_kv_read    rows of given slots back as values of 16 bits
+ *   cvr_kv_weigh   what each cached token's attention weight adds up to
+ *   cvr_kv_evict   histories over a limit cut to their heaviest tokens, pages back to the free list
  * A slot is page * page_size + position in the page. With K = V (the ranking model's Query Decoding, whose
  * encoded states serve as both) a cache has one pool.
- * The three calls only enqueue (like cvr_score_async) and may be captured into a CUDA graph of the handle's
+ * The calls only enqueue (like cvr_score_async) and may be captured into a CUDA graph of the handle's
  * stream; cvr_kv_sync waits and returns the status of the device-side checks. Calls never allocate.
  * Arrays are aligned to their elements, where no more is said; other pointers are refused (CVR_E_ARG).
  * A handle is not thread-safe, and its calls and the graphs captured from it share its workspace: run them one
@@ -301,7 +304,9 @@ void cvr_destroy(cvr_handle* h);
  * valid while calls or graphs use them. */
 typedef struct cvr_kv cvr_kv;
 
-typedef enum { CVR_DTYPE_BF16 = 0, CVR_DTYPE_F16 = 1, CVR_DTYPE_I8 = 2 } cvr_dtype;
+/* CVR_DTYPE_FP4, pools only: 4-bit floats (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) with an e4m3 scale per 16 values of a
+ * row and an fp32 scale per row; a value is row scale * block scale * code. */
+typedef enum { CVR_DTYPE_BF16 = 0, CVR_DTYPE_F16 = 1, CVR_DTYPE_I8 = 2, CVR_DTYPE_FP4 = 3 } cvr_dtype;
 
 typedef struct {
   int32_t q_heads;     /* query heads, a multiple of kv_heads: query head i reads kv head i / (q_heads / kv_heads) */
@@ -311,17 +316,19 @@ typedef struct {
   int32_t max_req;     /* most requests of a call, 1 .. 65535 */
   int32_t max_pages;   /* columns of a block table, >= 1; max_pages * page_size <= 2^30 */
   int32_t dtype;       /* CVR_DTYPE_BF16 or CVR_DTYPE_F16: q, out and the new rows */
-  int32_t cache_dtype; /* the pools: `dtype`, or CVR_DTYPE_I8 */
+  int32_t cache_dtype; /* the pools: `dtype`, CVR_DTYPE_I8 or CVR_DTYPE_FP4 */
   int32_t window;      /* 0: a query sees the whole history; w > 0: its last w tokens */
   int32_t reserved;    /* 0 */
   int64_t n_pages;     /* pages of a pool, 1 .. 2^31 - 1 */
-  /* DEVICE pools, 16-byte aligned. The head_dim values of a row are contiguous; strides of page, kv head and token
+  /* DEVICE pools, 16-byte aligned. The head_dim values of a row are contiguous (CVR_DTYPE_FP4: two to a byte, the even one
+   * in its low half); strides of page, kv head and token
    * are in values, multiples of 16 bytes, and rows must not overlap (any nesting order of the three). k = NULL: a
    * handle for cvr_kv_tables only. v = NULL: values are the keys (K = V; v_stride and v_scale are ignored). */
   void *k, *v;
   int64_t k_stride[3], v_stride[3];
   /* with CVR_DTYPE_I8: fp32 [n_pages][kv_heads][page_size], one scale per row (a value is q * scale), 16-byte
-   * aligned; otherwise NULL */
+   * aligned. With CVR_DTYPE_FP4: [n_pages][kv_heads] records of page_size * (4 + head_dim / 16) bytes, 16-byte aligned: the
+   * rows' fp32 scales [page_size], then their e4m3 block scales [page_size][head_dim / 16]. Otherwise NULL */
   float *k_scale, *v_scale;
 } cvr_kv_config;
 
@@ -358,7 +365,11 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
  *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned, not among the rows that the call writes; consecutive tokens k_stride / v_stride
  *         values apart (a multiple of 8, at least kv_heads * head_dim). With K = V pass v = NULL.
  * CVR_DTYPE_I8 pools: per row scale = max|x| / 127 and q = round-half-even(127 x / max|x|); a zero row has q = 0 and
- * scale 0; a row with an infinity or NaN gets a scale that is not finite, so that it reads as no number. */
+ * scale 0; a row with an infinity or NaN gets a scale that is not finite, so that it reads as no number.
+ * CVR_DTYPE_FP4 pools: per row scale = max|x| / 2688 (6 * 448, the largest code times the largest block scale); per 16 values
+ * block scale = e4m3(448 max|x of the block| / max|x|), code = e2m1(2688 x / (max|x| * block scale)), both to the nearest, ties to
+ * even, codes beyond 6 as 6; a block whose scale is 0 (largest value below 2^-19 of the row's) has codes 0; infinities and NaN
+ * as for 8 bits. */
 cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const void* k, int64_t k_stride, const void* v,
                          int64_t v_stride);
 
@@ -375,9 +386,9 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  * softmax and sums are fp32: scale times a query value, a key value times 2^24, the logits, and sums of |v| times 2^6 have
  * to lie in its range.
  * Weights enter the sum over v as two 16-bit halves: with bf16 pools to 2^-16 of a weight, with fp16 pools to 2^-22 of it or
- * 2^-33 of its query row's largest, with 8-bit pools, times the V scale, to 2^-22 of it or of the row's largest such product,
- * however much larger the scales of tokens without weight are. bf16 queries on 8-bit pools are held in fp16 relative to their
- * row's largest value: exact down to 2^-14 of it, to 2^-25 of it below; on bf16 pools exact but for values below 2^-141 of a
+ * 2^-33 of its query row's largest, with 8- and 4-bit pools, times V's row scale, to 2^-22 of it or of the row's largest such
+ * product, however much larger the scales of tokens without weight are. bf16 queries on 8- and 4-bit pools are held in fp16
+ * relative to their row's largest value: exact down to 2^-14 of it, to 2^-25 of it below; on bf16 pools exact but for values below 2^-141 of a
  * largest value above 2^16.
  * Results do not change from call to call. Errors at cvr_kv_sync: CVR_E_INPUT for a length outside
  * [0, max_pages * page_size] (used clamped), CVR_E_ID_RANGE for a page id outside the pool (page 0 was read; out is not
@@ -385,6 +396,57 @@ cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const v
  * written, but for the empty requests), CVR_E_TIMEOUT. */
 cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
                          const int32_t* table, float scale, void* out, int64_t out_stride, float* lse);
+
+/* Rows of n_tok slots (0 <= n_tok <= 2^31 - 1) as values, the way back of cvr_kv_append:
+ *   slots [n_tok] int64; of a negative slot nothing is written; a slot outside the pool is skipped and reported (CVR_E_ID_RANGE);
+ *         the same slot may come more than once
+ *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned, written by the call; consecutive tokens k_stride /
+ *         v_stride values apart (a multiple of 8, at least kv_heads * head_dim). NULL: not wanted (one of them at least is);
+ *         with K = V pass v = NULL. k and v must not overlap each other, the slots or the pools.
+ * 16-bit pools give the rows' bits; 8- and 4-bit pools the values that codes and scales stand for, in fp32, rounded to `dtype`. */
+cvr_status cvr_kv_read(cvr_kv* h, int64_t n_tok, const int64_t* slots, void* k, int64_t k_stride, void* v, int64_t v_stride);
+
+/* Attention weights of one query token per request (0 <= n_req <= max_req; DEVICE arrays), added up per cached token and kv head:
+ *   weight[slot of j][h] = decay weight[slot of j][h] + sum_i exp(scale q[r][i] . k_j - lse[r][i])
+ * over the query heads i of kv head h, for every token j < lens[r]: what cvr_kv_evict ranks tokens by.
+ *   q, q_stride, lens, table, scale   as in cvr_kv_attend, whose products of queries and keys these are
+ *   lse       fp32 [n_req][q_heads], as cvr_kv_attend of the same queries wrote it
+ *   new_lens  [n_req] int32 how many of a request's tokens, the last ones, have no weight yet: theirs starts from 0 whatever their
+ *             place held before. NULL: one of each request that is not empty
+ *   decay     finite, >= 0; 1 adds up over a token's whole life, less forgets; 0 reads no old weight
+ *   weight    fp32 [n_pages][kv_heads][page_size], in place; places of other tokens are left as they are
+ * Sums are fp32, in one order on every call. A page must not be in two of the call's requests. weight must not overlap the
+ * other arrays. Not for handles with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length or new length out
+ * of range (used clamped), CVR_E_ID_RANGE for a page id outside the pool (its tokens are left out). */
+cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
+                        const int32_t* new_lens, const int32_t* table, float scale, const float* lse, float decay,
+                        float* weight);
+
+/* Cuts every request of more than `limit` tokens to `keep` of them (0 <= n_req <= max_req; DEVICE arrays). Per kv head the first
+ * `first` and the last `last` tokens stay, and of those between them the keep - first - last of the largest weight (of equal ones the
+ * earlier; NaN counts as the least). What stays becomes tokens 0 .. keep - 1 in the order it had: key and value rows, their
+ * scales and their weights move within the request's own pages.
+ *   lens     [n_req] int32 tokens of each request
+ *   limit, keep, first, last   1 <= keep <= limit <= 2^30, 0 <= first, 0 <= last, first + last <= keep (CVR_E_SHAPE)
+ *   held     [n_req] int32 leading entries of the request's table row that hold pages; NULL: ceil(lens / page_size)
+ *   table    [n_req][max_pages] int32, read only: entries behind a request's pages are ignored here and elsewhere
+ *   weight   fp32 [n_pages][kv_heads][page_size] as cvr_kv_weigh leaves it, in place
+ *   kept     [n_req][kv_heads][keep] int32: which token became token i; rows of requests that were not cut are not written
+ *   lens_out [n_req] int32: keep, or lens where nothing was cut
+ *   pages    [n_req] int32 entries that hold pages afterwards (`held` of the next step); NULL: not written
+ *   free_pages [n_free] int32 the free list of cvr_kv_tables, in place: pages that a cut request no longer needs, in request
+ *            and entry order, take the positions in front of *free_head, whose own pages are in use. NULL with n_free = 0:
+ *            requests keep their pages
+ *   free_head, free_head_out   int32, with free_pages: *free_head less the pages given back
+ * Requests must have pages of their own (none in two of them). An array that the call writes must not overlap any other of its
+ * arrays (CVR_E_ARG). Not for handles without pools or with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length,
+ * held count (a request's pages among them) or list head out of range (used clamped), CVR_E_PAGES when the list has no room in
+ * front of its head (the first pages are not given back), CVR_E_ID_RANGE for a page id outside the pool (rows of page 0 were
+ * read, none written). */
+cvr_status cvr_kv_evict(cvr_kv* h, int32_t n_req, const int32_t* lens, int32_t limit, int32_t keep, int32_t first,
+                        int32_t last, const int32_t* held, const int32_t* table, float* weight, int32_t* kept,
+                        int32_t* lens_out, int32_t* pages, int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                        int32_t* free_head_out);
 
 /* Waits for the handle's stream; the status of the device-side checks since the previous cvr_kv_sync. CVR_E_ARG while the
  * stream captures (or, for the legacy stream, a blocking stream does): nothing is waited for and the capture goes on. */
