@@ -189,10 +189,14 @@ cudaError_t prepare_attend(cvr_kv* h) {
   const cvr_kv_config* c = &h->cfg;
   const bool i8 = c->cache_dtype == CVR_DTYPE_I8;
   const int group = c->q_heads / c->kv_heads;
-  h->attend = code_of(*c) == kKv4 ? kv_attend_kernel_fp4(c->dtype, c->head_dim, group)
-              : c->head_dim == 32 ? kv_attend_kernel_32(c->dtype, i8, group)
-              : c->head_dim == 64 ? kv_attend_kernel_64(c->dtype, i8, group)
-                                  : kv_attend_kernel_128(c->dtype, i8, group);
+  if (code_of(*c) == kKv4)
+    h->attend = c->head_dim == 32   ? kv_attend_kernel_fp4_32(c->dtype, group)
+                : c->head_dim == 64 ? kv_attend_kernel_fp4_64(c->dtype, group)
+                                    : kv_attend_kernel_fp4_128(c->dtype, group);
+  else
+    h->attend = c->head_dim == 32   ? kv_attend_kernel_32(c->dtype, i8, group)
+                : c->head_dim == 64 ? kv_attend_kernel_64(c->dtype, i8, group)
+                                    : kv_attend_kernel_128(c->dtype, i8, group);
   if (!encode_pool(&h->tm_k, c->k, c->k_stride, c, h->attend.tile)) return cudaErrorInvalidValue;
   h->tm_v = h->tm_k;
   if (c->v && !encode_pool(&h->tm_v, c->v, c->v_stride, c, h->attend.tile)) return cudaErrorInvalidValue;

@@ -117,7 +117,9 @@ struct KvAttendKernel {
 KvAttendKernel kv_attend_kernel_32(int dtype, bool int8, int group);
 KvAttendKernel kv_attend_kernel_64(int dtype, bool int8, int group);
 KvAttendKernel kv_attend_kernel_128(int dtype, bool int8, int group);
-KvAttendKernel kv_attend_kernel_fp4(int dtype, int head_dim, int group);
+KvAttendKernel kv_attend_kernel_fp4_32(int dtype, int group);
+KvAttendKernel kv_attend_kernel_fp4_64(int dtype, int group);
+KvAttendKernel kv_attend_kernel_fp4_128(int dtype, int group);
 
 cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s);
 // dtype: a cvr_dtype of the rows; code: a KvCode

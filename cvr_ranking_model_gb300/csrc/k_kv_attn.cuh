@@ -33,6 +33,7 @@
 
 #include "../../include/cvr.h"
 #include "cvr_kv_rows.cuh"
+#include "k_kv_attn_fp4.cuh"
 
 namespace cvr {
 namespace kv {
@@ -57,8 +58,10 @@ struct Shape {
   static constexpr int kRow = kv_row_bytes(CODE, D);            // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int kCtasPerSm = D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
-  static constexpr int kUnitMost = kCtasPerSm == 2 && ((MT == 1 && !(F4 && MODE == 1)) || D < 128) ? 16384 : 8192;
+  static constexpr int kHeadTiles = MODE == 0 ? 1 : 2;          // 4 bits: tiles of 8 query heads per warp
+  static constexpr int kCtasPerSm = F4 && MODE == 0 ? (D == 128 ? 3 : 4) : D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
+  static constexpr int kUnitMost = F4 ? (D == 128 ? (MODE == 3 ? 4096 : 8192) : D == 64 && MODE == 0 ? 4096 : 8192)
+                                      : kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
@@ -73,12 +76,14 @@ struct Shape {
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
   // ring units: what is left of this CTA's share of the SM's 228 KB (1 KB of it reserved, 1 KB for the ring's alignment)
   static constexpr int kShare = kCtasPerSm == 1 ? 232448 : 233472 / kCtasPerSm - 1024;
-  static constexpr int kFixed = 2 * kQBytes + kOAreas * kOBytes + 3 * (int)sizeof(Part) + 5 * 8 + 64 + 1024;
+  static constexpr int kFragBytes = F4 ? kHeadTiles * (D / 16) * 256 : 0;  // 4 bits: a warp's query fragments
+  static constexpr int kFixed = 2 * kQBytes + kConsumers * kFragBytes + kOAreas * kOBytes + 3 * (int)sizeof(Part) + 5 * 8 + 64 + 1024;
   static constexpr int kRing = (kShare - kFixed) / (kUnit + kScaleBytes + 16);
   // shared memory
   static constexpr int oScale = kRing * kUnit;
   static constexpr int oQ = oScale + kRing * kScaleBytes;
-  static constexpr int oO = oQ + 2 * kQBytes;
+  static constexpr int oFrag = oQ + 2 * kQBytes;
+  static constexpr int oO = oFrag + kConsumers * kFragBytes;
   static constexpr int oPart = oO + kOAreas * kOBytes;
   static constexpr int oBar = oPart + 3 * (int)sizeof(Part);
   static constexpr int kSmem = oBar + (2 * kRing + 5) * 8 + 64 + 1024;
@@ -93,10 +98,10 @@ __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
                : "memory");
 }
 __device__ __forceinline__ void ldsm2(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm2_trans(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4_trans(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     attend_kernel(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v) {
   typedef Shape<CODE, D, MODE> S;
-  constexpr bool I8 = S::I8, F4 = S::F4, SCALED = I8 || F4;  // (row scales)
+  constexpr bool I8 = S::I8, F4 = S::F4;
   constexpr int MT = S::MT, KP = S::KP, TK = S::TK, NB = S::NB, NBS = S::NBS, RING = S::kRing;
   constexpr bool R8 = MODE == 0;
   extern __shared__ uint8_t smem_raw[];
@@ -422,10 +427,14 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
                           4 << log2_br, full + slot);
               if (F4) {
                 const uint8_t* const record = kv4_record(w ? a.v_scale : a.k_scale, (int64_t)page * H + h, a.page_log2, D);
-                const uint32_t to = smem_u32(sm + S::oScale + slot * S::kScaleBytes);
-                bulk_load(to + (lane << log2_br) * 4, record + row * 4, 4 << log2_br, full + slot);
-                bulk_load(to + TK * 4 + (lane << log2_br) * (D / 16), record + (4 << a.page_log2) + row * (D / 16),
-                          (D / 16) << log2_br, full + slot);
+                constexpr int kRec = kv_scale_bytes(CODE, D);
+                const uint32_t to = smem_u32(sm + S::oScale + slot * S::kScaleBytes) + lane * (kRec << log2_br);
+                if (!long_pages) {
+                  bulk_load(to, record, kRec << log2_br, full + slot);
+                } else {
+                  bulk_load(to, record + row * 4, 4 << log2_br, full + slot);
+                  bulk_load(to + (4 << log2_br), record + (4 << a.page_log2) + row * (D / 16), (D / 16) << log2_br, full + slot);
+                }
               }
             }
             filled = min(filled + 1, RING);
@@ -490,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
   // 8-bit rows and their V scales over a power of two (below). The two halves hold a weight to 2^-22 of it, or to 2^-25, 2^-33
   // of a weight of 1.
   constexpr float kGrow = 6.f;
-  constexpr bool kF16 = !SCALED && std::is_same<T, __half>::value;
+  constexpr bool kF16 = CODE == kKv16 && std::is_same<T, __half>::value;
   constexpr float kShift = kF16 ? 8.f : 0.f;
-  typedef typename std::conditional<SCALED, __half, T>::type M;  // operand type of the products
+  typedef typename std::conditional<I8, __half, T>::type M;  // operand type of the products
   // fp16 weights are summed by a product of their halves, 2^-22 of each, with ones; others as they are (bf16's halves hold 2^-16)
   constexpr bool kOnesSum = kF16;
   constexpr uint32_t kOnes = 0x3c003c00u;  // 1, 1
@@ -515,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     return l7 * S::kLine + upper * (log2_br >= 4 ? 8 * S::kLine : S::kHalves * 8 * S::kLine);
   };
   const uint32_t ring = smem_u32(sm);
-  // (lines of 16 bytes have one piece: matrices 0 and 1 are rows 0-7 and 8-15)
-  const uint32_t lane_k = S::kLine == 16 ? ring + row_off(up8) : ring + row_off(up16) + ((up8 << 4) ^ swz);
-  const uint32_t lane_v = S::kLine == 16 ? lane_k : ring + row_off(up8) + ((up16 << 4) ^ swz);
+  const uint32_t lane_k = ring + row_off(up16) + ((up8 << 4) ^ swz);
+  // (lines of 16 bytes have one piece: matrices 0 and 1 are all)
+  const uint32_t lane_v = ring + row_off(up8) + (S::kLine == 16 ? 0 : (up16 << 4) ^ swz);
   auto block_at = [&](int key) -> uint32_t {
     return (uint32_t)(((key >> log2_br) * S::kHalves << log2_br) + (key & ((1 << log2_br) - 1))) * S::kLine;
   };
@@ -534,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
 
   for (bool last = !some; !last;) {
     // ---- a part: the tiles of one (request, head) in this CTA's run ----
+    Heads4<T, F4 ? D : 32, S::kHeadTiles> heads4;  // 4 bits: all that follows here is in it
     uint32_t qf[D / 16][4];
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: sums of the weights by products
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
@@ -559,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     {
       const uint8_t* qs = sm + S::oQ + qb * S::kQBytes + mt * 16 * S::kQRow;
       const bool inA = mt * 16 + gid < G, inB = !R8 && mt * 16 + gid + 8 < G;
-      if (!SCALED) {
+      if constexpr (F4) {
+        heads4.begin(sm + S::oFrag + warp * S::kFragBytes, qs, S::kQRow, G - mt * 16, a.scale);
+      } else if (!I8) {
         uint32_t bigA = 0, bigB = 0;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -596,13 +608,12 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
           }
         }
       } else {
-        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's (values 4 tig .. of 16, or 8 tig .. of 32): the products' k
-        // index is permuted to match
+        // a K row's bytes 4 tig .. 4 tig + 3 of each 16 are this thread's: the products' k index is permuted to match
         float upA = sign, upB = sign;
         uint2 xa[D / 16], xb[D / 16];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint8_t* pa = qs + gid * S::kQRow + (F4 ? (k >> 1) * 64 + tig * 16 + (k & 1) * 8 : k * 32 + tig * 8);
+          const uint8_t* pa = qs + gid * S::kQRow + k * 32 + tig * 8;
           xa[k] = inA ? *reinterpret_cast<const uint2*>(pa) : make_uint2(0, 0);
           xb[k] = inB ? *reinterpret_cast<const uint2*>(pa + 8 * S::kQRow) : make_uint2(0, 0);
         }
@@ -645,10 +656,29 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     // One tile: its K and V units, and its tokens [j0, j1) that are seen. Whole tiles take the instance without masks.
     auto step = [&](auto masked, int k_slot, int v_slot, uint32_t v_phase, int j0, int j1) {
       constexpr bool MASK = decltype(masked)::value;
+      if constexpr (F4) {
+        const uint32_t k_base = lane_v + k_slot * S::kUnit, v_base = lane_v + v_slot * S::kUnit;
+        const uint8_t* const k_scales = sm + S::oScale + k_slot * S::kScaleBytes;
+        const uint8_t* const v_scales = sm + S::oScale + v_slot * S::kScaleBytes;
+#pragma unroll 1
+        for (int sub = 0; sub < NB / NBS && ok; ++sub) {
+          auto key = [&](int b) { return ((sub * NBS + b) * KP + kp) * 16; };
+          ok = heads4.template step<MASK, NBS>(
+              k_scales, v_scales, log2_br, j0, j1, key,
+              [&](int b, int p, uint32_t* f) {
+                if (D == 32) ldsm2(f, k_base + block_at(key(b)));
+                else ldsm4(f, piece(k_base + block_at(key(b)), p / 2));
+              },
+              [&](int b, int p, uint32_t* f) {
+                if (D == 32) ldsm2_trans(f, v_base + block_at(key(b)));
+                else ldsm4_trans(f, piece(v_base + block_at(key(b)), p / 2));
+              },
+              [&]() { return sub > 0 || !two || wait_warp(full + v_slot, v_phase, abort_flag, a.err); });
+        }
+        return;
+      }
       const float* k_sc = reinterpret_cast<const float*>(sm + S::oScale + k_slot * S::kScaleBytes);
       const float* v_sc = reinterpret_cast<const float*>(sm + S::oScale + v_slot * S::kScaleBytes);
-      const uint8_t* const k_blocks = reinterpret_cast<const uint8_t*>(k_sc + TK);  // 4 bits: block scales
-      const uint8_t* const v_blocks = reinterpret_cast<const uint8_t*>(v_sc + TK);
 #pragma unroll 1
       for (int sub = 0; sub < NB / NBS; ++sub) {
         // S = Q K^T
@@ -664,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
             continue;
           }
           const uint32_t base = lane_k + k_slot * S::kUnit + block_at(key);
-          if (!SCALED) {
+          if (!I8) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               uint32_t f[4];
@@ -674,34 +704,6 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
                 if (k == 0) mma16816<M, true>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
                 else mma16816<M>(s[b][n], qf[k], f[2 * n], f[2 * n + 1]);
               }
-            }
-          } else if (F4) {
-            uint2 bs[2];  // block scales of tokens gid and 8 + gid
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint8_t* at = k_blocks + (key + n * 8 + gid) * (D / 16);
-              if (D == 128) bs[n] = *reinterpret_cast<const uint2*>(at);
-              else bs[n].x = D == 64 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-            }
-#pragma unroll
-            for (int k = 0; k < D / 16; k += D == 32 ? 2 : 4) {
-              uint32_t f[4];
-              if (D == 32) ldsm2(f, base);
-              else ldsm4(f, piece(base, k / 4));
-              constexpr int kPieces = D == 32 ? 1 : 2;  // of 32 values
-#pragma unroll
-              for (int p = 0; p < kPieces; ++p)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  const uint32_t x = f[kPieces * n + p];
-                  const int g = k / 2 + p;  // the row's piece, whose block of this thread is 2 g + tig / 2
-                  const uint32_t sc = e4m3_f16x2(__byte_perm(g < 2 ? bs[n].x : bs[n].y, 0, (g & 1) * 0x22 + (tig >> 1) * 0x11));
-                  const uint32_t e0 = mul2<M>(e2m1_f16x2<0>(x), sc), e1 = mul2<M>(e2m1_f16x2<1>(x), sc);
-                  const uint32_t d0 = mul2<M>(e2m1_f16x2<2>(x), sc), d1 = mul2<M>(e2m1_f16x2<3>(x), sc);
-                  if (g == 0) mma16816<M, true>(s[b][n], qf[0], e0, e1);
-                  else mma16816<M>(s[b][n], qf[2 * g], e0, e1);
-                  mma16816<M>(s[b][n], qf[2 * g + 1], d0, d1);
-                }
             }
           } else {
 #pragma unroll
@@ -726,13 +728,13 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
           if (!ok) return;
         }
         float nA = -INFINITY, nB = -INFINITY;
-        float2 sv[NBS][2];  // V's row scales
+        float2 sv[NBS][2];  // 8 bits: V's row scales
 #pragma unroll
         for (int b = 0; b < NBS; ++b)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int key = ((sub * NBS + b) * KP + kp) * 16 + n * 8 + 2 * tig;
-            if (SCALED) {
+            if (I8) {
               const float2 sk = *reinterpret_cast<const float2*>(k_sc + key);
               sv[b][n] = *reinterpret_cast<const float2*>(v_sc + key);
               s[b][n][0] *= sk.x;
@@ -745,11 +747,11 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
             if (MASK) {  // tokens that are not seen are out
               if (key < j0 || key >= j1) {
                 s[b][n][0] = s[b][n][2] = -INFINITY;
-                if (SCALED) sv[b][n].x = 0.f;
+                if (I8) sv[b][n].x = 0.f;
               }
               if (key + 1 < j0 || key + 1 >= j1) {
                 s[b][n][1] = s[b][n][3] = -INFINITY;
-                if (SCALED) sv[b][n].y = 0.f;
+                if (I8) sv[b][n].y = 0.f;
               }
             }
             nA = fmaxf(nA, fmaxf(s[b][n][0], s[b][n][1]));
@@ -759,13 +761,13 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
         auto logit = [](float s, float c) { return __fmul_rn(s, c); };
         nA = logit(nA, cA);
         if (!R8) nB = logit(nB, cB);
-        // Row scales: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
+        // 8 bits: the magnitude of one token's V scale in each lane, as bits plus x (not seen: 0), and whether it is outside
         auto size_and = [&](uint32_t x) -> uint32_t {
           const int key = ((sub * NBS + (NBS == 2 ? lane >> 4 : 0)) * KP + kp) * 16 + (lane & 15);
           return !MASK || (key >= j0 && key < j1) ? (__float_as_uint(v_sc[key]) & 0x7fffffffu) + x : 0u;
         };
         auto is_outside = [&]() { return size_and(__float_as_uint(mulA) - (251u << 23)) > 11u << 23; };  // (less the bits of hi / 2^11)
-        const bool outside = SCALED && is_outside();
+        const bool outside = I8 && is_outside();
         // The exponents' base follows the running maximum only when a logit passes it by more than kGrow: most steps then need
         // neither shuffles nor a rescaling.
         if (__any_sync(0xffffffffu, nA > mA + kGrow || (!R8 && nB > mB + kGrow) || outside)) {
@@ -788,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
             lA *= fA;
             if (!R8) lB *= fB;
           }
-          if (SCALED) {
+          if (I8) {
             const int top = (int)(__reduce_max_sync(0xffffffffu, size_and(0u)) >> 23);
             if (mulA == 0.f) mulA = mulB = power(262 - min(max(top + 4, 12), 254));
             if (__any_sync(0xffffffffu, is_outside())) {
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
               lA += pA0 + pA1;
               if (!R8) lB += pB0 + pB1;
             }
-            if (SCALED) {
+            if (I8) {
               pA0 *= sv[b][n].x * fabsf(mulA);
               pA1 *= sv[b][n].y * fabsf(mulA);
               if (!R8) {
@@ -875,58 +877,11 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (!I8 && MASK) {
             const int key = key0 + 2 * tig;
-            constexpr uint32_t kFirst = F4 ? 0xffu : 0xffffu, kSecond = F4 ? 0xff00u : 0xffff0000u;
-            keep0 = (key >= j0 && key < j1 ? kFirst : 0u) | (key + 1 >= j0 && key + 1 < j1 ? kSecond : 0u);
-            keep1 = (key + 8 >= j0 && key + 8 < j1 ? kFirst : 0u) | (key + 9 >= j0 && key + 9 < j1 ? kSecond : 0u);
+            keep0 = (key >= j0 && key < j1 ? 0xffffu : 0u) | (key + 1 >= j0 && key + 1 < j1 ? 0xffff0000u : 0u);
+            keep1 = (key + 8 >= j0 && key + 8 < j1 ? 0xffffu : 0u) | (key + 9 >= j0 && key + 9 < j1 ? 0xffff0000u : 0u);
           }
           const uint32_t base = lane_v + v_slot * S::kUnit + block_at(key0);
-          if (F4) {
-            // A loaded register holds 4 values of two tokens. Block scales of tokens 2 tig, 2 tig + 1 and 8 further, those that are not
-            // seen cleared (they may be no numbers).
-            uint4 bs[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint8_t* at = v_blocks + (key0 + t * 8 + 2 * tig) * (D / 16);
-              if (D == 128) {
-                bs[t] = *reinterpret_cast<const uint4*>(at);
-              } else if (D == 64) {
-                const uint2 x = *reinterpret_cast<const uint2*>(at);
-                bs[t] = make_uint4(x.x, 0, x.y, 0);
-              } else {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(at);
-                bs[t] = make_uint4(x, 0, x >> 16, 0);
-              }
-            }
-            const uint32_t pick = (gid >> 2) * 0x11 + 0x40;  // block gid / 4 of a piece's two, of either token
-#pragma unroll
-            for (int c = 0; c < (D + 63) / 64; ++c) {
-              uint32_t f[4];
-              if (D == 32) ldsm2_trans(f, base);
-              else ldsm4_trans(f, piece(base, c));
-#pragma unroll
-              for (int p = 0; p < (D == 32 ? 1 : 2); ++p) {
-                const int g = 2 * c + p;
-                uint32_t v[2][4];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                  const uint32_t x = f[2 * p + t];
-                  uint32_t both = __byte_perm(g < 2 ? bs[t].x : bs[t].y, g < 2 ? bs[t].z : bs[t].w, pick + (g & 1) * 0x22);
-                  if (MASK) both &= t ? keep1 : keep0;
-                  const uint32_t sc = e4m3_f16x2(both);
-                  const uint32_t y0 = e2m1_f16x2<0>(x), y1 = e2m1_f16x2<1>(x), y2 = e2m1_f16x2<2>(x), y3 = e2m1_f16x2<3>(x);
-                  v[t][0] = mul2<M>(__byte_perm(y0, y2, 0x5410), sc);
-                  v[t][1] = mul2<M>(__byte_perm(y0, y2, 0x7632), sc);
-                  v[t][2] = mul2<M>(__byte_perm(y1, y3, 0x5410), sc);
-                  v[t][3] = mul2<M>(__byte_perm(y1, y3, 0x7632), sc);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {  // values 4 gid + e of the piece's 32 form an n-tile
-                  mma16816<M>(o[4 * g + e], hi, v[0][e], v[1][e]);
-                  if (!R8) mma16816<M>(o[4 * g + e], lw, v[0][e], v[1][e]);
-                }
-              }
-            }
-          } else if (!I8) {
+          if (!I8) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t f[4];
@@ -974,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
       const int v_slot = two ? (ks + 1 == RING ? 0 : ks + 1) : ks;
       const uint32_t v_phase = v_slot < ks ? phase ^ 1 : phase;
       const int k0 = pt.k0 + i * TK;
-      if (D < 128 && k0 >= pt.lo && k0 + TK <= pt.len) step(std::false_type(), ks, v_slot, v_phase, 0, TK);
+      if ((D < 128 || F4) && k0 >= pt.lo && k0 + TK <= pt.len) step(std::false_type(), ks, v_slot, v_phase, 0, TK);
       else step(std::true_type(), ks, v_slot, v_phase, max(pt.lo - k0, 0), min(pt.len - k0, TK));
       if (!ok) return;
       __syncwarp();
@@ -987,7 +942,8 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     }
 
     // ---- the part's end: the warps' (m, l, o) to shared memory, and summed ----
-    if (!kOnesSum) {
+    if (F4) {
+    } else if (!kOnesSum) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
         lA += __shfl_xor_sync(0xffffffffu, lA, d);
@@ -997,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
       lA = R8 ? ls[0] + ls[2] : ls[0];
       lB = ls[2];
     }
-    const float o_mulA = SCALED ? power(254 - exponent(mulA)) : 1.f, o_mulB = SCALED ? power(254 - exponent(mulB)) : 1.f;  // (1 / mul)
+    const float o_mulA = I8 ? power(254 - exponent(mulA)) : 1.f, o_mulB = I8 ? power(254 - exponent(mulB)) : 1.f;  // (1 / mul)
     // values c .. c + 3 of query row g of a (request, head), all tokens joined: the output; or so far: to a place of the
     // workspace
     auto finish = [&](const Part& of, int g, int c, float m, float l, const float* acc) {
@@ -1022,8 +978,10 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
       float* const s_m = s_o + kConsumers * S::kORows * S::kORow;
       float* const s_l = s_m + kConsumers * S::kORows;
       ++areas;
+      if constexpr (F4)
+        heads4.store(s_o + warp * S::kORows * S::kORow, s_m + warp * S::kORows, s_l + warp * S::kORows, S::kORow, G - mt * 16);
 #pragma unroll
-      for (int half = 0; half < S::kORows / 8; ++half) {
+      for (int half = 0; half < (F4 ? 0 : S::kORows / 8); ++half) {
         const bool upper = half != 0;
         if (mt * 16 + upper * 8 + gid >= G) continue;
         const int row = warp * S::kORows + half * 8 + gid;
@@ -1033,18 +991,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
         for (int j = 0; j < D / 8; ++j) {
           const float x = (R8 ? o[j][0] + o[j][2] : upper ? o[j][2] : o[j][0]) * o_mul;
           const float y = (R8 ? o[j][1] + o[j][3] : upper ? o[j][3] : o[j][1]) * o_mul;
-          if (F4) {
-            // (column 2 tig of an n-tile is dim 4 (2 tig) + j mod 4 of its piece, the next column 4 further)
-            if (j & 3) continue;
-            float u[4], v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              u[e] = (R8 ? o[j + e][0] + o[j + e][2] : upper ? o[j + e][2] : o[j + e][0]) * o_mul;
-              v[e] = (R8 ? o[j + e][1] + o[j + e][3] : upper ? o[j + e][3] : o[j + e][1]) * o_mul;
-            }
-            *reinterpret_cast<float4*>(dst + j * 8 + 8 * tig) = make_float4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<float4*>(dst + j * 8 + 8 * tig + 4) = make_float4(v[0], v[1], v[2], v[3]);
-          } else if (!I8) {
+          if (!I8) {
             *reinterpret_cast<float2*>(dst + j * 8 + 2 * tig) = make_float2(x, y);
           } else if (j & 1) {
             // (even dims from the tile before: dims 4 tig .. 4 tig + 3 of the 16)

@@ -1,0 +1,6 @@
+// The paged history attention's kernels for rows of 64 values in 4 bits (k_kv_attn.cuh).
+#include "k_kv_attn.cuh"
+
+namespace cvr {
+KvAttendKernel kv_attend_kernel_fp4_64(int dtype, int group) { return kv::instance<64, kKv4>(dtype, group); }
+}  // namespace cvr

@@ -41,7 +41,7 @@ def test_names():
         assert "CVR_DTYPE_FP4 = 3" in f.read()
 
 
-@pytest.mark.parametrize("name", ["cvr_kv_rows.cuh", "k_kv_weigh.cu", "k_kv_evict.cu", "k_kv_attn_fp4.cu"])
+@pytest.mark.parametrize("name", ["cvr_kv_rows.cuh", "k_kv_weigh.cu", "k_kv_evict.cu", "k_kv_attn_fp4.cuh"])
 def test_no_read_only_loads(name):
     """What a kernel reads may still be written when it starts (programmatic dependent launch)."""
     with open(os.path.join(CSRC, name)) as f:
