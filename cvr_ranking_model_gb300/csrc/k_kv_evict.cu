@@ -4,37 +4,64 @@
 // out, of the rows that stay.
 //
 // A (request, kv head) is one cluster's, of 1 to 8 CTAs:
-//   1. Selection. Weights become whole numbers that order as they do; the b-th largest is found by its four bytes, from the
-//      highest: a histogram of the next byte of the numbers that begin like it, summed over the cluster.
+//   1. Selection. Weights become whole numbers that order as they do; the b-th largest is found by its 11, 11 and 10 bits, from the
+//      highest: a histogram of the next bits of the numbers that begin like it, summed over the cluster.
 //   2. The list `kept`, in order: every warp counts and then writes what stays of its share of the tokens; of the tokens whose
 //      weight is the b-th largest the earliest stay.
-//   3. Rows. Place i gets the row of token kept[i] >= i. In rounds, places in order: the cluster reads a round's rows into
-//      registers, meets, and writes them. A round's places lie at or before the tokens that it and later rounds read, and behind none of
-//      them is written before all have been read: so nothing is lost, and rows that do not move are the same again.
+//   3. Rows. Place i gets the row of token kept[i] >= i. Rounds of places in order: asynchronous copies bring a round's rows to shared
+//      memory, two rounds ahead; when the cluster has a round's rows, it meets and writes them to their places. These lie at or before
+//      the tokens that this and later rounds read, so nothing is written before it has been read, and reading ahead reads nothing
+//      written. A thread writes the pieces that it brought.
 // Pages behind the places go back to the free list, in blocks of requests of their own: what they need, the lengths, is known.
+#include <cstddef>
+
 #include "../../include/cvr.h"
 #include "cvr_kv_rows.cuh"
 
 namespace cvr {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+#ifndef EVT
+#define EVT 256
+#define EVB 3
+#define EVM 4
+#endif
+#ifndef EVS
+#define EVS 3
+#define EVK 49152
+#endif
+constexpr int kThreads = EVT, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256, kCopies = 8;  // a histogram's copies: lanes that meet in one bin mostly count in different ones
-constexpr int kKeys = 8192;              // a CTA's share of the weights that shared memory holds; longer shares are read again
-constexpr int kInFlight = 8;             // 16-byte pieces of rows in flight per thread
+constexpr int kBins = 2048, kPerThread = kBins / kThreads;
+constexpr int kPieces = 4;               // 16-byte pieces of rows per thread and round
+constexpr int kStages = EVS, kStageBytes = kThreads * kPieces * 16;  // rounds of rows in shared memory, and the most that one takes
+constexpr int kMaxRows = 64;             // rows of a round and CTA
+constexpr int kLooked = kStages + 2;     // rounds whose rows' offsets are held: looked up a round before they are read
+// a CTA's share of the weights that shared memory holds; longer shares are read again
+constexpr int kKeys = EVK / 4 - kBins;
 
 struct __align__(16) Shared {
-  uint32_t hist[kBins * kCopies];
-  uint32_t mine[kBins];   // this CTA's histogram, read by the cluster
-  uint32_t total[kBins];  // the cluster's
   uint32_t above, ties;   // this CTA's tokens over the b-th largest weight, and of that weight, read by the cluster
   uint32_t w_above[kWarps], w_ties[kWarps];
-  uint32_t found, rest;   // the byte, and how many are wanted of its bin
-  int64_t sum[kWarps], sum2[kWarps];
-  uint32_t start[kThreads + 1];
-  uint32_t keys[kKeys];
+  uint32_t found, rest;   // the next bits, and how many are wanted of their bin
+  int64_t sum[kWarps], sum2[kWarps], sum3[kWarps];
+  int64_t from[kLooked][2][kMaxRows], to[kLooked][2][kMaxRows];  // where rows are in the pools, and go (-1: nowhere)
+  struct {
+    uint2 blocks[2];       // block scales (of rows of 32 values those of two tokens)
+    float weight, scale[2];
+    int page, pos;         // where the row goes (page -1: nowhere)
+  } row[kStages][kMaxRows];
+  union {
+    struct {  // while tokens are selected
+      uint32_t hist[kBins];  // read by the cluster
+      uint32_t keys[kKeys];
+    };
+    uint32_t start[kThreads + 1];
+    __align__(16) uint8_t rows[kStages * kStageBytes];  // while rows move
+  };
 };
+static_assert(offsetof(Shared, rows) % 16 == 0 && offsetof(Shared, row) % 8 == 0 && sizeof(Shared::row[0][0]) % 8 == 0,
+              "what the copies into shared memory ask for");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -59,6 +86,12 @@ __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) 
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void async_in(void* dst, const void* src) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 
 // Numbers that order as weights do, both zeros the same and NaN below all.
@@ -125,7 +158,7 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
   if (lane == 31) s.sum[warp] = wide;
   if (lane == 0) {
     s.sum2[warp] = before;
-    reinterpret_cast<int64_t*>(s.hist)[warp] = all;
+    s.sum3[warp] = all;
   }
   __syncthreads();
   before = all = 0;
@@ -135,7 +168,7 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
     if (w < warp) ahead += s.sum[w];
     items += s.sum[w];
     before += s.sum2[w];
-    all += reinterpret_cast<int64_t*>(s.hist)[w];
+    all += s.sum3[w];
   }
   if (a.free_pages) {
     int head = *a.free_head;
@@ -154,8 +187,8 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
     const uint32_t end = s.start[kThreads];
     for (int64_t x = skip + tid; x < end; x += kThreads) {
       int k = 0;
-      for (int step = kThreads / 2; step > 0; step >>= 1)
-        if (s.start[k + step] <= x) k += step;
+      for (int step = 256; step > 0; step >>= 1)
+        if (k + step < kThreads && s.start[k + step] <= x) k += step;
       const Request o = request_of(a, r0 + k, &ignored);
       a.free_pages[at0 + x] = a.table[(int64_t)(r0 + k) * a.max_pages + stays(a, o) + (int)(x - s.start[k])];
     }
@@ -164,13 +197,16 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ KvEvictArgs a, int n_release) {
-  extern __shared__ uint8_t smem_raw[];
+__global__ void __launch_bounds__(kThreads, EVB) evict_kernel(const __grid_constant__ KvEvictArgs a, int n_release) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int64_t n_items = n_release + (int64_t)a.n_req * a.kv_heads;
   const int page_mask = (1 << a.page_log2) - 1;
+  // 16-byte pieces of a row in a pool and in both (powers of two), rows of a round
+  const int row_vecs = kv_row_bytes(CODE, a.head_dim) / 16, pools = a.pool[1] ? 2 : 1, log2_vecs = 31 - __clz(row_vecs * pools);
+  const int rows = min(kMaxRows, kThreads * kPieces >> log2_vecs);
   int bad = 0, ignored = 0;
   pdl_trigger();
   pdl_wait();
@@ -187,67 +223,81 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     int32_t* const kept = a.kept + ((int64_t)r * a.kv_heads + h) * a.keep;
     auto page_of = [&](int j) {  // of token j, 0 where the entry is none of the pool
       const int p = row[j >> a.page_log2];
-      if ((unsigned)p < (unsigned)a.n_pages) return p;
-      bad |= kKvErrPage;
-      return 0;
+      const bool ok = (unsigned)p < (unsigned)a.n_pages;
+      bad |= ok ? 0 : kKvErrPage;  // (without a branch: loads of several tokens are in flight together)
+      return ok ? p : 0;
     };
     auto key_of = [&](int j) { return order_of(__ldcg(a.weight + ((((int64_t)page_of(j) * a.kv_heads + h) << a.page_log2) + (j & page_mask)))); };
 
     // ---- 1. the b-th largest weight of the tokens [first, n - last) ----
     const int m = n - a.first - a.last, b = a.keep - a.first - a.last;  // (b < m)
     const int c0 = a.first + (int)((int64_t)m * rank / C), c1 = a.first + (int)((int64_t)m * (rank + 1) / C);  // this CTA's share
-    const bool held = c1 - c0 <= kKeys;
-    auto key = [&](int j) { return held ? s.keys[j - c0] : key_of(j); };
-    uint32_t threshold = 0, ties = 0;  // weights over it stay, and this many of those that are it
-    if (b > 0) {
+    const bool held = c1 - c0 <= kKeys - 32;  // (a warp's last step may look behind the share)
+    // f(token, its number) for tokens from, from + step, .. of this CTA's share, from the share held or from their pages
+    auto each = [&](int from, int to, int step, auto f) {
       if (held) {
-#pragma unroll 4
-        for (int j = c0 + tid; j < c1; j += kThreads) s.keys[j - c0] = key_of(j);
+#pragma unroll 8
+        for (int j = from; j < to; j += step) f(j, s.keys[j - c0]);
+      } else {
+#pragma unroll 8
+        for (int j = from; j < to; j += step) f(j, key_of(min(j, n - 1)));
       }
+    };
+    uint32_t threshold = 0, ties = 0;  // numbers over it stay, and this many of those that are it
+    if (b > 0) {
       uint32_t want = b;
 #pragma unroll 1
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < kBins * kCopies; i += kThreads) s.hist[i] = 0;
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int j = c0 + tid; j < c1; j += kThreads) {
-          const uint32_t k = key(j);
-          if (shift == 24 || (k ^ threshold) >> (shift + 8) == 0) atomicAdd(&s.hist[(k >> shift & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
-        }
-        __syncthreads();
-        if (tid < kBins) {
-          uint32_t sum = 0;
-#pragma unroll
-          for (int i = 0; i < kCopies; ++i) sum += s.hist[tid * kCopies + i];
-          s.mine[tid] = sum;
+        if (pass == 0 && held) {
+          // (the weights come from memory: as many in flight as registers allow)
+#pragma unroll 16
+          for (int j = c0 + tid; j < c1; j += kThreads) {
+            const uint32_t k = key_of(j);
+            s.keys[j - c0] = k;
+            atomicAdd(&s.hist[k >> 21], 1u);
+          }
+        } else {
+          each(c0 + tid, c1, kThreads, [&](int, uint32_t k) {
+            if (pass == 0 || ((k ^ threshold) >> (shift + (pass == 1 ? 11 : 10))) == 0) atomicAdd(&s.hist[k >> shift & mask], 1u);
+          });
         }
         meet(C);
-        if (tid < kBins) {
-          uint32_t sum = 0;
-          if (C == 1) sum = s.mine[tid];
+        // thread t has the bins from kBins - 1 - kPerThread t down: sums from the top
+        uint32_t count[kPerThread], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+          const uint32_t* const bin = &s.hist[kBins - 1 - tid * kPerThread - i];
+          count[i] = 0;
+          if (C == 1) count[i] = *bin;
           else
-            for (uint32_t c = 0; c < C; ++c) sum += peer_load(&s.mine[tid], c);
-          s.total[tid] = sum;
+            for (uint32_t c = 0; c < C; ++c) count[i] += peer_load(bin, c);
+          sum += count[i];
         }
+        uint32_t incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += u;
+        }
+        if (lane == 31) s.w_above[warp] = incl;
         __syncthreads();
-        if (warp == 0) {
-          // lane l has bins 255 - 8 l .. 248 - 8 l: sums from the top
-          uint32_t sum = 0;
+        uint32_t over = incl - sum;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum += s.total[255 - lane * 8 - i];
-          uint32_t incl = sum;
+        for (int w = 0; w < kWarps; ++w) over += w < warp ? s.w_above[w] : 0;
+        if (over < want && want <= over + sum) {
+          int bin = kBins - 1 - tid * kPerThread;
 #pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += u;
-          }
-          const unsigned reach = __ballot_sync(0xffffffffu, incl >= want);
-          if (lane == __ffs(reach) - 1) {
-            uint32_t over = incl - sum;
-            int bin = 255 - lane * 8;
-            while (over + s.total[bin] < want) over += s.total[bin--];
-            s.found = bin;
-            s.rest = want - over;
+          for (int i = 0; i < kPerThread; ++i) {
+            if (over < want && want <= over + count[i]) {
+              s.found = bin;
+              s.rest = want - over;
+            }
+            over += count[i];
+            --bin;
           }
         }
         meet(C);  // (also: all have read the histograms)
@@ -261,11 +311,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     const int w0 = c0 + (int)((int64_t)(c1 - c0) * warp / kWarps), w1 = c0 + (int)((int64_t)(c1 - c0) * (warp + 1) / kWarps);
     if (b > 0) {
       uint32_t above = 0, equal = 0;
-      for (int j = w0 + lane; j < w1; j += 32) {
-        const uint32_t k = key(j);
+      each(w0 + lane, w1, 32, [&](int, uint32_t k) {
         above += k > threshold;
         equal += k == threshold;
-      }
+      });
       above = __reduce_add_sync(0xffffffffu, above);
       equal = __reduce_add_sync(0xffffffffu, equal);
       if (lane == 0) {
@@ -274,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       }
       __syncthreads();
       uint32_t at = 0, tie = 0, cta_above = 0, cta_ties = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) {
           at += s.w_above[w];
@@ -294,95 +344,149 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         }
       }
       // the place of the next that stays: those over the threshold and the ties so far, at most `ties` of them
-      for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t k = j < w1 ? key(j) : 0u;
-        const bool is_above = j < w1 && k > threshold, is_tie = j < w1 && k == threshold;
-        const unsigned over = __ballot_sync(0xffffffffu, is_above), same = __ballot_sync(0xffffffffu, is_tie), below = (1u << lane) - 1;
-        const uint32_t my_tie = tie + __popc(same & below);
-        const uint32_t place = at + __popc(over & below) + min(my_tie, ties);
-        // (in bounds whatever the weights do meanwhile, as those of a page that is another request's too)
-        if ((is_above || (is_tie && my_tie < ties)) && place < (uint32_t)b) kept[a.first + place] = j;
+      at += min(tie, ties);
+      const unsigned below = (1u << lane) - 1;
+      // (whole warps stay together; places are in bounds whatever the weights do meanwhile, as those of a page that is another
+      // request's too)
+      each(w0 + lane, w0 + (w1 - w0 + 31) / 32 * 32 + lane, 32, [&](int j, uint32_t k) {
+        const bool in = j < w1, is_above = in && k > threshold;
+        const unsigned over = __ballot_sync(0xffffffffu, is_above);
+        if (__any_sync(0xffffffffu, in && k == threshold) && tie < ties) {
+          const unsigned same = __ballot_sync(0xffffffffu, in && k == threshold);
+          const uint32_t my_tie = tie + __popc(same & below), before = min(my_tie, ties) - tie;
+          const uint32_t place = at + __popc(over & below) + before;
+          if ((is_above || (same >> lane & 1 && my_tie < ties)) && place < (uint32_t)b) kept[a.first + place] = j;
+          const uint32_t taken = min(tie + __popc(same), ties) - tie;
+          tie += taken;
+          at += taken;
+        } else {
+          const uint32_t place = at + __popc(over & below);
+          if (is_above && place < (uint32_t)b) kept[a.first + place] = j;
+        }
         at += __popc(over);
-        tie += __popc(same);
-      }
+      });
     }
     for (int i = rank * kThreads + tid; i < a.first; i += C * kThreads) kept[i] = i;
     for (int i = rank * kThreads + tid; i < a.last; i += C * kThreads) kept[a.keep - a.last + i] = n - a.last + i;
     meet(C);  // (the list is written, and every weight has been read)
 
     // ---- 3. rows, scales and weights, in rounds of `rows` places per CTA ----
-    const int row_vecs = kv_row_bytes(CODE, a.head_dim) / 16, pools = a.pool[1] ? 2 : 1, vecs = row_vecs * pools;  // (powers of two)
-    const int at_once = kThreads / vecs, rows = min(kThreads, at_once * kInFlight);
-    const int vec = tid % vecs, w = vec / row_vecs, part = vec % row_vecs;
-    auto where = [&](int p, int j) {
-      return static_cast<char*>(a.pool[w]) + p * a.stride[w][0] + h * a.stride[w][1] + (j & page_mask) * a.stride[w][2] + part * 16;
-    };
-    // (a row of a page that is none of the pool's is not written)
-    auto token = [&](int64_t i) { return min(max(__ldcg(kept + i), 0), n - 1); };  // (in bounds, as above)
-    auto writable = [&](int j) { return (unsigned)row[j >> a.page_log2] < (unsigned)a.n_pages; };
-#pragma unroll 1
-    for (int64_t i0 = (int64_t)rank * rows; i0 - (int64_t)rank * rows < a.keep; i0 += (int64_t)C * rows) {
-      const int n_rows = (int)max((int64_t)0, min((int64_t)rows, a.keep - i0));
-      uint4 x[kInFlight];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int i = tid / vecs + u * at_once;
-        if (i < n_rows) {
-          const int j = token(i0 + i);
-          x[u] = __ldcg(reinterpret_cast<const uint4*>(where(page_of(j), j)));
-        }
+    const int n_rounds = (int)(((int64_t)a.keep + (int64_t)C * rows - 1) / ((int64_t)C * rows));
+    auto place = [&](int q) { return ((int64_t)q * C + rank) * rows + tid; };  // this thread's of round q
+    auto has = [&](int q) { return tid < rows && q < n_rounds && place(q) < a.keep; };
+    // Where rows of a round come from and go to. Loads are issued a round before what they bring is used: the list's entry, then the
+    // table's entries.
+    int listed = has(0) ? __ldcg(kept + place(0)) : 0, token = 0, from_page = 0, to_page = 0;
+    auto entries = [&](int q) {  // of round q, whose list entry has come; and the next list entry
+      if (has(q)) {
+        token = min(max(listed, 0), n - 1);  // (in bounds, as above)
+        from_page = row[token >> a.page_log2];
+        to_page = row[(int)place(q) >> a.page_log2];
       }
-      float weight = 0.f, scale[2] = {0.f, 0.f};
-      uint2 blocks[2] = {};
-      if (tid < n_rows) {
-        const int j = token(i0 + tid);
-        const int64_t page_head = (int64_t)page_of(j) * a.kv_heads + h;
-        const int pos = j & page_mask;
-        weight = __ldcg(a.weight + (page_head << a.page_log2) + pos);
+      if (has(q + 1)) listed = __ldcg(kept + place(q + 1));
+    };
+    auto offset = [&](int w, int page, int pos) { return page * a.stride[w][0] + h * a.stride[w][1] + pos * a.stride[w][2]; };
+    auto look_up = [&](int q) {  // round q's offsets, its entries have come
+      if (tid < rows && q < n_rounds) {
+        const bool there = has(q), ok = there && (unsigned)from_page < (unsigned)a.n_pages, writes = there && (unsigned)to_page < (unsigned)a.n_pages;
+        if (there && !(ok && writes)) bad |= kKvErrPage;
+        const int from = ok ? from_page : 0, pos = token & page_mask, to_pos = (int)place(q) & page_mask;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          if (CODE == kKv16 || v >= pools) continue;
-          if (CODE == kKv8) scale[v] = __ldcg(static_cast<const float*>(a.scale[v]) + (page_head << a.page_log2) + pos);
-          if (CODE == kKv4) {
-            const uint8_t* const record = kv4_record(a.scale[v], page_head, a.page_log2, a.head_dim);
-            scale[v] = __ldcg(reinterpret_cast<const float*>(record) + pos);
-            const uint8_t* const from = record + (4 << a.page_log2) + pos * (a.head_dim >> 4);
-            if (a.head_dim == 128) blocks[v] = __ldcg(reinterpret_cast<const uint2*>(from));
-            else if (a.head_dim == 64) blocks[v].x = __ldcg(reinterpret_cast<const uint32_t*>(from));
-            else blocks[v].x = __ldcg(reinterpret_cast<const uint16_t*>(from));
+        for (int w = 0; w < 2; ++w) {
+          if (w >= pools) continue;
+          s.from[q % kLooked][w][tid] = there ? offset(w, from, pos) : -1;
+          s.to[q % kLooked][w][tid] = writes ? offset(w, to_page, to_pos) : -1;
+        }
+        // this row's scalars (its own thread writes them too)
+        auto& x = s.row[q % kStages][tid];
+        x.page = writes ? to_page : -1;
+        x.pos = to_pos;
+        if (there) {
+          const int64_t page_head = (int64_t)from * a.kv_heads + h;
+          async_in<4>(&x.weight, a.weight + (page_head << a.page_log2) + pos);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w >= pools) continue;
+            if (CODE == kKv8) async_in<4>(&x.scale[w], static_cast<const float*>(a.scale[w]) + (page_head << a.page_log2) + pos);
+            if (CODE == kKv4) {
+              const uint8_t* const record = kv4_record(a.scale[w], page_head, a.page_log2, a.head_dim);
+              const uint8_t* const blocks = record + (4 << a.page_log2) + pos * (a.head_dim >> 4);
+              async_in<4>(&x.scale[w], record + pos * 4);
+              if (a.head_dim == 128) async_in<8>(&x.blocks[w], blocks);
+              else async_in<4>(&x.blocks[w], reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(blocks) & ~(uintptr_t)3));
+              if (a.head_dim == 32) x.blocks[w].y = pos & 1;  // (which of the two)
+            }
           }
         }
       }
+    };
+    auto piece_of = [&](int u, int* r, int* w, int* part) {  // a thread's u-th piece of a round: row, pool, bytes into the row
+      const int x = tid + u * kThreads, vec = x & ((1 << log2_vecs) - 1);
+      *r = x >> log2_vecs;
+      *w = vec >= row_vecs;
+      *part = (vec & (row_vecs - 1)) * 16;
+    };
+    auto fetch = [&](int q) {
+      if (q < n_rounds) {
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+          int r, w, part;
+          piece_of(u, &r, &w, &part);
+          if (r >= rows) continue;
+          const int64_t from = s.from[q % kLooked][w][r];
+          if (from >= 0) async_in<16>(s.rows + q % kStages * kStageBytes + (tid + u * kThreads) * 16, static_cast<const char*>(a.pool[w]) + from + part);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // A round's scalars come with the group of the round before its rows: look_up(q + 1) precedes fetch(q)'s commit.
+    entries(0);
+    look_up(0);
+    entries(1);
+    __syncthreads();
+    for (int q = 0; q < kStages - 1; ++q) {
+      look_up(q + 1);
+      entries(q + 2);
+      fetch(q);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int q = 0; q < n_rounds; ++q) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       meet(C);
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int i = tid / vecs + u * at_once;
-        if (i < n_rows) {
-          const int to = (int)i0 + i;
-          if (writable(to)) *reinterpret_cast<uint4*>(where(page_of(to), to)) = x[u];
-        }
+      for (int u = 0; u < kPieces; ++u) {
+        int r, w, part;
+        piece_of(u, &r, &w, &part);
+        if (r >= rows) continue;
+        const int64_t to = s.to[q % kLooked][w][r];
+        if (to >= 0) *reinterpret_cast<uint4*>(static_cast<char*>(a.pool[w]) + to + part) = *reinterpret_cast<const uint4*>(s.rows + q % kStages * kStageBytes + (tid + u * kThreads) * 16);
       }
-      if (tid < n_rows && writable((int)i0 + tid)) {
-        const int to = (int)i0 + tid;
-        const int64_t page_head = (int64_t)page_of(to) * a.kv_heads + h;
-        const int pos = to & page_mask;
-        a.weight[(page_head << a.page_log2) + pos] = weight;
+      if (tid < rows) {
+        const auto& x = s.row[q % kStages][tid];
+        if (x.page >= 0) {
+          const int64_t page_head = (int64_t)x.page * a.kv_heads + h;
+          a.weight[(page_head << a.page_log2) + x.pos] = x.weight;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          if (CODE == kKv16 || v >= pools) continue;
-          if (CODE == kKv8) static_cast<float*>(a.scale[v])[(page_head << a.page_log2) + pos] = scale[v];
-          if (CODE == kKv4) {
-            uint8_t* const record = kv4_record(a.scale[v], page_head, a.page_log2, a.head_dim);
-            reinterpret_cast<float*>(record)[pos] = scale[v];
-            uint8_t* const to_blocks = record + (4 << a.page_log2) + pos * (a.head_dim >> 4);
-            if (a.head_dim == 128) *reinterpret_cast<uint2*>(to_blocks) = blocks[v];
-            else if (a.head_dim == 64) *reinterpret_cast<uint32_t*>(to_blocks) = blocks[v].x;
-            else *reinterpret_cast<uint16_t*>(to_blocks) = (uint16_t)blocks[v].x;
+          for (int w = 0; w < 2; ++w) {
+            if (w >= pools) continue;
+            if (CODE == kKv8) static_cast<float*>(a.scale[w])[(page_head << a.page_log2) + x.pos] = x.scale[w];
+            if (CODE == kKv4) {
+              uint8_t* const record = kv4_record(a.scale[w], page_head, a.page_log2, a.head_dim);
+              uint8_t* const blocks = record + (4 << a.page_log2) + x.pos * (a.head_dim >> 4);
+              reinterpret_cast<float*>(record)[x.pos] = x.scale[w];
+              if (a.head_dim == 128) *reinterpret_cast<uint2*>(blocks) = x.blocks[w];
+              else if (a.head_dim == 64) *reinterpret_cast<uint32_t*>(blocks) = x.blocks[w].x;
+              else *reinterpret_cast<uint16_t*>(blocks) = (uint16_t)(x.blocks[w].x >> (x.blocks[w].y * 16));
+            }
           }
         }
       }
+      look_up(q + kStages);
+      entries(q + kStages + 1);
+      fetch(q + kStages - 1);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     meet(C);  // (a CTA's shared memory is read by others until here)
   }
   if (bad) atomicOr(a.err, bad);
@@ -394,7 +498,7 @@ cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)a.n_req * a.kv_heads, most = (int64_t)a.max_pages << a.page_log2;
   // as many CTAs per (request, head) as the SMs hold, of 1024 tokens at least
   int ctas = 1;
-  while (ctas < kMaxCluster && pairs * ctas * 2 <= num_sms * 2 && most / (ctas * 2) >= 1024) ctas *= 2;
+  while (ctas < kMaxCluster && pairs * ctas * 2 <= num_sms * EVM && most / (ctas * 2) >= 1024) ctas *= 2;
   const int64_t items = n_release + pairs, clusters = items < 65536 ? items : 65536;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(clusters * ctas));
