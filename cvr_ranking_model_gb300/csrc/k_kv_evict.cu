@@ -21,48 +21,45 @@
 namespace cvr {
 namespace {
 
-#ifndef EVT
-#define EVT 256
-#define EVB 3
-#define EVM 4
-#endif
-#ifndef EVS
-#define EVS 3
-#define EVK 49152
-#endif
-constexpr int kThreads = EVT, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048, kPerThread = kBins / kThreads;
-constexpr int kPieces = 4;               // 16-byte pieces of rows per thread and round
-constexpr int kStages = EVS, kStageBytes = kThreads * kPieces * 16;  // rounds of rows in shared memory, and the most that one takes
-constexpr int kMaxRows = 64;             // rows of a round and CTA
-constexpr int kLooked = kStages + 2;     // rounds whose rows' offsets are held: looked up a round before they are read
-// a CTA's share of the weights that shared memory holds; longer shares are read again
-constexpr int kKeys = EVK / 4 - kBins;
+constexpr int kReleased = 256;  // requests whose pages one CTA gives back
+constexpr int kBins = 2048;
+constexpr int kPieces = 4;      // 16-byte pieces of rows per thread and round
 
-struct __align__(16) Shared {
+// A CTA's shape: three on an SM, or, where there are too few (request, head)s to fill the GPU, one with rounds of four times the rows.
+template <int THREADS>
+struct Shape {
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kCtasPerSm = THREADS == 256 ? 3 : 1;
+  static constexpr int kPerThread = kBins / THREADS;
+  static constexpr int kStages = THREADS == 256 ? 3 : 2, kStageBytes = THREADS * kPieces * 16;  // rounds of rows in shared memory, and the most that one takes
+  static constexpr int kMaxRows = THREADS == 256 ? 64 : 128;                                  // rows of a round
+  static constexpr int kLooked = kStages + 2;  // rounds whose rows' offsets are held: looked up a round before they are read
+  // a CTA's share of the weights that shared memory holds; longer shares are read again
+  static constexpr int kKeys = kStages * kStageBytes / 4 - kBins;
+};
+
+template <int THREADS>
+struct __align__(16) Shared : Shape<THREADS> {
+  typedef Shape<THREADS> S;
   uint32_t above, ties;   // this CTA's tokens over the b-th largest weight, and of that weight, read by the cluster
-  uint32_t w_above[kWarps], w_ties[kWarps];
+  uint32_t w_above[S::kWarps], w_ties[S::kWarps];
   uint32_t found, rest;   // the next bits, and how many are wanted of their bin
-  int64_t sum[kWarps], sum2[kWarps], sum3[kWarps];
-  int64_t from[kLooked][2][kMaxRows], to[kLooked][2][kMaxRows];  // where rows are in the pools, and go (-1: nowhere)
+  int64_t sum[S::kWarps], sum2[S::kWarps], sum3[S::kWarps];
+  int64_t from[S::kLooked][2][S::kMaxRows], to[S::kLooked][2][S::kMaxRows];  // where rows are in the pools, and go (-1: nowhere)
   struct {
     uint2 blocks[2];       // block scales (of rows of 32 values those of two tokens)
     float weight, scale[2];
     int page, pos;         // where the row goes (page -1: nowhere)
-  } row[kStages][kMaxRows];
+  } row[S::kStages][S::kMaxRows];
   union {
     struct {  // while tokens are selected
       uint32_t hist[kBins];  // read by the cluster
-      uint32_t keys[kKeys];
+      uint32_t keys[S::kKeys];
     };
-    uint32_t start[kThreads + 1];
-    __align__(16) uint8_t rows[kStages * kStageBytes];  // while rows move
+    uint32_t start[kReleased + 1];
+    __align__(16) uint8_t rows[S::kStages * S::kStageBytes];  // while rows move
   };
 };
-static_assert(offsetof(Shared, rows) % 16 == 0 && offsetof(Shared, row) % 8 == 0 && sizeof(Shared::row[0][0]) % 8 == 0,
-              "what the copies into shared memory ask for");
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -124,8 +121,10 @@ __device__ __forceinline__ int stays(const KvEvictArgs& a, const Request& q) {
   return q.cut && a.free_pages ? min(q.held, (a.keep + (1 << a.page_log2) - 1) >> a.page_log2) : q.held;
 }
 
-// Lengths, page counts and the free list of requests [r0, r0 + kThreads), by one CTA.
-__device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
+// Lengths, page counts and the free list of requests [r0, r0 + kReleased), by one CTA.
+template <int THREADS>
+__device__ void release(const KvEvictArgs& a, Shared<THREADS>& s, int r0) {
+  constexpr int kThreads = THREADS, kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bad = 0, ignored = 0;
   int64_t before = 0, all = 0;  // pages given back by the requests before r0, and by all
@@ -142,10 +141,11 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
     all += __shfl_xor_sync(0xffffffffu, all, d);
   }
   const int r = r0 + tid;
+  const bool mine = tid < kReleased && r < a.n_req;
   Request q = {0, 0, false};
-  if (r < a.n_req) q = request_of(a, r, &bad);
+  if (mine) q = request_of(a, r, &bad);
   const int left = stays(a, q), n = q.held - left;
-  if (r < a.n_req) {
+  if (mine) {
     a.lens_out[r] = q.cut ? a.keep : q.len;
     if (a.pages) a.pages[r] = left;
   }
@@ -179,16 +179,16 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
       if (all > head) bad |= kKvErrPages;
     }
     // entry x of these requests' pages goes to position head - all + before + x
-    s.start[tid] = (uint32_t)min(ahead, (int64_t)0xffffffff);
-    if (tid == 0) s.start[kThreads] = (uint32_t)min(items, (int64_t)0xffffffff);
+    if (tid < kReleased) s.start[tid] = (uint32_t)min(ahead, (int64_t)0xffffffff);
+    if (tid == 0) s.start[kReleased] = (uint32_t)min(items, (int64_t)0xffffffff);
     __syncthreads();
     const int64_t at0 = (int64_t)head - all + before;
     const int64_t skip = at0 < 0 ? -at0 : 0;  // (no room in front of the list)
-    const uint32_t end = s.start[kThreads];
+    const uint32_t end = s.start[kReleased];
     for (int64_t x = skip + tid; x < end; x += kThreads) {
       int k = 0;
-      for (int step = 256; step > 0; step >>= 1)
-        if (k + step < kThreads && s.start[k + step] <= x) k += step;
+      for (int step = kReleased / 2; step > 0; step >>= 1)
+        if (s.start[k + step] <= x) k += step;
       const Request o = request_of(a, r0 + k, &ignored);
       a.free_pages[at0 + x] = a.table[(int64_t)(r0 + k) * a.max_pages + stays(a, o) + (int)(x - s.start[k])];
     }
@@ -196,10 +196,15 @@ __device__ void release(const KvEvictArgs& a, Shared& s, int r0) {
   if (bad) atomicOr(a.err, bad);
 }
 
-template <int CODE>
-__global__ void __launch_bounds__(kThreads, EVB) evict_kernel(const __grid_constant__ KvEvictArgs a, int n_release) {
+template <int CODE, int THREADS>
+__global__ void __launch_bounds__(THREADS, Shape<THREADS>::kCtasPerSm) evict_kernel(const __grid_constant__ KvEvictArgs a, int n_release) {
+  typedef Shape<THREADS> S;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kPerThread = S::kPerThread, kStages = S::kStages, kStageBytes = S::kStageBytes;
+  constexpr int kMaxRows = S::kMaxRows, kLooked = S::kLooked, kKeys = S::kKeys;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Shared& s = *reinterpret_cast<Shared*>(smem_raw);
+  typedef Shared<THREADS> Mem;
+  static_assert(offsetof(Mem, rows) % 16 == 0 && offsetof(Mem, row) % 8 == 0 && sizeof(Mem::row[0][0]) % 8 == 0, "what the copies into shared memory ask for");
+  Mem& s = *reinterpret_cast<Mem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int64_t n_items = n_release + (int64_t)a.n_req * a.kv_heads;
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, EVB) evict_kernel(const __grid_const
   pdl_wait();
   for (int64_t item = blockIdx.x / C; item < n_items; item += gridDim.x / C) {
     if (item < n_release) {
-      if (rank == 0) release(a, s, (int)item * kThreads);
+      if (rank == 0) release(a, s, (int)item * kReleased);
       __syncthreads();
       continue;
     }
@@ -492,18 +497,14 @@ __global__ void __launch_bounds__(kThreads, EVB) evict_kernel(const __grid_const
   if (bad) atomicOr(a.err, bad);
 }
 
-template <int CODE>
-cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
-  const int n_release = a.n_req > 0 ? (a.n_req + kThreads - 1) / kThreads : 1;
-  const int64_t pairs = (int64_t)a.n_req * a.kv_heads, most = (int64_t)a.max_pages << a.page_log2;
-  // as many CTAs per (request, head) as the SMs hold, of 1024 tokens at least
-  int ctas = 1;
-  while (ctas < kMaxCluster && pairs * ctas * 2 <= num_sms * EVM && most / (ctas * 2) >= 1024) ctas *= 2;
-  const int64_t items = n_release + pairs, clusters = items < 65536 ? items : 65536;
+template <int CODE, int THREADS>
+cudaError_t launch(const KvEvictArgs& a, int ctas, cudaStream_t s) {
+  const int n_release = a.n_req > 0 ? (a.n_req + kReleased - 1) / kReleased : 1;
+  const int64_t items = n_release + (int64_t)a.n_req * a.kv_heads, clusters = items < 65536 ? items : 65536;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(clusters * ctas));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = sizeof(Shared);
+  lc.blockDim = dim3(THREADS);
+  lc.dynamicSmemBytes = sizeof(Shared<THREADS>);
   lc.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -513,8 +514,17 @@ cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel<CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&lc, evict_kernel<CODE>, a, n_release);
+  cudaError_t e = cudaFuncSetAttribute(evict_kernel<CODE, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<THREADS>));
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&lc, evict_kernel<CODE, THREADS>, a, n_release);
+}
+
+template <int CODE>
+cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
+  // as many CTAs per (request, head) as the SMs hold, of 1024 tokens at least
+  const int64_t pairs = (int64_t)a.n_req * a.kv_heads, most = (int64_t)a.max_pages << a.page_log2;
+  int ctas = 1;
+  while (ctas < kMaxCluster && pairs * ctas * 2 <= num_sms * 2 && most / (ctas * 2) >= 1024) ctas *= 2;
+  return pairs * ctas <= num_sms && most >= 16384 ? launch<CODE, 1024>(a, ctas, s) : launch<CODE, 256>(a, ctas, s);
 }
 
 }  // namespace
