@@ -495,7 +495,7 @@ cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_strid
   a.weight = weight;
   a.q_stride = q_stride;
   a.n_pages = c.n_pages;
-  for (int i = 0; i < 3; ++i) a.k_stride[i] = c.k_stride[i];
+  for (int i = 0; i < 3; ++i) a.k_stride[i] = value_bytes(code_of(c), c.k_stride[i]);
   a.scale = scale;
   a.decay = decay;
   a.n_req = n_req;

@@ -72,7 +72,7 @@ struct KvWeighArgs {
   const float* lse;
   const void* k_scale;
   float* weight;  // [page][head][token]
-  int64_t q_stride, n_pages, k_stride[3];
+  int64_t q_stride, n_pages, k_stride[3];  // (keys' in bytes: page, head, token)
   float scale, decay;
   int n_req, kv_heads, group, page_log2, max_pages;
   int* err;

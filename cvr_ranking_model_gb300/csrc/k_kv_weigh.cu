@@ -6,9 +6,9 @@
 // Work: blocks of 16 tokens of a (request, kv head). The blocks of all requests form one line (request, then head, then
 // position), which the warps of a persistent grid cut into equal runs, so ragged lengths load the SMs alike. A warp computes S =
 // K Q^T on mma.sync m16n8k16 with the tokens on M and 8 query heads on N: a row's sum over the heads is then a sum of two
-// accumulators and two shuffles, and up to 8 heads nothing is padded but the heads themselves. K goes from global memory straight
-// into the fragments: the products' k index is permuted so that a thread's values of a row are 16 consecutive bytes, and the next
-// block's loads are in flight while this one is computed.
+// accumulators and two shuffles, and up to 8 heads nothing is padded but the heads themselves. The products' k index is permuted so
+// that a thread's values of a row are 16 consecutive bytes: every thread copies what it will use to shared memory, asynchronously and
+// some blocks ahead, and reads it back itself, so no warp waits for another and no registers hold what is in flight.
 #include "../../include/cvr.h"
 #include "cvr_kv_rows.cuh"
 
@@ -24,9 +24,22 @@ struct Rows {
   static constexpr int kWords = kv_row_bytes(CODE, D) / 16;             // 32-bit words of a row per thread (4 threads a row)
   static constexpr int kLoad = kWords < 4 ? kWords : 4;                 // words of one load
   static constexpr int kRun = kLoad * 4 * D / kv_row_bytes(CODE, D);    // values of one load
+// a warp's ring of blocks in shared memory: per block and thread its words of rows gid and gid + 8, the rows' scales and block
+  // scales, the old weight and where the new one goes
+  static constexpr int kStages = kWords >= 16 ? 2 : kWords == 8 ? 3 : 4, kScaled = CODE == kKv16 ? 0 : CODE == kKv8 ? 2 : 4;
+  static constexpr int oScale = kWords * 2 * 128, oOld = oScale + kScaled * 128, oWeight = oOld + 128, kStage = oWeight + 256;
+  static constexpr int kWarpBytes = kStages * kStage;
   // the first of this thread's 4 values of k-step ks
   static __device__ __forceinline__ int dim(int ks, int tig) { return ks * 4 / kRun * 4 * kRun + tig * kRun + ks * 4 % kRun; }
 };
+
+// BYTES copied to shared memory asynchronously, or as many zeros
+template <int BYTES>
+__device__ __forceinline__ void copy(void* dst, const void* src, bool there) {
+  const int n = there ? BYTES : 0;
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
 
 __device__ __forceinline__ int64_t scan_before(int64_t x, int64_t* sums, int64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -48,19 +61,24 @@ __device__ __forceinline__ int64_t scan_before(int64_t x, int64_t* sums, int64_t
   return before;
 }
 
+// CTAs that share an SM (two head tiles of rows of 128, or many, need the registers)
+constexpr int ctas_per_sm(int dim, int tiles) { return tiles == 1 || dim < 128 ? 3 : 2; }
+
 // TILES: head tiles held in registers (1 or 2), or 0: any number, in shared memory
 template <typename T, int CODE, int D, int TILES>
-__global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ KvWeighArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(const __grid_constant__ KvWeighArgs a) {
   typedef Rows<CODE, D> R;
   constexpr bool SCALED = CODE != kKv16;
   typedef typename std::conditional<SCALED, __half, T>::type M;  // operand type of the products
   constexpr int KS = D / 16, kHeld = TILES ? TILES : 1;
-  extern __shared__ uint32_t s_q[];  // TILES = 0: per warp [tile][ks][2][lane] fragments, then [tile * 8] factors and lse
+  // the warps' rings, then (TILES = 0) per warp [tile][ks][lane][2] fragments, [tile * 8] factors and lse
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_before[kThreads + 1], s_sums[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int H = a.kv_heads, G = a.group, page_mask = (1 << a.page_log2) - 1;
   const int n_tiles = TILES ? TILES : (G + 7) / 8;
-  uint32_t* const my_q = s_q + warp * n_tiles * (KS * 64 + 16);
+  uint8_t* const my_ring = smem + warp * R::kWarpBytes;
+  uint32_t* const my_q = reinterpret_cast<uint32_t*>(smem + kWarps * R::kWarpBytes) + warp * n_tiles * (KS * 64 + 16);
   float* const my_c = reinterpret_cast<float*>(my_q + n_tiles * KS * 64);
   float* const my_l = my_c + n_tiles * 8;
   pdl_trigger();
@@ -129,67 +147,57 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
       auto entries = [&](int e) { return e + lane < a.max_pages ? row[e + lane] : 0; };
       int ids = entries(e0), more_ids = entries(e0 + 32);
 
-      // a block's rows as loaded: tokens gid and gid + 8
-      struct Block {
-        uint32_t w[2][R::kWords];
-        float scale[2], old;
-        uint32_t block_scale[2];
-        int page[2];
-      };
-      auto load = [&](Block& x, int b) {
-        const int j0 = (t0 + b) * 16;
-        if ((j0 + 15) >> a.page_log2 >= e0 + 32) {  // (a block of two pages never straddles: 32 entries begin at an even one)
-          ids = more_ids;
-          e0 += 32;
-          more_ids = entries(e0 + 32);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = j0 + gid + 8 * u;
-          int page = __shfl_sync(0xffffffffu, ids, ((j >> a.page_log2) - e0) & 31);
-          if (j >= len) page = -1;
-          else if ((unsigned)page >= (unsigned)a.n_pages) {
-            bad |= kKvErrPage;
-            page = -1;
+      // what does not depend on the page: this head's, this thread's
+      const char* const k_head = static_cast<const char*>(a.k) + h * a.k_stride[1] + gid * a.k_stride[2] + tig * (R::kLoad * 4);
+      const uint32_t page_places = (uint32_t)H << a.page_log2;  // rows of a page
+      float* const weight_head = a.weight + ((uint32_t)h << a.page_log2) + gid;
+      const uint32_t record_bytes = (uint32_t)kv_scale_bytes(CODE, D) << a.page_log2;
+      const uint8_t* const scale_head = static_cast<const uint8_t*>(a.k_scale) + (SCALED ? h * record_bytes + gid * 4 : 0);
+      // (4 bytes of the row's block scales, this thread's among them)
+      const int blocks_at = (4 << a.page_log2) + gid * (D / 16 - 4) + (D == 128 ? tig & 2 ? 4 : 0 : 0);
+      auto fetch = [&](int b) {
+        if (b < count) {
+          const int j0 = (t0 + b) * 16;
+          if ((j0 + 15) >> a.page_log2 >= e0 + 32) {  // (a block of two pages never straddles: 32 entries begin at an even one)
+            ids = more_ids;
+            e0 += 32;
+            more_ids = entries(e0 + 32);
           }
-          x.page[u] = page;
-          const int pos = j & page_mask;
-          const int64_t from = page * a.k_stride[0] + h * a.k_stride[1] + pos * a.k_stride[2];
-          const char* p = static_cast<const char*>(a.k) + (CODE == kKv16 ? from * 2 : CODE == kKv8 ? from : from >> 1) + tig * (R::kLoad * 4);
+          uint8_t* const slot = my_ring + (b % R::kStages) * R::kStage;
+          const int e = (j0 >> a.page_log2) - e0, p0 = __shfl_sync(0xffffffffu, ids, e);
+          const int p1 = a.page_log2 == 3 ? __shfl_sync(0xffffffffu, ids, e + 1) : p0;
+          float* at[2];
 #pragma unroll
-          for (int c = 0; c < R::kWords / R::kLoad; ++c) {
-            uint32_t* d = x.w[u] + c * R::kLoad;
-            if (R::kLoad == 4) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (page >= 0) v = *reinterpret_cast<const uint4*>(p + c * 64);
-              d[0] = v.x;
-              d[1 % R::kLoad] = v.y;
-              d[2 % R::kLoad] = v.z;
-              d[3 % R::kLoad] = v.w;
-            } else if (R::kLoad == 2) {
-              uint2 v = make_uint2(0, 0);
-              if (page >= 0) v = *reinterpret_cast<const uint2*>(p);
-              d[0] = v.x;
-              d[1 % R::kLoad] = v.y;
-            } else {
-              d[0] = page >= 0 ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t page = u ? p1 : p0;
+            const int pos = (j0 + 8 * u) & page_mask;  // (of the block's token 8 u)
+            const bool seen = j0 + gid + 8 * u < len, there = seen && page < (uint32_t)a.n_pages;
+            bad |= seen && !there ? kKvErrPage : 0;
+            const uint32_t from = there ? page : 0;  // (rows that are not there are zeros, and nothing is read)
+            const char* p = k_head + from * a.k_stride[0] + pos * a.k_stride[2];
+#pragma unroll
+            for (int c = 0; c < R::kWords / R::kLoad; ++c)
+              copy<R::kLoad * 4>(slot + (u * R::kWords / R::kLoad + c) * (R::kLoad * 128) + lane * (R::kLoad * 4), p + c * 64, there);
+            if (SCALED) {
+              const uint8_t* const record = scale_head + (uint64_t)from * (H * record_bytes) + pos * 4;
+              copy<4>(slot + R::oScale + u * 128 + lane * 4, record, there);
+              if (CODE == kKv4) {
+                const uint8_t* const blocks = record + blocks_at + pos * (D / 16 - 4);
+                copy<4>(slot + R::oScale + (2 + u) * 128 + lane * 4, D == 32 ? (const uint8_t*)((uintptr_t)blocks & ~(uintptr_t)3) : blocks, there);
+              }
             }
+            at[u] = there ? weight_head + (uint64_t)from * page_places + pos : nullptr;
           }
-          const int64_t page_head = (int64_t)page * H + h;
-          if (CODE == kKv8) x.scale[u] = page >= 0 ? static_cast<const float*>(a.k_scale)[(page_head << a.page_log2) + pos] : 0.f;
-          if (CODE == kKv4) {
-            const uint8_t* record = kv4_record(a.k_scale, page_head, a.page_log2, D);
-            const uint8_t* blocks = record + (4 << a.page_log2) + pos * (D / 16);
-            x.scale[u] = page >= 0 ? reinterpret_cast<const float*>(record)[pos] : 0.f;
-            x.block_scale[u] = page < 0 ? 0u : D == 128 ? reinterpret_cast<const uint16_t*>(blocks)[tig] : D == 64 ? blocks[tig] : blocks[tig >> 1];
-          }
+          float* const weight = tig > 1 ? nullptr : tig ? at[1] : at[0];
+          *reinterpret_cast<float**>(slot + R::oWeight + lane * 8) = weight;
+          const bool is_old = weight && j0 + gid + 8 * (tig & 1) < old_end;
+          copy<4>(slot + R::oOld + lane * 4, is_old ? weight : a.weight, is_old);
         }
-        // threads 0 and 1 of a row's four keep the weights of tokens gid and gid + 8
-        const int j = j0 + gid + 8 * (tig & 1), page = tig & 1 ? x.page[1] : x.page[0];
-        x.old = tig < 2 && page >= 0 && j < old_end ? a.weight[(((int64_t)page * H + h) << a.page_log2) + (j & page_mask)] : 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      Block now, next;
-      load(now, 0);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+      for (int b = 0; b < R::kStages - 1; ++b) fetch(b);
 
       // ---- the query rows: fragments, and per head the logits' factor and lse ----
       // As in the attention: q times the scale's sign, -1, 0 or 1; bf16 rows times a power of two, which goes into the factor (on 16-bit
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
           const float2 u = unpack2<T>(x[ks].x), v = unpack2<T>(x[ks].y);
           big = fmaxf(fmaxf(big, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
         }
-        lse = in ? a.lse[((int64_t)r * H + h) * G + head] : 0.f;
+        lse = in ? a.lse[((int64_t)r * H + h) * G + head] : INFINITY;  // (heads that there are none of weigh nothing)
         float up = sign;
         factor = fabsf(a.scale);
         if (std::is_same<T, __nv_bfloat16>::value) {
@@ -254,41 +262,67 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
         }
       }
 
-      auto compute = [&](const Block& x, int b) {
+      auto compute = [&](int b) {
+        const uint8_t* const slot = my_ring + (b % R::kStages) * R::kStage;
+        const int row0 = (t0 + b) * 16 + gid;
         uint32_t sc[2][2] = {};  // 4 bits: the block scales of the thread's words, of tokens gid and gid + 8, as pairs
         if (CODE == kKv4)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            sc[u][0] = e4m3_f16x2(__byte_perm(x.block_scale[u], 0, 0x00));
-            sc[u][1] = D == 128 ? e4m3_f16x2(__byte_perm(x.block_scale[u], 0, 0x11)) : sc[u][0];
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(slot + R::oScale + (2 + u) * 128 + lane * 4);
+            // rows of 128: bytes 2 (tig mod 2) and the next; of 64: tig; of 32: the row's two of the four, tig / 2
+            const uint32_t first = D == 128 ? (tig & 1) * 2 : D == 64 ? tig : (row0 & 1) * 2 + (tig >> 1);
+            sc[u][0] = e4m3_f16x2(__byte_perm(x, 0, first * 0x11));
+            sc[u][1] = D == 128 ? e4m3_f16x2(__byte_perm(x, 0, first * 0x11 + 0x11)) : sc[u][0];
           }
-        auto fragment = [&](int ks, uint32_t* k) {
+        uint32_t words[2][R::kLoad];
+        auto bring = [&](int c) {  // the thread's words of load c of both rows
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            if (CODE == kKv16) {
-              k[u] = x.w[u][(2 * ks) % R::kWords];
-              k[2 + u] = x.w[u][(2 * ks + 1) % R::kWords];
-            } else if (CODE == kKv8) {
-              const uint32_t v = x.w[u][ks % R::kWords] ^ 0x80808080u;
-              k[u] = i8_pair<0x4140>(v);
-              k[2 + u] = i8_pair<0x4342>(v);
+            const uint8_t* from = slot + (u * R::kWords / R::kLoad + c) * (R::kLoad * 128) + lane * (R::kLoad * 4);
+            if (R::kLoad == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from);
+              words[u][0] = v.x;
+              words[u][1 % R::kLoad] = v.y;
+              words[u][2 % R::kLoad] = v.z;
+              words[u][3 % R::kLoad] = v.w;
+            } else if (R::kLoad == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(from);
+              words[u][0] = v.x;
+              words[u][1 % R::kLoad] = v.y;
             } else {
-              const uint32_t v = x.w[u][ks / 2 % R::kWords], s = sc[u][ks / 2 * 2 / R::kWords % 2];
-              k[u] = mul2<M>(ks & 1 ? e2m1_f16x2<2>(v) : e2m1_f16x2<0>(v), s);
-              k[2 + u] = mul2<M>(ks & 1 ? e2m1_f16x2<3>(v) : e2m1_f16x2<1>(v), s);
+              words[u][0] = *reinterpret_cast<const uint32_t*>(from);
             }
           }
         };
-        const float sA = SCALED ? x.scale[0] : 1.f, sB = SCALED ? x.scale[1] : 1.f;
+        // k-steps of a word: half a one on 16-bit pools, one on 8-bit pools, two on 4-bit pools
+        auto fragment = [&](int ks, uint32_t* k) {
+          const int word = CODE == kKv16 ? 2 * ks : CODE == kKv8 ? ks : ks / 2;
+          if (word % R::kLoad == 0 && (CODE != kKv4 || ks % 2 == 0)) bring(word / R::kLoad);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = words[u][word % R::kLoad];
+            if (CODE == kKv16) {
+              k[u] = x;
+              k[2 + u] = words[u][(word + 1) % R::kLoad];
+            } else if (CODE == kKv8) {
+              const uint32_t v = x ^ 0x80808080u;
+              k[u] = i8_pair<0x4140>(v);
+              k[2 + u] = i8_pair<0x4342>(v);
+            } else {
+              const uint32_t scale = sc[u][word * 2 / R::kWords % 2];
+              k[u] = mul2<M>(ks & 1 ? e2m1_f16x2<2>(x) : e2m1_f16x2<0>(x), scale);
+              k[2 + u] = mul2<M>(ks & 1 ? e2m1_f16x2<3>(x) : e2m1_f16x2<1>(x), scale);
+            }
+          }
+        };
+        const float sA = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + lane * 4) : 1.f;
+        const float sB = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + 128 + lane * 4) : 1.f;
         float sumA = 0.f, sumB = 0.f;
-        auto add = [&](const float* s, int tile, float c0, float c1, float l0, float l1) {
-          auto weight = [&](float s, float scale, float c, float l, int head) {
-            const float p = ex2(fmaf(SCALED ? s * scale : s, c, -l) * kLog2e);
-            return head < G ? p : 0.f;
-          };
-          const int head = tile * 8 + 2 * tig;
-          sumA += weight(s[0], sA, c0, l0, head) + weight(s[1], sA, c1, l1, head + 1);
-          sumB += weight(s[2], sB, c0, l0, head) + weight(s[3], sB, c1, l1, head + 1);
+        auto add = [&](const float* s, float c0, float c1, float l0, float l1) {
+          auto weight = [&](float s, float scale, float c, float l) { return ex2(fmaf(SCALED ? s * scale : s, c, -l) * kLog2e); };
+          sumA += weight(s[0], sA, c0, l0) + weight(s[1], sA, c1, l1);
+          sumB += weight(s[2], sB, c0, l0) + weight(s[3], sB, c1, l1);
         };
         if (TILES == 0) {
           uint32_t k[KS][4];
@@ -303,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
               mma16816<M>(s, k[ks], q.x, q.y);
             }
             const float2 c = *reinterpret_cast<const float2*>(my_c + tile * 8 + 2 * tig), l = *reinterpret_cast<const float2*>(my_l + tile * 8 + 2 * tig);
-            add(s, tile, c.x, c.y, l.x, l.y);
+            add(s, c.x, c.y, l.x, l.y);
           }
         } else {
           float s[kHeld][4];
@@ -318,27 +352,25 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
             }
           }
 #pragma unroll
-          for (int tile = 0; tile < kHeld; ++tile) add(s[tile], tile, c0[tile], c1[tile], l0[tile], l1[tile]);
+          for (int tile = 0; tile < kHeld; ++tile) add(s[tile], c0[tile], c1[tile], l0[tile], l1[tile]);
         }
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
           sumA += __shfl_xor_sync(0xffffffffu, sumA, d);
           sumB += __shfl_xor_sync(0xffffffffu, sumB, d);
         }
-        const int j = (t0 + b) * 16 + gid + 8 * (tig & 1), page = tig & 1 ? x.page[1] : x.page[0];
-        if (tig < 2 && page >= 0) {
-          // (the old weight of a token that has none, or of no decay, was not read)
-          const float sum = tig & 1 ? sumB : sumA;
-          a.weight[(((int64_t)page * H + h) << a.page_log2) + (j & page_mask)] = j < old_end ? fmaf(a.decay, x.old, sum) : sum;
+        float* const weight = *reinterpret_cast<float* const*>(slot + R::oWeight + lane * 8);
+        if (weight) {
+          // (the old weight of a token that has none, or of no decay, was not read: 0)
+          const float sum = tig & 1 ? sumB : sumA, old = *reinterpret_cast<const float*>(slot + R::oOld + lane * 4);
+          *weight = row0 + 8 * (tig & 1) < old_end ? fmaf(a.decay, old, sum) : sum;
         }
       };
 #pragma unroll 1
-      for (int b = 0; b < count; b += 2) {
-        if (b + 1 < count) load(next, b + 1);
-        compute(now, b);
-        if (b + 1 == count) break;
-        if (b + 2 < count) load(now, b + 2);
-        compute(next, b + 1);
+      for (int b = 0; b < count; ++b) {
+        fetch(b + R::kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
+        compute(b);
       }
     }
   }
@@ -349,13 +381,14 @@ template <typename T, int CODE, int D>
 cudaError_t launch(const KvWeighArgs& a, int num_sms, cudaStream_t s) {
   const int tiles = (a.group + 7) / 8;
   const int64_t blocks = (((int64_t)a.max_pages << a.page_log2) + 15) / 16 * a.n_req * a.kv_heads;  // at most
-  const int64_t want = (blocks + kWarps - 1) / kWarps, fit = (int64_t)num_sms * 2;
+  const int64_t want = (blocks + kWarps - 1) / kWarps, fit = (int64_t)num_sms * ctas_per_sm(D, tiles > 2 ? 0 : tiles);
   const dim3 grid((unsigned)(want < fit ? want : fit)), block(kThreads);
-  if (tiles == 1) return launch_kernel(weigh_kernel<T, CODE, D, 1>, grid, block, 0, s, true, a);
-  if (tiles == 2) return launch_kernel(weigh_kernel<T, CODE, D, 2>, grid, block, 0, s, true, a);
-  const int smem = kWarps * tiles * (D / 16 * 64 + 16) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(weigh_kernel<T, CODE, D, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e : launch_kernel(weigh_kernel<T, CODE, D, 0>, grid, block, smem, s, true, a);
+  const int smem = kWarps * (Rows<CODE, D>::kWarpBytes + (tiles > 2 ? tiles * (D / 16 * 64 + 16) * 4 : 0));
+  auto run = [&](auto kern) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : launch_kernel(kern, grid, block, smem, s, true, a);
+  };
+  return tiles == 1 ? run(weigh_kernel<T, CODE, D, 1>) : tiles == 2 ? run(weigh_kernel<T, CODE, D, 2>) : run(weigh_kernel<T, CODE, D, 0>);
 }
 
 }  // namespace
