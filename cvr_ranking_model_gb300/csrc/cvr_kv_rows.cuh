@@ -83,8 +83,8 @@ __device__ __forceinline__ uint32_t i8_pair(uint32_t x) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 4-bit floats (e2m1): byte I of x, two of them, as an fp16 pair, and two values rounded to them (to the nearest, ties to even,
-// beyond 6 to 6), the first in the low half of a byte
+// 4-bit floats (e2m1): byte I of x, two of them, as an fp16 pair, and 8 values rounded to them (to the nearest, ties to even,
+// beyond 6 to 6), the first in the lowest bits
 template <int I>
 __device__ __forceinline__ uint32_t e2m1_f16x2(uint32_t x) {
   uint32_t y;
@@ -94,10 +94,13 @@ __device__ __forceinline__ uint32_t e2m1_f16x2(uint32_t x) {
   if (I == 3) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, d;\n}\n" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t e2m1_pair(float a, float b) {
-  uint32_t y;
-  asm("{\n .reg .b8 a;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.u32.u8 %0, a;\n}\n" : "=r"(y) : "f"(a), "f"(b));
-  return y;
+__device__ __forceinline__ uint32_t e2m1_8(const float* y) {
+  uint32_t x;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(x)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return x;
 }
 // the e4m3 numbers in the two low bytes of x as an fp16 pair (exact)
 __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t x) {

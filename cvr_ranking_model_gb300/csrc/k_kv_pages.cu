@@ -346,36 +346,46 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, float big) {
   return make_uint2(four(code), four(code + 4));
 }
 
-// 4-bit codes of 8 values x of a block and the block's scale, of a row whose largest magnitude is `big`, finite, the block's `top`:
-// the quotients of the definition are rounded as in exact arithmetic.
-//   - scale: 448 top is exact and the quotient rounded once to 24 bits. It is no tie of two e4m3 values by that: a quotient of
-//     numbers of 11 and 3 by 11 bits that is not a tie (of 5 bits) lies 2^-16 of it from one.
-//   - codes: y = 2688 x / (big scale) has 16 bits over 15 (2688 = 21 * 2^7), a tie of two codes at most 3: one that is no tie lies
-//     at least 2^-18 of it from one. x (2688 / (big scale)) is within 2^-22 of y, and rounded to 20 bits it is the tie where y is.
+// The 16 4-bit codes of a block x and the block's scale, of a row whose largest magnitude is `big`, finite, the block's `top`: the
+// quotients of the definition are rounded as in exact arithmetic. A quotient that is no tie of two codes or scales lies at least 2^-18
+// of it from one, by its numbers of bits: of the scales 448 top / big, 11 and 3 bits by 11, against ties of 5; of the codes 2688 x / (big
+// scale), 16 bits (2688 = 21 * 2^7) by 15, against ties of 3. The ones computed here are within 2^-21 of theirs, and rounded to 20 bits
+// they are the tie where the exact one is, else on its side of it.
+__device__ __forceinline__ float to_20_bits(float y) { return __uint_as_float((__float_as_uint(y) + 8u) & ~15u); }
 template <typename T>
-__device__ __forceinline__ uint32_t codes4(const uint4& x, float big, float top, uint32_t& scale) {
-  // (a power of two brings rows at the type's ends to where nothing below leaves fp32)
-  const float up = big < 0x1p-60f ? 0x1p64f : big > 0x1p60f ? 0x1p-64f : 1.f;
-  big *= up;
-  const float ratio = big > 0.f ? __fdiv_rn(top * up * 448.f, big) : 0.f;
+__device__ __forceinline__ uint2 codes4(const uint4* x, float big, float top, uint32_t& scale) {
+  uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  if (std::is_same<T, __nv_bfloat16>::value && (big < 0x1p-60f || big > 0x1p60f)) {
+    // a power of two brings rows at the type's ends to where nothing below leaves fp32 (what it makes subnormal has the code 0)
+    const float up = big < 1.f ? 0x1p64f : 0x1p-64f;
+    big *= up;
+    top *= up;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = kv::mul2<T>(w[j], kv::pack2<T>(up, up));
+  }
+  const float ratio = big > 0.f ? to_20_bits(__fdividef(top * 448.f, big)) : 0.f;
   uint16_t s8;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(ratio));
   scale = s8;
-  const float den = big * kv::unpack2<__half>(kv::e4m3_f16x2(scale)).x, c = den > 0.f ? __fdiv_rn(2688.f, den) : 0.f;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t code = 0;
+  const float den = big * kv::unpack2<__half>(kv::e4m3_f16x2(scale)).x, c = den > 0.f ? __fdividef(2688.f, den) : 0.f;
+  uint32_t code[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 v = kv::unpack2<T>(w[j]);
-    auto to_20_bits = [](float y) { return __uint_as_float((__float_as_uint(y) + 8u) & ~15u); };
-    code |= kv::e2m1_pair(to_20_bits(v.x * up * c), to_20_bits(v.y * up * c)) << (8 * j);
+  for (int h = 0; h < 2; ++h) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = kv::unpack2<T>(w[4 * h + j]);
+      y[2 * j] = to_20_bits(v.x * c);
+      y[2 * j + 1] = to_20_bits(v.y * c);
+    }
+    code[h] = kv::e2m1_8(y);
   }
-  return code;
+  return make_uint2(code[0], code[1]);
 }
 
 constexpr int kAppThreads = 256;
 
-template <typename T, int CODE>
+template <typename T, bool I8>
 __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendArgs a) {
   const unsigned vec_row = a.head_dim >> 3;  // vectors of 8 values per row: 4, 8 or 16, within one warp
   const unsigned vec_tok = a.kv_heads * vec_row;
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
         if (!a.src[w]) continue;
         const uint4 x = row[w];
         const int64_t at = page * a.stride[w][0] + head * a.stride[w][1] + pos * a.stride[w][2] + piece * 8;
-        if (CODE == kKv16) {
+        if (!I8) {
           if (ok) *reinterpret_cast<uint4*>(static_cast<T*>(a.pool[w]) + at) = x;
           continue;
         }
@@ -413,26 +423,13 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
         // infinities and NaN last
         uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                               __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-        auto largest = [](uint32_t m) { return kv::unpack2<T>(max(m & 0xffffu, m >> 16)).x; };
-        float top = 0.f;  // 4 bits: of the block of 16, two threads'
-        if (CODE == kKv4) {
-          m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          top = largest(m);
-        }
-        for (unsigned d = vec_row >> 1; d > (CODE == kKv4); d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float big = largest(m);
+        for (unsigned d = vec_row >> 1; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float2 m2 = kv::unpack2<T>(max(m & 0xffffu, m >> 16));
+        const float big = m2.x;
         const bool finite = big < INFINITY;  // (not for NaN either)
-        if (ok && CODE == kKv8) {
+        if (ok) {
           *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.pool[w]) + at) = finite ? codes8<T>(x, big) : make_uint2(0, 0);
           if (piece == 0) static_cast<float*>(a.scale[w])[((page * a.kv_heads + head) << a.page_log2) + pos] = __fdiv_rn(big, 127.f);
-        }
-        if (ok && CODE == kKv4) {
-          uint8_t* const record = kv4_record(a.scale[w], page * a.kv_heads + head, a.page_log2, a.head_dim);
-          uint32_t code = 0, scale = 0;
-          if (finite) code = codes4<T>(x, big, top, scale);
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.pool[w]) + (at >> 1)) = code;
-          if (!(piece & 1)) record[(4 << a.page_log2) + pos * (a.head_dim >> 4) + (piece >> 1)] = (uint8_t)scale;
-          if (piece == 0) reinterpret_cast<float*>(record)[pos] = __fdiv_rn(big, 2688.f);
         }
       }
     }
@@ -440,11 +437,70 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const KvAppendAr
   if (bad) atomicOr(a.err, bad);
 }
 
+// Rows in 4 bits: a block of 16 values per thread, the key's and the value's loads in flight together. Bound by HBM and, nearly, by
+// issue: every value is scaled, rounded and converted.
+template <typename T>
+__global__ void __launch_bounds__(kAppThreads) kv_append4_kernel(const KvAppendArgs a) {
+  const unsigned row_blocks = a.head_dim >> 4, tok_blocks = a.kv_heads * row_blocks;  // blocks per row: 2, 4 or 8, within one warp
+  const int log2_row = 31 - __clz(row_blocks);
+  const int64_t n_slots = a.n_pages << a.page_log2;
+  int bad = 0;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t t0 = 0; t0 < a.n_tok; t0 += 1 << 18) {
+    const unsigned total = (unsigned)min(a.n_tok - t0, (int64_t)1 << 18) * tok_blocks;
+    for (unsigned base = blockIdx.x * kAppThreads; base < total; base += gridDim.x * kAppThreads) {
+      const unsigned i = base + threadIdx.x;
+      const bool in = i < total;
+      const unsigned at_tok = in ? i / tok_blocks : 0, c = in ? i - at_tok * tok_blocks : 0;
+      const unsigned head = c >> log2_row, piece = c & (row_blocks - 1);
+      const int64_t tok = t0 + at_tok, slot = in ? a.slots[tok] : -1;
+      const bool ok = slot >= 0 && slot < n_slots;
+      if (slot >= n_slots) bad |= kKvErrSlot;
+      const int64_t page = slot >> a.page_log2;
+      const int pos = (int)slot & ((1 << a.page_log2) - 1);
+      uint4 row[2][2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          row[w][h] = ok && a.src[w] ? *(reinterpret_cast<const uint4*>(static_cast<const T*>(a.src[w]) + tok * a.src_stride[w]) + 2 * c + h)
+                                     : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!a.src[w]) continue;
+        // the block's and the row's largest magnitude on the bits, in pairs
+        uint32_t m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = row[w][h];
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+        auto largest = [](uint32_t m) { return kv::unpack2<T>(max(m & 0xffffu, m >> 16)).x; };
+        const float top = largest(m);
+        for (unsigned d = row_blocks >> 1; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float big = largest(m);
+        if (!ok) continue;
+        uint32_t scale = 0;
+        uint2 code = make_uint2(0, 0);
+        if (big < INFINITY) code = codes4<T>(row[w], big, top, scale);  // (not for NaN either)
+        const int64_t at = page * a.stride[w][0] + head * a.stride[w][1] + pos * a.stride[w][2] + piece * 16;
+        uint8_t* const record = kv4_record(a.scale[w], page * a.kv_heads + head, a.page_log2, a.head_dim);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.pool[w]) + (at >> 1)) = code;
+        record[(4 << a.page_log2) + pos * row_blocks + piece] = (uint8_t)scale;
+        if (piece == 0) reinterpret_cast<float*>(record)[pos] = __fdiv_rn(big, 2688.f);
+      }
+    }
+  }
+  if (bad) atomicOr(a.err, bad);
+}
+
 // ------------------------------------------------------------------------------------------
-// Read: append's threads the other way round.
+// Read: 8 values per thread, which writes 16 bytes, as in append. Bound by HBM.
 template <typename T, int CODE>
 __global__ void __launch_bounds__(kAppThreads) kv_read_kernel(const KvReadArgs a) {
   const unsigned vec_row = a.head_dim >> 3, vec_tok = a.kv_heads * vec_row;
+  const int log2_row = 31 - __clz(vec_row);
   const int64_t n_slots = a.n_pages << a.page_log2;
   int bad = 0;
   pdl_trigger();
@@ -453,42 +509,54 @@ __global__ void __launch_bounds__(kAppThreads) kv_read_kernel(const KvReadArgs a
     const unsigned total = (unsigned)min(a.n_tok - t0, (int64_t)1 << 18) * vec_tok;
     for (unsigned i = blockIdx.x * kAppThreads + threadIdx.x; i < total; i += gridDim.x * kAppThreads) {
       const unsigned at_tok = i / vec_tok, c = i - at_tok * vec_tok;
-      const unsigned head = c / vec_row, piece = c - head * vec_row;
+      const unsigned head = c >> log2_row, piece = c & (vec_row - 1);
       const int64_t tok = t0 + at_tok, slot = a.slots[tok];
       if (slot >= n_slots) bad |= kKvErrSlot;
       if (slot < 0 || slot >= n_slots) continue;
-      const int64_t page = slot >> a.page_log2, pos = slot & ((1 << a.page_log2) - 1);
+      const int64_t page = slot >> a.page_log2, page_head = page * a.kv_heads + head;
+      const int pos = (int)slot & ((1 << a.page_log2) - 1);
+      // (the loads of both rows first)
+      uint4 x16[2];
+      uint2 x[2];
+      float s[2];
+      uint32_t b[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!a.dst[w]) continue;
         const int64_t at = page * a.stride[w][0] + head * a.stride[w][1] + pos * a.stride[w][2] + piece * 8;
-        uint4 x;
-        if (CODE == kKv16) x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.pool[w]) + at);
+        if (CODE == kKv16) x16[w] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.pool[w]) + at);
         if (CODE == kKv8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.pool[w]) + at);
-          const float s = static_cast<const float*>(a.scale[w])[((page * a.kv_heads + head) << a.page_log2) + pos];
-          const uint32_t b[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
-          auto two = [&](uint32_t y) {
-            const float2 f = kv::unpack2<__half>(y);
-            return kv::pack2<T>(f.x * s, f.y * s);
-          };
-          x = make_uint4(two(kv::i8_pair<0x4140>(b[0])), two(kv::i8_pair<0x4342>(b[0])), two(kv::i8_pair<0x4140>(b[1])),
-                         two(kv::i8_pair<0x4342>(b[1])));
+          x[w] = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.pool[w]) + at);
+          s[w] = static_cast<const float*>(a.scale[w])[(page_head << a.page_log2) + pos];
         }
         if (CODE == kKv4) {
-          const uint8_t* const record = kv4_record(a.scale[w], page * a.kv_heads + head, a.page_log2, a.head_dim);
-          const uint32_t q = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.pool[w]) + (at >> 1));
-          const float s = reinterpret_cast<const float*>(record)[pos];
-          const uint32_t b = record[(4 << a.page_log2) + pos * (a.head_dim >> 4) + (piece >> 1)];
-          const uint32_t b2 = kv::e4m3_f16x2(b | b << 8);
-          auto two = [&](uint32_t y) {  // (code times block scale is exact in fp16)
-            const float2 f = kv::unpack2<__half>(kv::mul2<__half>(y, b2));
-            return kv::pack2<T>(f.x * s, f.y * s);
-          };
-          x = make_uint4(two(kv::e2m1_f16x2<0>(q)), two(kv::e2m1_f16x2<1>(q)), two(kv::e2m1_f16x2<2>(q)),
-                         two(kv::e2m1_f16x2<3>(q)));
+          const uint8_t* const record = kv4_record(a.scale[w], page_head, a.page_log2, a.head_dim);
+          x[w].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.pool[w]) + (at >> 1));
+          s[w] = reinterpret_cast<const float*>(record)[pos];
+          b[w] = record[(4 << a.page_log2) + pos * (vec_row >> 1) + (piece >> 1)];
         }
-        *(reinterpret_cast<uint4*>(static_cast<T*>(a.dst[w]) + tok * a.dst_stride[w]) + c) = x;
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!a.dst[w]) continue;
+        uint4* const dst = reinterpret_cast<uint4*>(static_cast<T*>(a.dst[w]) + tok * a.dst_stride[w]) + c;
+        auto two = [&](uint32_t y) {
+          const float2 f = kv::unpack2<__half>(y);
+          return kv::pack2<T>(f.x * s[w], f.y * s[w]);
+        };
+        if (CODE == kKv16) *dst = x16[w];
+        if (CODE == kKv8) {
+          const uint32_t q0 = x[w].x ^ 0x80808080u, q1 = x[w].y ^ 0x80808080u;
+          *dst = make_uint4(two(kv::i8_pair<0x4140>(q0)), two(kv::i8_pair<0x4342>(q0)), two(kv::i8_pair<0x4140>(q1)), two(kv::i8_pair<0x4342>(q1)));
+        }
+        if (CODE == kKv4) {
+          const uint32_t b2 = kv::e4m3_f16x2(b[w] | b[w] << 8);  // (code times block scale is exact in fp16)
+          auto four = [&](uint32_t q) {
+            return make_uint4(two(kv::mul2<__half>(kv::e2m1_f16x2<0>(q), b2)), two(kv::mul2<__half>(kv::e2m1_f16x2<1>(q), b2)),
+                              two(kv::mul2<__half>(kv::e2m1_f16x2<2>(q), b2)), two(kv::mul2<__half>(kv::e2m1_f16x2<3>(q), b2)));
+          };
+          *dst = four(x[w].x);
+        }
       }
     }
   }
@@ -508,13 +576,13 @@ cudaError_t launch_kv_tables(const KvTablesArgs& a, int num_sms, cudaStream_t s)
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, int code, int num_sms, cudaStream_t s) {
-  const int64_t total = a.n_tok * a.kv_heads * (a.head_dim / 8);
+  const int64_t total = a.n_tok * a.kv_heads * (a.head_dim / (code == kKv4 ? 16 : 8));
   const int64_t want = (total + kAppThreads - 1) / kAppThreads, most = (int64_t)num_sms * 8;
   const dim3 grid((unsigned)(want < most ? want : most));
   auto run = [&](auto kern) { return launch_kernel(kern, grid, dim3(kAppThreads), 0, s, true, a); };
   auto of = [&](auto t) {
     typedef decltype(t) T;
-    return code == kKv16 ? run(kv_append_kernel<T, kKv16>) : code == kKv8 ? run(kv_append_kernel<T, kKv8>) : run(kv_append_kernel<T, kKv4>);
+    return code == kKv16 ? run(kv_append_kernel<T, false>) : code == kKv8 ? run(kv_append_kernel<T, true>) : run(kv_append4_kernel<T>);
   };
   return dtype == CVR_DTYPE_BF16 ? of(__nv_bfloat16()) : of(__half());
 }
