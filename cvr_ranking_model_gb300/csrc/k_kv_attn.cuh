@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kHalves = kRow / kLine;
   static constexpr int kHeadTiles = MODE == 0 ? 1 : 2;          // 4 bits: tiles of 8 query heads per warp
   static constexpr int kCtasPerSm = F4 && MODE == 0 ? (D == 128 ? 3 : 4) : D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
-  static constexpr int kUnitMost = F4 ? (D == 128 ? (MODE == 3 ? 4096 : 8192) : D == 64 && MODE == 0 ? 4096 : 8192)
+  static constexpr int kUnitMost = F4 ? (D == 128 ? (MODE == 3 ? 4096 : 8192) : D == 64 ? 4096 : 2048)
                                       : kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;

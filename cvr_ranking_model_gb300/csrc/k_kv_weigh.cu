@@ -164,34 +164,42 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
             more_ids = entries(e0 + 32);
           }
           uint8_t* const slot = my_ring + (b % R::kStages) * R::kStage;
-          const int e = (j0 >> a.page_log2) - e0, p0 = __shfl_sync(0xffffffffu, ids, e);
-          const int p1 = a.page_log2 == 3 ? __shfl_sync(0xffffffffu, ids, e + 1) : p0;
-          float* at[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t page = u ? p1 : p0;
-            const int pos = (j0 + 8 * u) & page_mask;  // (of the block's token 8 u)
-            const bool seen = j0 + gid + 8 * u < len, there = seen && page < (uint32_t)a.n_pages;
-            bad |= seen && !there ? kKvErrPage : 0;
-            const uint32_t from = there ? page : 0;  // (rows that are not there are zeros, and nothing is read)
-            const char* p = k_head + from * a.k_stride[0] + pos * a.k_stride[2];
+          const int e = (j0 >> a.page_log2) - e0, pos = j0 & page_mask;
+          const uint32_t p0 = __shfl_sync(0xffffffffu, ids, e);
+          const bool small = a.page_log2 == 3;  // (8 tokens a page: the block has two)
+          const uint32_t p1 = small ? __shfl_sync(0xffffffffu, ids, e + 1) : p0;
+          // (tokens behind the history, and those of a page that is none of the pool's, are zeros, and nothing is read)
+          const bool ok0 = p0 < (uint32_t)a.n_pages, ok1 = p1 < (uint32_t)a.n_pages;
+          const bool there0 = j0 + gid < len && ok0, there1 = j0 + gid + 8 < len && ok1;
+          if (!ok0 || !ok1) bad |= (j0 < len && !ok0) || (j0 + 8 < len && !ok1) ? kKvErrPage : 0;
+          const uint32_t from0 = ok0 ? p0 : 0, from1 = ok1 ? p1 : 0;
+          auto bring = [&](int u, const char* p, const uint8_t* record, const uint8_t* blocks, bool there) {
 #pragma unroll
             for (int c = 0; c < R::kWords / R::kLoad; ++c)
               copy<R::kLoad * 4>(slot + (u * R::kWords / R::kLoad + c) * (R::kLoad * 128) + lane * (R::kLoad * 4), p + c * 64, there);
-            if (SCALED) {
-              const uint8_t* const record = scale_head + (uint64_t)from * (H * record_bytes) + pos * 4;
-              copy<4>(slot + R::oScale + u * 128 + lane * 4, record, there);
-              if (CODE == kKv4) {
-                const uint8_t* const blocks = record + blocks_at + pos * (D / 16 - 4);
-                copy<4>(slot + R::oScale + (2 + u) * 128 + lane * 4, D == 32 ? (const uint8_t*)((uintptr_t)blocks & ~(uintptr_t)3) : blocks, there);
-              }
-            }
-            at[u] = there ? weight_head + (uint64_t)from * page_places + pos : nullptr;
+            if (SCALED) copy<4>(slot + R::oScale + u * 128 + lane * 4, record, there);
+            if (CODE == kKv4)
+              copy<4>(slot + R::oScale + (2 + u) * 128 + lane * 4, D == 32 ? (const uint8_t*)((uintptr_t)blocks & ~(uintptr_t)3) : blocks, there);
+          };
+          const char* p = k_head + from0 * a.k_stride[0] + pos * a.k_stride[2];
+          const uint8_t* record = scale_head + (SCALED ? (uint64_t)from0 * (H * record_bytes) + pos * 4 : 0);
+          const uint8_t* blocks = record + blocks_at + pos * (D / 16 - 4);
+          bring(0, p, record, blocks, there0);
+          if (small) {
+            p = k_head + from1 * a.k_stride[0];
+            record = scale_head + (SCALED ? (uint64_t)from1 * (H * record_bytes) : 0);
+            blocks = record + blocks_at;
+          } else {
+            p += 8 * a.k_stride[2];
+            record += 32;
+            blocks += D / 2;
           }
-          float* const weight = tig > 1 ? nullptr : tig ? at[1] : at[0];
-          *reinterpret_cast<float**>(slot + R::oWeight + lane * 8) = weight;
-          const bool is_old = weight && j0 + gid + 8 * (tig & 1) < old_end;
-          copy<4>(slot + R::oOld + lane * 4, is_old ? weight : a.weight, is_old);
+          bring(1, p, record, blocks, there1);
+          // threads 0 and 1 of a row's four keep the weights of tokens gid and gid + 8
+          const bool there = tig == 0 ? there0 : tig == 1 && there1;
+          float* const at = weight_head + (uint64_t)(tig ? from1 : from0) * page_places + (small ? 0 : pos + 8 * (tig & 1));
+          *reinterpret_cast<float**>(slot + R::oWeight + lane * 8) = there ? at : nullptr;
+          copy<4>(slot + R::oOld + lane * 4, at, there && j0 + gid + 8 * (tig & 1) < old_end);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
