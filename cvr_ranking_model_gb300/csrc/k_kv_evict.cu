@@ -271,16 +271,18 @@ __global__ void __launch_bounds__(THREADS, Shape<THREADS>::kCtasPerSm) evict_ker
           });
         }
         meet(C);
-        // thread t has the bins from kBins - 1 - kPerThread t down: sums from the top
-        uint32_t count[kPerThread], sum = 0;
+        // The cluster's CTAs have a slice of the bins each, from the top, and a thread some of its CTA's: sums over the CTAs, and
+        // from the top down to the bin in which the wanted number lies.
+        const int slice = kBins / C, per = slice > kThreads ? slice / kThreads : 1;  // (per: at most kPerThread)
+        uint32_t count[kPerThread] = {}, sum = 0;
+        const int top = kBins - 1 - (int)rank * slice - tid * per;
+        if (tid * per < slice) {
+          for (uint32_t c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-          const uint32_t* const bin = &s.hist[kBins - 1 - tid * kPerThread - i];
-          count[i] = 0;
-          if (C == 1) count[i] = *bin;
-          else
-            for (uint32_t c = 0; c < C; ++c) count[i] += peer_load(bin, c);
-          sum += count[i];
+            for (int i = 0; i < kPerThread; ++i)
+              if (i < per) count[i] += C == 1 ? s.hist[top - i] : peer_load(&s.hist[top - i], c);
+#pragma unroll
+          for (int i = 0; i < kPerThread; ++i) sum += count[i];
         }
         uint32_t incl = sum;
 #pragma unroll
@@ -290,22 +292,39 @@ __global__ void __launch_bounds__(THREADS, Shape<THREADS>::kCtasPerSm) evict_ker
         }
         if (lane == 31) s.w_above[warp] = incl;
         __syncthreads();
-        uint32_t over = incl - sum;
+        uint32_t over = incl - sum, all = 0, owner = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) over += w < warp ? s.w_above[w] : 0;
+        for (int w = 0; w < kWarps; ++w) {
+          over += w < warp ? s.w_above[w] : 0;
+          all += s.w_above[w];
+        }
+        if (C > 1) {
+          if (tid == 0) s.above = all;
+          meet(C);
+          uint32_t before = 0;
+          for (uint32_t c = 0; c < C; ++c) {  // slices before this one, and the one that has the wanted number
+            const uint32_t x = peer_load(&s.above, c);
+            if (c < rank) over += x;
+            if (before < want && want <= before + x) owner = c;
+            before += x;
+          }
+        }
         if (over < want && want <= over + sum) {
-          int bin = kBins - 1 - tid * kPerThread;
 #pragma unroll
           for (int i = 0; i < kPerThread; ++i) {
-            if (over < want && want <= over + count[i]) {
-              s.found = bin;
+            if (i < per && over < want && want <= over + count[i]) {
+              s.found = top - i;
               s.rest = want - over;
             }
             over += count[i];
-            --bin;
           }
         }
         meet(C);  // (also: all have read the histograms)
+        if (C > 1) {
+          threshold |= peer_load(&s.found, owner) << shift;
+          want = peer_load(&s.rest, owner);
+          continue;
+        }
         threshold |= s.found << shift;
         want = s.rest;
       }
