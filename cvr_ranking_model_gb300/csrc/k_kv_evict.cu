@@ -539,11 +539,16 @@ cudaError_t launch(const KvEvictArgs& a, int ctas, cudaStream_t s) {
 
 template <int CODE>
 cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
-  // as many CTAs per (request, head) as the SMs hold, of 1024 tokens at least
+  // As many CTAs per (request, head) as the SMs hold, of 1024 tokens at least: a large one per SM for long histories, two small ones for
+  // others. A cluster pays for its meetings: 4 requests of 20000 tokens, 8 heads, 51 us in 4 large CTAs each, 67 us in 8 small ones; 512
+  // (request, head)s in clusters of two 153 us instead of 104.
   const int64_t pairs = (int64_t)a.n_req * a.kv_heads, most = (int64_t)a.max_pages << a.page_log2;
+  const bool large = most >= 16384 && pairs <= num_sms;
+  // (clusters of 8 have to find 8 free SMs of one group: 16 of them on 128 SMs run in two waves)
+  const auto fit = [&](int n) { return large ? (n == 8 ? num_sms * 2 / 3 : num_sms) : 2 * num_sms; };
   int ctas = 1;
-  while (ctas < kMaxCluster && pairs * ctas * 2 <= num_sms * 2 && most / (ctas * 2) >= 1024) ctas *= 2;
-  return pairs * ctas <= num_sms && most >= 16384 ? launch<CODE, 1024>(a, ctas, s) : launch<CODE, 256>(a, ctas, s);
+  while (ctas < kMaxCluster && pairs * ctas * 2 <= fit(ctas * 2) && most / (ctas * 2) >= 1024) ctas *= 2;
+  return large ? launch<CODE, 1024>(a, ctas, s) : launch<CODE, 256>(a, ctas, s);
 }
 
 }  // namespace
