@@ -49,27 +49,27 @@ struct __align__(16) Part {
 };
 constexpr int kGroup = 16;  // parts that are joined at once
 
-// MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64
+// MODE: query rows per kv head 0: at most 8, 1: 16, 2: 32, 3: 64; 4 bits also 4: at most 4
 template <int CODE, int D, int MODE>
 struct Shape {
-  static constexpr bool I8 = CODE == kKv8, F4 = CODE == kKv4;
+  static constexpr bool I8 = CODE == kKv8, F4 = CODE == kKv4, R8 = MODE == 0 || MODE == 4;
   static constexpr int MT = MODE == 3 ? 4 : MODE == 2 ? 2 : 1;  // 16-row tiles of query heads
   static constexpr int KP = kConsumers / MT;                    // consumer warps that share a row tile's tokens
   static constexpr int kRow = kv_row_bytes(CODE, D);            // bytes of a row
   static constexpr int kLine = kRow < 128 ? kRow : 128;         // bytes of a swizzled line
   static constexpr int kHalves = kRow / kLine;
-  static constexpr int kHeadTiles = MODE == 0 ? 1 : 2;          // 4 bits: tiles of 8 query heads per warp
-  static constexpr int kCtasPerSm = F4 && MODE == 0 ? (D == 128 ? 3 : 4) : D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
+  static constexpr int kHeadTiles = R8 ? 1 : 2, kPerLane = MODE == 4 ? 1 : 2;  // 4 bits: tiles of 8 columns of query heads per warp, heads of a tile per lane
+  static constexpr int kCtasPerSm = F4 && R8 ? (D == 128 ? 3 : 4) : D == 32 ? (MT == 1 ? 4 : 3) : D == 64 ? (MT == 1 && (I8 || F4) ? 3 : 2) : 2;
   static constexpr int kUnitMost = F4 ? (D == 128 ? (MODE == 3 ? 4096 : 8192) : D == 64 ? 4096 : 2048)
                                       : kCtasPerSm == 2 && (MT == 1 || D < 128) ? 16384 : 8192;
   static constexpr int TK = kUnitMost / kRow < 256 ? kUnitMost / kRow : 256;  // tokens per tile
   static constexpr int kUnit = TK * kRow;
   static constexpr int kQRow = D * 2 + 16;                      // padded: conflict-free fragment loads
-  static constexpr int kQBytes = (MODE == 0 ? 8 : MT * 16) * kQRow;
+  static constexpr int kQBytes = (R8 ? 8 : MT * 16) * kQRow;
   static constexpr int kORow = D + (F4 ? 4 : I8 ? 16 : 8);      // padded fp32 rows of the joining area
-  static constexpr int kORows = MODE == 0 ? 8 : 16;             // a warp's rows in the joining area
+  static constexpr int kORows = R8 ? 8 : 16;             // a warp's rows in the joining area
   static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
-  static constexpr int kOAreas = D == 32 && MODE == 0 ? 2 : 1;           // (two spare a barrier per use, where they fit)
+  static constexpr int kOAreas = D == 32 && R8 ? 2 : 1;           // (two spare a barrier per use, where they fit)
   static constexpr int kScaleBytes = TK * kv_scale_bytes(CODE, D);  // the row scales, then the block scales
   static constexpr int kPartCost = MT == 1 ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
   typedef Shape<CODE, D, MODE> S;
   constexpr bool I8 = S::I8, F4 = S::F4;
   constexpr int MT = S::MT, KP = S::KP, TK = S::TK, NB = S::NB, NBS = S::NBS, RING = S::kRing;
-  constexpr bool R8 = MODE == 0;
+  constexpr bool R8 = S::R8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* const full = reinterpret_cast<uint64_t*>(sm + S::oBar);
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
 
   for (bool last = !some; !last;) {
     // ---- a part: the tiles of one (request, head) in this CTA's run ----
-    Heads4<T, F4 ? D : 32, S::kHeadTiles> heads4;  // 4 bits: all that follows here is in it
+    Heads4<T, F4 ? D : 32, S::kHeadTiles, S::kPerLane> heads4;  // 4 bits: all that follows here is in it
     uint32_t qf[D / 16][4];
     float o[D / 8][4], ls[4] = {0.f, 0.f, 0.f, 0.f};  // ls: sums of the weights by products
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
@@ -1135,13 +1135,15 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
 // The instance for a configuration: its kernel, shared memory, CTAs per SM and tile.
 template <int D, int CODE>
 KvAttendKernel instance(int dtype, int group) {
-  const int mode = group <= 8 ? 0 : group <= 16 ? 1 : group <= 32 ? 2 : 3;
+  const int mode = CODE == kKv4 && group <= 4 ? 4 : group <= 8 ? 0 : group <= 16 ? 1 : group <= 32 ? 2 : 3;
   auto of = [&](auto t, auto m) {
     typedef decltype(t) T;
     typedef Shape<CODE, D, decltype(m)::value> S;
     return KvAttendKernel{reinterpret_cast<const void*>(&attend_kernel<T, CODE, D, decltype(m)::value>), S::kSmem, S::kCtasPerSm, S::TK};
   };
   auto by_mode = [&](auto t) {
+    if constexpr (CODE == kKv4)
+      if (mode == 4) return of(t, std::integral_constant<int, 4>());
     if (mode == 0) return of(t, std::integral_constant<int, 0>());
     if (mode == 1) return of(t, std::integral_constant<int, 1>());
     if (mode == 2) return of(t, std::integral_constant<int, 2>());

@@ -37,15 +37,17 @@ __device__ __forceinline__ uint32_t mul_half(uint32_t x, uint32_t y) {
 }
 
 // What a consumer warp holds of 8 NT heads. Lane (gid, tig): of K^T's and V^T's fragments tokens or values gid and gid + 8, of results
-// heads 2 tig and 2 tig + 1 of each 8.
-template <typename T, int D, int NT>
+// heads 2 tig and 2 tig + 1 of each 8. PER_LANE = 1: of at most 4 heads, which take every other column: softmax is per column and lane,
+// used or not, and half of the columns are then left out.
+template <typename T, int D, int NT, int PER_LANE>
 struct Heads4 {
   static constexpr int kPieces = D / 32;  // 32 values: 16 bytes of a row
   static constexpr float kGrow = 6.f;     // weights are at most 2^kGrow
   static constexpr int kQBytes = NT * D / 16 * 256;  // a warp's query fragments in shared memory: [k-step][tile][lane], 8 bytes each
   uint2* qf;                                          // this lane's
-  float o[NT][kPieces][2][4];  // values 32 g + 4 gid + (0, 1 | 2, 3) of heads (2 tig, 2 tig + 1)
-  float m[NT][2], l[NT][2], c[NT][2], mul[NT][2];
+  float o[NT][kPieces][2][4];  // values 32 g + 4 gid + (0, 1 | 2, 3) of columns (2 tig, 2 tig + 1)
+  static constexpr int N = PER_LANE;
+  float m[NT][N], l[NT][N], c[NT][N], mul[NT][N];
   uint32_t range;  // a V scale's bits plus this are at most 11 << 23 where it lies in [hi / 2^11, hi]
 
   // Query rows `q` (row_bytes apart, `rows` of them there) of up to 16 heads; scale: of the logits.
@@ -55,7 +57,7 @@ struct Heads4 {
     const float sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int head = t * 8 + gid;
+      const int head = N == 2 ? t * 8 + gid : gid & 1 ? rows : gid >> 1;  // (of column gid)
       uint4 x[kPieces];
       uint32_t big = 0;
 #pragma unroll
@@ -83,7 +85,7 @@ struct Heads4 {
       }
       const float f = scale == 0.f ? 1.f : fmaxf(fabsf(scale) * __uint_as_float(e << 23) * kLog2e, 1.4e-45f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         c[t][i] = __shfl_sync(0xffffffffu, f, tig * 8 + i * 4);
         m[t][i] = -INFINITY;
         l[t][i] = mul[t][i] = 0.f;
@@ -105,7 +107,7 @@ struct Heads4 {
                                        Wait wait_v) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     constexpr int kRec = kv_scale_bytes(kKv4, D);
-    asm volatile("" : "+r"(log2_box));  // (offsets are computed where they are used: held over the loop of tiles they would spill)
+    if (D == 128) asm volatile("" : "+r"(log2_box));  // (offsets are computed where they are used: held over the loop of tiles they would spill)
     // offsets of token j's row scale and block scales, and from token gid's to token gid + 8's
     auto row_at = [&](int j) { return (j >> log2_box) * (kRec << log2_box) + (j & ((1 << log2_box) - 1)) * 4; };
     auto blocks_at = [&](int j) { return (j >> log2_box) * (kRec << log2_box) + (4 << log2_box) + (j & ((1 << log2_box) - 1)) * (D / 16); };
@@ -173,9 +175,11 @@ struct Heads4 {
     }
     if (!wait_v()) return false;
     // ---- row scales, tokens that are not seen, the heads' largest logits ----
-    float sv[NBS][2], top[NT][2];
+    float sv[NBS][2], top[NT][N];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < N; ++i) top[t][i] = -INFINITY;
 #pragma unroll
     for (int b = 0; b < NBS; ++b)
 #pragma unroll
@@ -189,7 +193,7 @@ struct Heads4 {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < N; ++i) {
             float& x = s[b][t][2 * u + i];
             x = seen ? x * sk : -INFINITY;
             top[t][i] = fmaxf(top[t][i], x);
@@ -201,7 +205,7 @@ struct Heads4 {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         top[t][i] = logit(top[t][i], c[t][i]);
         grows = grows || top[t][i] > m[t][i] + kGrow;
       }
@@ -213,11 +217,11 @@ struct Heads4 {
     auto is_outside = [&](uint32_t x) { return x + range > 11u << 23 && x != 0u; };
     if (__any_sync(0xffffffffu, grows || is_outside(size()))) rescale<NBS>(s, sv, top, size, is_outside);
     // ---- O^T += V^T P^T ----
-    float base[NT][2];  // (a base of -infinity is left out of the exponent: nothing was seen yet, or every logit is -infinity)
+    float base[NT][N];  // (a base of -infinity is left out of the exponent: nothing was seen yet, or every logit is -infinity)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) base[t][i] = m[t][i] == -INFINITY ? 0.f : m[t][i];
+      for (int i = 0; i < N; ++i) base[t][i] = m[t][i] == -INFINITY ? 0.f : m[t][i];
 #pragma unroll
     for (int b = 0; b < NBS; ++b) {
       if (MASK && !any[b]) continue;
@@ -226,9 +230,9 @@ struct Heads4 {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float w[2];
+          float w[2] = {0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < N; ++i) {
             const float p = ex2(logit(s[b][t][2 * u + i], c[t][i]) - base[t][i]);
             l[t][i] += p;
             w[i] = p * (sv[b][u] * mul[t][i]);
@@ -236,7 +240,7 @@ struct Heads4 {
           const uint32_t h = pack2<__half>(w[0], w[1]);
           const float2 f = unpack2<__half>(h);
           hi[t][u] = transposed(h);
-          lo[t][u] = transposed(pack2<__half>(w[0] - f.x, w[1] - f.y));
+          lo[t][u] = transposed(pack2<__half>(w[0] - f.x, N == 2 ? w[1] - f.y : 0.f));
         }
       // block scales of tokens 2 tig, 2 tig + 1 and of those 8 further; unseen tokens' cleared (they may be no numbers)
       uint32_t vs[2][4], keep[2] = {0xffffffffu, 0xffffffffu};
@@ -303,7 +307,7 @@ struct Heads4 {
 
   // A logit passed its base by more than kGrow, or a V scale lies outside: bases and powers of two follow.
   template <int NBS, typename Size, typename Outside>
-  __device__ __forceinline__ void rescale(const float (&s)[NBS][NT][4], const float (&sv)[NBS][2], float (&top)[NT][2], Size size, Outside is_outside) {
+  __device__ __forceinline__ void rescale(const float (&s)[NBS][NT][4], const float (&sv)[NBS][2], float (&top)[NT][N], Size size, Outside is_outside) {
     auto exponent = [](float x) { return (int)(__float_as_uint(x) >> 23 & 255u); };
     auto power = [](int e) { return __uint_as_float((uint32_t)e << 23); };
     const uint32_t my_size = size();
@@ -311,7 +315,9 @@ struct Heads4 {
     if (mul[0][0] == 0.f) {
       const float first = power(262 - min(max(largest + 4, 12), 254));
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mul[t][0] = mul[t][1] = first;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < N; ++i) mul[t][i] = first;
       range = __float_as_uint(first) - (251u << 23);
     }
     const bool far = __any_sync(0xffffffffu, is_outside(my_size));
@@ -319,7 +325,7 @@ struct Heads4 {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         float n = top[t][i];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
@@ -354,17 +360,17 @@ struct Heads4 {
       }
   }
 
-  // The sums to shared memory: rows of head t * 8 + 2 tig + i (those below `rows`), `stride` floats apart, and their m and l.
+  // The sums to shared memory: rows of the heads (those below `rows`), `stride` floats apart, and their m and l.
   __device__ __forceinline__ void store(float* dst, float* dst_m, float* dst_l, int stride, int rows) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         float sum = l[t][i];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const int head = t * 8 + 2 * tig + i;
+        const int head = N == 2 ? t * 8 + 2 * tig + i : tig;
         if (head >= rows) continue;
         const float back = __uint_as_float(254u - (__float_as_uint(mul[t][i]) >> 23) << 23);  // 1 / mul
 #pragma unroll

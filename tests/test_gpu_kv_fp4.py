@@ -41,7 +41,7 @@ def check(c, q_heads, window=0, scale=None, **kw):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("dim", [32, 64, 128])
-@pytest.mark.parametrize("heads,group", [(4, 1), (2, 4), (1, 12), (1, 17), (1, 64)])
+@pytest.mark.parametrize("heads,group", [(4, 1), (2, 4), (3, 3), (2, 7), (1, 8), (1, 12), (1, 17), (1, 64)])
 def test_types_dims_and_heads(dtype, dim, heads, group):
     check(Cache4(EDGES, heads, dim, 16, dtype, seed=dim + group), heads * group)
 
@@ -91,7 +91,7 @@ def test_queries_at_the_ends_of_bf16(log2_q, log2_k, scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("group", [2, 12, 24, 40])
+@pytest.mark.parametrize("group", [2, 6, 12, 24, 40])
 @pytest.mark.parametrize("dim", [32, 64, 128])
 @pytest.mark.parametrize("at", [[0], [150, 299]])
 def test_a_large_value_without_weight_leaves_the_others_their_bits(dtype, group, dim, at):
