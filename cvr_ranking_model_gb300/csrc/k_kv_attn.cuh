@@ -138,6 +138,9 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag, err);
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
 
   if (tid == 0) {
     for (int i = 0; i < RING; ++i) {
-      mbar_init(full + i, 1);
+      mbar_init(full + i, F4 ? 33 : 1);  // (the thread that announces the copies; 4 bits: the producer's threads, whose own copies count too)
       mbar_init(empty + i, kConsumers);
     }
     for (int i = 0; i < 2; ++i) {
@@ -361,9 +364,19 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
       ids0 = n_ids;
       more0 = entries(r, first_entry(len) + 32);
       bool ok = true;
-      constexpr int kTokBytes = S::kRow + kv_scale_bytes(CODE, D);
+      constexpr int kTokBytes = S::kRow + (F4 ? 0 : kv_scale_bytes(CODE, D));  // (what bulk copies bring)
       const uint32_t box_bytes = br * kTokBytes, tile_bytes = TK * kTokBytes;
       const bool long_pages = a.page_log2 > log2_br;  // several tiles per page, one box per tile
+      // 4 bits: a tile's scales, 16 bytes per thread and copy: of which box, and how far into it (of long pages the row scales, then the
+      // block scales, in 16 bytes). A bulk copy per box would cost the warp a loop over the threads that issue one.
+      constexpr int kRec = kv_scale_bytes(CODE, D), kScaleCopies = (TK * kRec / 16 + 31) / 32;
+      int scale_box[F4 ? kScaleCopies : 1], scale_at[F4 ? kScaleCopies : 1];
+#pragma unroll
+      for (int c = 0; c < (F4 ? kScaleCopies : 0); ++c) {
+        const int x = c * 32 + lane, per_box = kRec << log2_br >> 4;
+        scale_box[c] = x < TK * kRec / 16 ? x / per_box : 32;
+        scale_at[c] = x - scale_box[c] * per_box;
+      }
       while (ok) {
         // ---- a part: its query rows and description, and its tiles ----
         const int first = P * H + h * w_t + lead;  // the (request, head)'s first tile's place
@@ -425,17 +438,20 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
                 bulk_load(smem_u32(sm + S::oScale + slot * S::kScaleBytes + (lane << log2_br) * 4),
                           static_cast<const float*>(w ? a.v_scale : a.k_scale) + ((((int64_t)page * H + h) << a.page_log2) + row),
                           4 << log2_br, full + slot);
-              if (F4) {
-                const uint8_t* const record = kv4_record(w ? a.v_scale : a.k_scale, (int64_t)page * H + h, a.page_log2, D);
-                constexpr int kRec = kv_scale_bytes(CODE, D);
-                const uint32_t to = smem_u32(sm + S::oScale + slot * S::kScaleBytes) + lane * (kRec << log2_br);
-                if (!long_pages) {
-                  bulk_load(to, record, kRec << log2_br, full + slot);
-                } else {
-                  bulk_load(to, record + row * 4, 4 << log2_br, full + slot);
-                  bulk_load(to + (4 << log2_br), record + (4 << a.page_log2) + row * (D / 16), (D / 16) << log2_br, full + slot);
-                }
+            }
+            if constexpr (F4) {
+              const uint32_t to = smem_u32(sm + S::oScale + slot * S::kScaleBytes) + lane * 16;
+#pragma unroll
+              for (int c = 0; c < kScaleCopies; ++c) {
+                const int of = __shfl_sync(0xffffffffu, page, scale_box[c] & 31);
+                if (scale_box[c] >= 32 || !(want >> scale_box[c] & 1)) continue;
+                const uint8_t* from = kv4_record(w ? a.v_scale : a.k_scale, (int64_t)of * H + h, a.page_log2, D);
+                if (!long_pages) from += scale_at[c] * 16;
+                else if (scale_at[c] < TK / 4) from += row * 4 + scale_at[c] * 16;
+                else from += (4 << a.page_log2) + row * (D / 16) + (scale_at[c] - TK / 4) * 16;
+                cp_async16(to + c * 512, from);
               }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot)) : "memory");
             }
             filled = min(filled + 1, RING);
             if (++slot == RING) {
@@ -472,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
       }
     }
     // the copies in flight land before the CTA's shared memory can go, also when a consumer's wait gave up
+    if (F4) asm volatile("cp.async.wait_all;" ::: "memory");
     for (int u = 0; u < filled; ++u) {
       if (--slot < 0) {
         slot = RING - 1;
