@@ -70,7 +70,7 @@ struct Shape {
   static constexpr int kORows = R8 ? 8 : 16;             // a warp's rows in the joining area
   static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
   static constexpr int kOAreas = D == 32 && R8 ? 2 : 1;           // (two spare a barrier per use, where they fit)
-  static constexpr int kScaleBytes = TK * kv_scale_bytes(CODE, D);  // the row scales, then the block scales
+  static constexpr int kScaleBytes = TK * kv_scale_bytes(CODE, D);  // (4 bits: of each box the row scales, then the block scales)
   static constexpr int kPartCost = MT == 1 ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, Shape<CODE, D, MODE>::kCtasPerSm)
     }
 
     // ---- the part's end: the warps' (m, l, o) to shared memory, and summed ----
-    if (F4) {
+    if (F4) {  // (store, below)
     } else if (!kOnesSum) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {

@@ -310,9 +310,9 @@ struct Heads4 {
   __device__ __forceinline__ void rescale(const float (&s)[NBS][NT][4], const float (&sv)[NBS][2], float (&top)[NT][N], Size size, Outside is_outside) {
     auto exponent = [](float x) { return (int)(__float_as_uint(x) >> 23 & 255u); };
     auto power = [](int e) { return __uint_as_float((uint32_t)e << 23); };
-    const uint32_t my_size = size();
-    const int largest = (int)(__reduce_max_sync(0xffffffffu, my_size) >> 23);
-    if (mul[0][0] == 0.f) {
+    const uint32_t my_size = size(), most = __reduce_max_sync(0xffffffffu, my_size);
+    const int largest = (int)(most >> 23);
+    if (mul[0][0] == 0.f && most != 0u) {  // (scales of zero set none: their tokens add nothing)
       const float first = power(262 - min(max(largest + 4, 12), 254));
 #pragma unroll
       for (int t = 0; t < NT; ++t)

@@ -112,6 +112,7 @@ __device__ __forceinline__ Request request_of(const KvEvictArgs& a, int r, int* 
     const int h = a.held[r];
     q.held = min(max(h, 0), a.max_pages);
     if (q.held != h || q.held < need) *bad |= kKvErrLens;
+    q.len = min(q.len, q.held << a.page_log2);  // (no entry behind the pages held is used)
   }
   q.cut = q.len > a.limit;
   return q;

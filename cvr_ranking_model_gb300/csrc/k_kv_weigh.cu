@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
           const float2 u = unpack2<T>(x[ks].x), v = unpack2<T>(x[ks].y);
           big = fmaxf(fmaxf(big, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
         }
-        lse = in ? a.lse[((int64_t)r * H + h) * G + head] : INFINITY;  // (heads that there are none of weigh nothing)
+        lse = in ? a.lse[((int64_t)r * H + h) * G + head] : 0.f;
         float up = sign;
         factor = fabsf(a.scale);
         if (std::is_same<T, __nv_bfloat16>::value) {
@@ -327,10 +327,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
         const float sA = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + lane * 4) : 1.f;
         const float sB = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + 128 + lane * 4) : 1.f;
         float sumA = 0.f, sumB = 0.f;
-        auto add = [&](const float* s, float c0, float c1, float l0, float l1) {
-          auto weight = [&](float s, float scale, float c, float l) { return ex2(fmaf(SCALED ? s * scale : s, c, -l) * kLog2e); };
-          sumA += weight(s[0], sA, c0, l0) + weight(s[1], sA, c1, l1);
-          sumB += weight(s[2], sB, c0, l0) + weight(s[3], sB, c1, l1);
+        auto add = [&](const float* s, int tile, float c0, float c1, float l0, float l1) {
+          // (a head that there is none of weighs nothing, also where its 0 times an infinity of a row is no number)
+          const bool in0 = tile * 8 + 2 * tig < G, in1 = tile * 8 + 2 * tig + 1 < G;
+          auto weight = [&](float s, float scale, float c, float l, bool in) {
+            const float p = ex2(fmaf(SCALED ? s * scale : s, c, -l) * kLog2e);
+            return in ? p : 0.f;
+          };
+          sumA += weight(s[0], sA, c0, l0, in0) + weight(s[1], sA, c1, l1, in1);
+          sumB += weight(s[2], sB, c0, l0, in0) + weight(s[3], sB, c1, l1, in1);
         };
         if (TILES == 0) {
           uint32_t k[KS][4];
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
               mma16816<M>(s, k[ks], q.x, q.y);
             }
             const float2 c = *reinterpret_cast<const float2*>(my_c + tile * 8 + 2 * tig), l = *reinterpret_cast<const float2*>(my_l + tile * 8 + 2 * tig);
-            add(s, c.x, c.y, l.x, l.y);
+            add(s, tile, c.x, c.y, l.x, l.y);
           }
         } else {
           float s[kHeld][4];
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
             }
           }
 #pragma unroll
-          for (int tile = 0; tile < kHeld; ++tile) add(s[tile], c0[tile], c1[tile], l0[tile], l1[tile]);
+          for (int tile = 0; tile < kHeld; ++tile) add(s[tile], tile, c0[tile], c1[tile], l0[tile], l1[tile]);
         }
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {

@@ -428,7 +428,8 @@ cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_strid
  * scales and their weights move within the request's own pages.
  *   lens     [n_req] int32 tokens of each request
  *   limit, keep, first, last   1 <= keep <= limit <= 2^30, 0 <= first, 0 <= last, first + last <= keep (CVR_E_SHAPE)
- *   held     [n_req] int32 leading entries of the request's table row that hold pages; NULL: ceil(lens / page_size)
+ *   held     [n_req] int32 leading entries of the request's table row that hold pages, enough for its tokens; NULL:
+ *            ceil(lens / page_size)
  *   table    [n_req][max_pages] int32, read only: entries behind a request's pages are ignored here and elsewhere
  *   weight   fp32 [n_pages][kv_heads][page_size] as cvr_kv_weigh leaves it, in place
  *   kept     [n_req][kv_heads][keep] int32: which token became token i; rows of requests that were not cut are not written
@@ -440,7 +441,7 @@ cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_strid
  *   free_head, free_head_out   int32, with free_pages: *free_head less the pages given back
  * Requests must have pages of their own (none in two of them). An array that the call writes must not overlap any other of its
  * arrays (CVR_E_ARG). Not for handles without pools or with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length,
- * held count (a request's pages among them) or list head out of range (used clamped), CVR_E_PAGES when the list has no room in
+ * held count or list head out of range (used clamped) or more tokens than the pages held have places (the others are left out), CVR_E_PAGES when the list has no room in
  * front of its head (the first pages are not given back), CVR_E_ID_RANGE for a page id outside the pool (rows of page 0 were
  * read, none written). */
 cvr_status cvr_kv_evict(cvr_kv* h, int32_t n_req, const int32_t* lens, int32_t limit, int32_t keep, int32_t first,

@@ -176,8 +176,11 @@ def test_errors_on_the_device():
     assert kv.sync(check=False) == 6 and o["lens"].tolist() == [112, 0]
     c = Cache4([100, 90], 1, 64, 8, "bf16", seed=2)
     kv = c.handle(1)
-    o = evict(c, kv, 40, 20, held=[5, 12])
-    assert kv.sync(check=False) == 6 and o["pages"].tolist() == [3, 3] and int(o["out"]) == 40 - 2 - 9
+    o = evict(c, kv, 30, 20, held=[5, 12])
+    assert kv.sync(check=False) == 6 and o["pages"].tolist() == [3, 3] and int(o["out"]) == 40 - 2 - 9 and o["lens"].tolist() == [20, 20]
+    assert int(o["kept"][0].max()) < 40  # (of the tokens that the held pages have places for)
+    o = evict(c, kv, 60, 20, held=[5, -1])
+    assert kv.sync(check=False) == 6 and o["pages"].tolist() == [5, 0] and int(o["out"]) == 40 and o["lens"].tolist() == [40, 0]
     # a page outside the pool: reported, nothing out of the pools touched
     c = Cache4([100, 90], 1, 64, 8, "bf16", cache="same", seed=2)
     c.table[0, 1] = c.n_pages

@@ -142,6 +142,18 @@ def test_a_large_value_without_weight_leaves_the_others_their_bits(dtype, group,
     assert_within(out, ref, bound, "out")
 
 
+@pytest.mark.parametrize("group", [1, 6, 12, 40])
+@pytest.mark.parametrize("zeros", [slice(0, 200), slice(100, 300), slice(0, 300), slice(37, 38)])
+def test_rows_of_zeros(zeros, group):
+    """Histories that begin with, end with or are zero rows, as a padded prompt leaves them: scales, block scales and codes 0."""
+    import torch
+    c = Cache4([300, 5], 2, 64, 16, "bf16", seed=group)
+    j = torch.arange(300, device="cuda")[zeros]
+    for p in (c.k, c.v):
+        p.put((c.table[0].long()[j // 16], slice(None), j % 16), torch.zeros((j.numel(), 2, 64), dtype=torch.uint8, device="cuda"), 0, 0.0)
+    check(c, 2 * group)
+
+
 def test_a_row_with_an_infinity_reads_as_no_number():
     import torch
     c = Cache4([40, 40], 1, 64, 8, "bf16", seed=3)

@@ -129,6 +129,21 @@ def test_weights_of_the_attention_add_up_to_one_per_head():
             assert bool(((total - 4).abs() < 4e-5).all()), (form, r, total)
 
 
+@pytest.mark.parametrize("group", [1, 3, 12, 20])
+def test_keys_with_infinities(group):
+    """A logit of -infinity weighs nothing, one of infinity infinitely much, whatever heads the products' tiles are filled up with."""
+    import torch
+    c = Cache4([40], 1, 64, 8, "bf16", cache="same", seed=1)
+    q = torch.ones((1, group, 64), dtype=torch.bfloat16, device="cuda")
+    c.k[int(c.table[0, 1]), 0, 3, 7], c.k[int(c.table[0, 2]), 0, 3, 7] = -math.inf, math.inf
+    lse, weight = torch.zeros((1, group), device="cuda"), torch.zeros((c.n_pages, 1, 8), device="cuda")
+    kv = c.handle(group)
+    kv.weigh(1, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.01, lse.data_ptr(), weight.data_ptr(), decay=0.0)
+    kv.sync()
+    got = weight[c.table[0, :5].long(), 0].flatten()
+    assert float(got[11]) == 0 and float(got[19]) == math.inf and bool(torch.isfinite(torch.cat([got[:19], got[20:]])).all())
+
+
 def test_the_same_bits_on_every_call():
     import torch
     c = Cache4([5000, 3, 777], 2, 128, 16, "bf16", cache="fp4", seed=9)
