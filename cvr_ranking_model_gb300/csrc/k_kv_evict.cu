@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(THREADS, Shape<THREADS>::kCtasPerSm) evict_ker
       bad |= ok ? 0 : kKvErrPage;  // (without a branch: loads of several tokens are in flight together)
       return ok ? p : 0;
     };
-    auto key_of = [&](int j) { return order_of(__ldcg(a.weight + ((((int64_t)page_of(j) * a.kv_heads + h) << a.page_log2) + (j & page_mask)))); };
+    auto weight_of = [&](int j) { return a.weight + ((((int64_t)page_of(j) * a.kv_heads + h) << a.page_log2) + (j & page_mask)); };
+    auto key_of = [&](int j) { return order_of(__ldcg(weight_of(j))); };
 
     // ---- 1. the b-th largest weight of the tokens [first, n - last) ----
     const int m = n - a.first - a.last, b = a.keep - a.first - a.last;  // (b < m)
@@ -259,10 +260,13 @@ __global__ void __launch_bounds__(THREADS, Shape<THREADS>::kCtasPerSm) evict_ker
         for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
         __syncthreads();
         if (pass == 0 && held) {
-          // (the weights come from memory: as many in flight as registers allow)
+          // (all of a thread's weights are on their way together)
 #pragma unroll 16
+          for (int j = c0 + tid; j < c1; j += kThreads) async_in<4>(&s.keys[j - c0], weight_of(j));
+          asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 8
           for (int j = c0 + tid; j < c1; j += kThreads) {
-            const uint32_t k = key_of(j);
+            const uint32_t k = order_of(__uint_as_float(s.keys[j - c0]));
             s.keys[j - c0] = k;
             atomicAdd(&s.hist[k >> 21], 1u);
           }
