@@ -71,7 +71,7 @@ struct Shape {
   static constexpr int kOBytes = kConsumers * kORows * (kORow + 2) * 4;  // with the rows' m and l
   static constexpr int kOAreas = D == 32 && R8 ? 2 : 1;           // (two spare a barrier per use, where they fit)
   static constexpr int kScaleBytes = TK * kv_scale_bytes(CODE, D);  // (4 bits: of each box the row scales, then the block scales)
-  static constexpr int kPartCost = MT == 1 ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
+  static constexpr int kPartCost = MT == 1 && !(F4 && MODE == 1) ? 1 : 2;  // what a part costs beside its tiles, in tiles (see attend_kernel's runs)
   // blocks of 16 tokens that a warp takes per tile, and per softmax step
   static constexpr int NB = TK / 16 / KP, NBS = NB < 2 ? NB : 2;
   // ring units: what is left of this CTA's share of the SM's 228 KB (1 KB of it reserved, 1 KB for the ring's alignment)
