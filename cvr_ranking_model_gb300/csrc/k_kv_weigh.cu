@@ -33,12 +33,11 @@ struct Rows {
   static __device__ __forceinline__ int dim(int ks, int tig) { return ks * 4 / kRun * 4 * kRun + tig * kRun + ks * 4 % kRun; }
 };
 
-// BYTES copied to shared memory asynchronously, or as many zeros
+// BYTES copied to shared memory asynchronously
 template <int BYTES>
-__device__ __forceinline__ void copy(void* dst, const void* src, bool there) {
-  const int n = there ? BYTES : 0;
-  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(n) : "memory");
+__device__ __forceinline__ void copy(void* dst, const void* src) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 
 __device__ __forceinline__ int64_t scan_before(int64_t x, int64_t* sums, int64_t* all) {
@@ -168,38 +167,43 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
           const uint32_t p0 = __shfl_sync(0xffffffffu, ids, e);
           const bool small = a.page_log2 == 3;  // (8 tokens a page: the block has two)
           const uint32_t p1 = small ? __shfl_sync(0xffffffffu, ids, e + 1) : p0;
-          // (tokens behind the history, and those of a page that is none of the pool's, are zeros, and nothing is read)
           const bool ok0 = p0 < (uint32_t)a.n_pages, ok1 = p1 < (uint32_t)a.n_pages;
-          const bool there0 = j0 + gid < len && ok0, there1 = j0 + gid + 8 < len && ok1;
-          if (!ok0 || !ok1) bad |= (j0 < len && !ok0) || (j0 + 8 < len && !ok1) ? kKvErrPage : 0;
           const uint32_t from0 = ok0 ? p0 : 0, from1 = ok1 ? p1 : 0;
-          auto bring = [&](int u, const char* p, const uint8_t* record, const uint8_t* blocks, bool there) {
-#pragma unroll
-            for (int c = 0; c < R::kWords / R::kLoad; ++c)
-              copy<R::kLoad * 4>(slot + (u * R::kWords / R::kLoad + c) * (R::kLoad * 128) + lane * (R::kLoad * 4), p + c * 64, there);
-            if (SCALED) copy<4>(slot + R::oScale + u * 128 + lane * 4, record, there);
-            if (CODE == kKv4)
-              copy<4>(slot + R::oScale + (2 + u) * 128 + lane * 4, D == 32 ? (const uint8_t*)((uintptr_t)blocks & ~(uintptr_t)3) : blocks, there);
-          };
-          const char* p = k_head + from0 * a.k_stride[0] + pos * a.k_stride[2];
-          const uint8_t* record = scale_head + (SCALED ? (uint64_t)from0 * (H * record_bytes) + pos * 4 : 0);
-          const uint8_t* blocks = record + blocks_at + pos * (D / 16 - 4);
-          bring(0, p, record, blocks, there0);
-          if (small) {
-            p = k_head + from1 * a.k_stride[0];
-            record = scale_head + (SCALED ? (uint64_t)from1 * (H * record_bytes) : 0);
-            blocks = record + blocks_at;
-          } else {
-            p += 8 * a.k_stride[2];
-            record += 32;
-            blocks += D / 2;
-          }
-          bring(1, p, record, blocks, there1);
+          const char* const row0 = k_head + from0 * a.k_stride[0] + pos * a.k_stride[2];
+          const char* const row1 = small ? k_head + from1 * a.k_stride[0] : row0 + 8 * a.k_stride[2];
+          const uint8_t* const record0 = scale_head + (SCALED ? (uint64_t)from0 * (H * record_bytes) + pos * 4 : 0);
+          const uint8_t* const record1 = small ? scale_head + (SCALED ? (uint64_t)from1 * (H * record_bytes) : 0) : record0 + 32;
+          const uint8_t* const blocks0 = record0 + blocks_at + pos * (D / 16 - 4);
+          const uint8_t* const blocks1 = small ? record1 + blocks_at : blocks0 + D / 2;
           // threads 0 and 1 of a row's four keep the weights of tokens gid and gid + 8
-          const bool there = tig == 0 ? there0 : tig == 1 && there1;
           float* const at = weight_head + (uint64_t)(tig ? from1 : from0) * page_places + (small ? 0 : pos + 8 * (tig & 1));
-          *reinterpret_cast<float**>(slot + R::oWeight + lane * 8) = there ? at : nullptr;
-          copy<4>(slot + R::oOld + lane * 4, at, there && j0 + gid + 8 * (tig & 1) < old_end);
+          auto bring = [&](auto all) {
+            // (of tokens behind the history, and of a page that is none of the pool's, nothing is read: the products' rows do not mix, and
+            // theirs go nowhere)
+            constexpr bool ALL = decltype(all)::value;
+            const bool there0 = ALL || (j0 + gid < len && ok0), there1 = ALL || (j0 + gid + 8 < len && ok1);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (!(u ? there1 : there0)) continue;
+#pragma unroll
+              for (int c = 0; c < R::kWords / R::kLoad; ++c)
+                copy<R::kLoad * 4>(slot + (u * R::kWords / R::kLoad + c) * (R::kLoad * 128) + lane * (R::kLoad * 4), (u ? row1 : row0) + c * 64);
+              if (SCALED) copy<4>(slot + R::oScale + u * 128 + lane * 4, u ? record1 : record0);
+              if (CODE == kKv4) {
+                const uint8_t* const blocks = u ? blocks1 : blocks0;
+                copy<4>(slot + R::oScale + (2 + u) * 128 + lane * 4, D == 32 ? (const uint8_t*)((uintptr_t)blocks & ~(uintptr_t)3) : blocks);
+              }
+            }
+            const bool there = tig == 0 ? there0 : tig == 1 && there1;
+            *reinterpret_cast<float**>(slot + R::oWeight + lane * 8) = there ? at : nullptr;
+            if (there && j0 + gid + 8 * (tig & 1) < old_end) copy<4>(slot + R::oOld + lane * 4, at);
+          };
+          if (j0 + 16 <= len && ok0 && ok1) {
+            bring(std::true_type());
+          } else {
+            bad |= (j0 < len && !ok0) || (j0 + 8 < len && !ok1) ? kKvErrPage : 0;
+            bring(std::false_type());
+          }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
         }
         float* const weight = *reinterpret_cast<float* const*>(slot + R::oWeight + lane * 8);
         if (weight) {
-          // (the old weight of a token that has none, or of no decay, was not read: 0)
+          // (the old weight of a token that has none, or of no decay, was not read)
           const float sum = tig & 1 ? sumB : sumA, old = *reinterpret_cast<const float*>(slot + R::oOld + lane * 4);
           *weight = row0 + 8 * (tig & 1) < old_end ? fmaf(a.decay, old, sum) : sum;
         }
