@@ -10,6 +10,12 @@
 //   - S^T leaves the tensor cores with a token's heads side by side; as P^T it has to enter with a head's tokens side by side: movmatrix
 //     transposes the packed weights.
 //   - Weights, times V's row scale and a power of two, enter as two fp16 halves, as on 8-bit pools (there: the rule for that power).
+//
+// Measured (one GB300, copy rate 6.78 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128: 70.8 us, 45% of the copy rate (pages
+// of 16; 65.7 us with pages of 32 and more, whose rows take fewer copies), against 112.6 us on bf16 rows; one request of 131071: 48.5 us,
+// 48%. Bound by issue: 26 to 28 warp instructions per token and kv head; the schedulers issue half of the time and the ALU pipe (conversions, masks, regrouping) is 48% busy. With the heads on M (112.3 and 61.4 us) the sums
+// took twice the registers and two CTAs shared an SM. 512 histories of up to 2000 events, 4 heads of 32, K = V: 46.4 us, 35.1 us on bf16
+// rows: rows of 32 are mostly softmax, and 4 bits add conversions. One request of 200: 6.0 us, latency.
 #pragma once
 
 #include "cvr_kv_rows.cuh"
