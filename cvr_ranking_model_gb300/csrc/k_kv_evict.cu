@@ -15,10 +15,9 @@
 // Pages behind the places go back to the free list, in blocks of requests of their own: what they need, the lengths, is known.
 //
 // Measured (one GB300, copy rate 6.78 TB/s): 64 requests of up to 8191 tokens cut to 1023 each, 8 heads of 128, bf16: 96.8 us. Cut to 8
-// tokens it takes 29 (mostly selection: latency of dependent loads, three passes over shared memory); the other 68 move 410 MB, at 89% of the
-// copy rate. Rows by
-// bulk copies, two in and two out per token: 181 us, some 20 ns each per SM. Rounds of register-held rows whose lookups waited for one
-// another: 187 us. One request of 131071 cut to 32768: 153 us in 8 clusters of 8 CTAs of 1024 threads, 457 us in CTAs of 256.
+// tokens each they take 29 us (mostly selection: latency of dependent loads, three passes over shared memory); the other 68 move 410 MB,
+// at 89% of the copy rate. Rows by bulk copies, two in and two out per token: 181 us, some 20 ns each per SM. Rounds of register-held
+// rows whose lookups waited for one another: 187 us. One request of 131071 cut to 32768: 153 us in 8 clusters of 8 CTAs of 1024 threads, 457 us in CTAs of 256.
 #include <cstddef>
 
 #include "../../include/cvr.h"

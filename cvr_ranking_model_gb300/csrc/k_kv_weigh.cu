@@ -29,7 +29,7 @@ struct Rows {
   static constexpr int kWords = kv_row_bytes(CODE, D) / 16;             // 32-bit words of a row per thread (4 threads a row)
   static constexpr int kLoad = kWords < 4 ? kWords : 4;                 // words of one load
   static constexpr int kRun = kLoad * 4 * D / kv_row_bytes(CODE, D);    // values of one load
-// a warp's ring of blocks in shared memory: per block and thread its words of rows gid and gid + 8, the rows' scales and block
+  // a warp's ring of blocks in shared memory: per block and thread its words of rows gid and gid + 8, the rows' scales and block
   // scales, the old weight and where the new one goes
   static constexpr int kStages = kWords >= 16 ? 2 : kWords == 8 ? 3 : 4, kScaled = CODE == kKv16 ? 0 : CODE == kKv8 ? 2 : 4;
   static constexpr int oScale = kWords * 2 * 128, oOld = oScale + kScaled * 128, oWeight = oOld + 128, kStage = oWeight + 256;
