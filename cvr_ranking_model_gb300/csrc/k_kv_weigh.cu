@@ -405,9 +405,12 @@ cudaError_t launch(const KvWeighArgs& a, int num_sms, cudaStream_t s) {
   const int64_t blocks = (((int64_t)a.max_pages << a.page_log2) + 15) / 16 * a.n_req * a.kv_heads;  // at most
   const int64_t want = (blocks + kWarps - 1) / kWarps, fit = (int64_t)num_sms * ctas_per_sm(D, tiles > 2 ? 0 : tiles);
   const dim3 grid((unsigned)(want < fit ? want : fit)), block(kThreads);
-  const int smem = kWarps * (Rows<CODE, D>::kWarpBytes + (tiles > 2 ? tiles * (D / 16 * 64 + 16) * 4 : 0));
+  // (a kernel's limit of shared memory is the process's: always what its largest launch asks for, or a handle of fewer heads would lower
+  // it between another thread's setting and launch)
+  const auto smem_of = [](int tiles) { return kWarps * (Rows<CODE, D>::kWarpBytes + (tiles > 2 ? tiles * (D / 16 * 64 + 16) * 4 : 0)); };
+  const int smem = smem_of(tiles), most = smem_of(tiles > 2 ? 64 / 8 : tiles);
   auto run = [&](auto kern) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return e != cudaSuccess ? e : launch_kernel(kern, grid, block, smem, s, true, a);
   };
   return tiles == 1 ? run(weigh_kernel<T, CODE, D, 1>) : tiles == 2 ? run(weigh_kernel<T, CODE, D, 2>) : run(weigh_kernel<T, CODE, D, 0>);

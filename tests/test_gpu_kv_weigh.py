@@ -212,3 +212,41 @@ def test_refusals():
     with pytest.raises(cvr.CvrError) as e:
         windowed.evict(1, lens, 4, 2, table, w, lse, q)
     assert e.value.status == 1
+
+
+def test_two_threads_with_handles_of_their_own():
+    """Handles of different numbers of query heads, whose launches of one kernel ask for different amounts of shared memory, each on a stream
+    and in a thread of its own: every call is taken, and the weights are those of a call alone."""
+    import threading
+    import torch
+    import cvr_ranking_model_gb300 as cvr
+    c = Cache4([40, 7], 1, 128, 16, "bf16", cache="same", seed=2)
+    jobs = []
+    for group in (24, 64):
+        q = torch.randn((2, group, 128), generator=c.gen, device="cuda").to(torch.bfloat16)
+        lse, stream = exact_lse(c, q, 0.1), torch.cuda.Stream()
+        alone, got = (torch.zeros((c.n_pages, 1, 16), device="cuda") for _ in range(2))
+        kv = c.handle(group)
+        kv.weigh(2, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.1, lse.data_ptr(), alone.data_ptr(), decay=0.0)
+        kv.sync()
+        jobs.append((c.handle(group, stream=stream.cuda_stream), q, lse, alone, got, stream))
+    torch.cuda.synchronize()
+    refused, start = [], threading.Barrier(2)
+
+    def work(kv, q, lse, alone, got, stream):
+        start.wait()
+        for _ in range(20000):
+            try:
+                kv.weigh(2, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 0.1, lse.data_ptr(), got.data_ptr(), decay=0.0)
+            except cvr.CvrError as e:
+                refused.append(str(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for kv, _, _, alone, got, _ in jobs:
+        kv.sync()
+        assert torch.equal(got, alone)
+    assert not refused, (len(refused), refused[0])
