@@ -45,6 +45,13 @@ __device__ __forceinline__ void copy(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 
+// the smaller, NaN if either is
+__device__ __forceinline__ float min_or_nan(float x, float y) {
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
 __device__ __forceinline__ int64_t scan_before(int64_t x, int64_t* sums, int64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = x;
@@ -335,16 +342,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, TILES)) weigh_kernel(
         };
         const float sA = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + lane * 4) : 1.f;
         const float sB = SCALED ? *reinterpret_cast<const float*>(slot + R::oScale + 128 + lane * 4) : 1.f;
-        float sumA = 0.f, sumB = 0.f;
+        // A finite logit above lse is so by the rounding of both and counts as lse: of logits about 2^24 that rounding is a factor of e, and a
+        // weight that it made infinite would never fade. (A row of an infinity gives no head a finite product, so one head's shows it.)
+        float sumA = 0.f, sumB = 0.f, mostA = 0.f, mostB = 0.f;
         auto add = [&](const float* s, int tile, float c0, float c1, float l0, float l1) {
           // (a head that there is none of weighs nothing, also where its 0 times an infinity of a row is no number)
           const bool in0 = tile * 8 + 2 * tig < G, in1 = tile * 8 + 2 * tig + 1 < G;
-          auto weight = [&](float s, float scale, float c, float l, bool in) {
-            const float p = ex2(fmaf(SCALED ? s * scale : s, c, -l) * kLog2e);
+          const float x[4] = {SCALED ? s[0] * sA : s[0], SCALED ? s[1] * sA : s[1], SCALED ? s[2] * sB : s[2], SCALED ? s[3] * sB : s[3]};
+          if (tile == 0) {
+            mostA = fabsf(x[0]) < INFINITY ? 0.f : INFINITY;
+            mostB = fabsf(x[2]) < INFINITY ? 0.f : INFINITY;
+          }
+          auto weight = [&](float x, float most, float c, float l, bool in) {
+            const float p = ex2(min_or_nan(fmaf(x, c, -l) * kLog2e, most));
             return in ? p : 0.f;
           };
-          sumA += weight(s[0], sA, c0, l0, in0) + weight(s[1], sA, c1, l1, in1);
-          sumB += weight(s[2], sB, c0, l0, in0) + weight(s[3], sB, c1, l1, in1);
+          sumA += weight(x[0], mostA, c0, l0, in0) + weight(x[1], mostA, c1, l1, in1);
+          sumB += weight(x[2], mostB, c0, l0, in0) + weight(x[3], mostB, c1, l1, in1);
         };
         if (TILES == 0) {
           uint32_t k[KS][4];

@@ -410,12 +410,14 @@ cvr_status cvr_kv_read(cvr_kv* h, int64_t n_tok, const int64_t* slots, void* k, 
  *   weight[slot of j][h] = decay weight[slot of j][h] + sum_i exp(scale q[r][i] . k_j - lse[r][i])
  * over the query heads i of kv head h, for every token j < lens[r]: what cvr_kv_evict ranks tokens by.
  *   q, q_stride, lens, table, scale   as in cvr_kv_attend, whose products of queries and keys these are
- *   lse       fp32 [n_req][q_heads], as cvr_kv_attend of the same queries wrote it
+ *   lse       fp32 [n_req][q_heads], as cvr_kv_attend of the same queries wrote it: a finite logit above it counts as lse, whose
+ *             exponential is 1
  *   new_lens  [n_req] int32 how many of a request's tokens, the last ones, have no weight yet: theirs starts from 0 whatever their
  *             place held before. NULL: one of each request that is not empty
  *   decay     finite, >= 0; 1 adds up over a token's whole life, less forgets; 0 reads no old weight
  *   weight    fp32 [n_pages][kv_heads][page_size], in place; places of other tokens are left as they are
- * Sums are fp32, in one order on every call. A page must not be in two of the call's requests. weight must not overlap the
+ * Sums are fp32, in one order on every call. Logits and lse are rounded to fp32, which moves a term by percents at logits of 2^20, by a
+ * factor of e at 2^24. A page must not be in two of the call's requests. weight must not overlap the
  * other arrays. Not for handles with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length or new length out
  * of range (used clamped), CVR_E_ID_RANGE for a page id outside the pool (its tokens are left out). */
 cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,

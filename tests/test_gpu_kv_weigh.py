@@ -250,3 +250,25 @@ def test_two_threads_with_handles_of_their_own():
         kv.sync()
         assert torch.equal(got, alone)
     assert not refused, (len(refused), refused[0])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [3, 12, 20])
+@pytest.mark.parametrize("log2", [10, 20, 24, 31, 60])
+def test_large_logits_weigh_at_most_one_per_head(log2, group, dtype, form):
+    """Logits about 2^log2 and their lse are off by 2^-23 of themselves and more, and a weight by e to the power of that. With lse from the
+    attention of the same queries no query head gives a token more than 1 for it (exp2 itself is off by at most 2^-21)."""
+    import torch
+    c = Cache4([1, 700, 33], 2, 64, 16, dtype, cache=form, seed=group)
+    q = torch.randn((3, 2 * group, 64), generator=c.gen, device="cuda").to(torch_type(dtype))
+    out, lse, weight = torch.zeros_like(q), torch.zeros((3, 2 * group), device="cuda"), torch.full((c.n_pages, 2, 16), math.nan, device="cuda")
+    kv = c.handle(2 * group)
+    kv.attend(3, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 2.0 ** (log2 - 3), out.data_ptr(), lse.data_ptr())
+    kv.weigh(3, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), 2.0 ** (log2 - 3), lse.data_ptr(), weight.data_ptr(), decay=0.0)
+    kv.sync()
+    assert bool(torch.isfinite(lse).all())
+    for r, n in enumerate(c.lens_list):
+        j = torch.arange(n, device="cuda")
+        w = weight[c.table[r].long()[j // 16], :, j % 16]
+        assert bool((w >= 0).all()) and float(w.max()) <= group * (1 + 2.0 ** -21), (r, float(w.max()))
