@@ -127,20 +127,60 @@ __device__ __forceinline__ int stays(const KvEvictArgs& a, const Request& q) {
   return q.cut && a.free_pages ? min(q.held, (a.keep + (1 << a.page_log2) - 1) >> a.page_log2) : q.held;
 }
 
-// Lengths, page counts and the free list of requests [r0, r0 + kReleased), by one CTA.
+// entries that a request's tokens take
+__device__ __forceinline__ int entries_of(const KvEvictArgs& a, const Request& q) { return (q.len + (1 << a.page_log2) - 1) >> a.page_log2; }
+
+// Lengths, page counts and the free list of requests [r0, r0 + kReleased), by one CTA. An id outside the pool among a cut request's tokens'
+// is not given back, so where the pages of these requests go depends on the ids of all: every CTA looks at them.
 template <int THREADS>
 __device__ void release(const KvEvictArgs& a, Shared<THREADS>& s, int r0) {
   constexpr int kThreads = THREADS, kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bad = 0, ignored = 0;
   int64_t before = 0, all = 0;  // pages given back by the requests before r0, and by all
-  if (a.free_pages)
-    for (int r = tid; r < a.n_req; r += kThreads) {
-      const Request q = request_of(a, r, &ignored);
-      const int n = q.held - stays(a, q);
-      all += n;
-      if (r < r0) before += n;
+  bool gaps = false;            // ids outside the pool among those of these requests
+  // (32 requests, one per lane, are one warp's, or where there are few requests several warps')
+  const int share = max(kWarps / max((a.n_req + 31) / 32, 1), 1), part = warp % share;
+  for (int r = warp / share * 32; r < (a.free_pages ? a.n_req : 0); r += kWarps / share * 32) {
+    Request q = {0, 0, false};
+    if (r + lane < a.n_req) q = request_of(a, r + lane, &ignored);
+    const int left = stays(a, q), n = part == 0 ? q.held - left : 0;
+    all += n;
+    if (r + lane < r0) before += n;
+    // the requests' entries behind those that stay, evenly over the lanes
+    const uint32_t look = max(entries_of(a, q) - left, 0);  // (at most 2^27 - 1)
+    uint32_t incl = look;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += u;
     }
+    const uint32_t start = incl - look, total = __shfl_sync(0xffffffffu, incl, 31);
+    constexpr int U = 8;  // (loads in flight together)
+    for (int64_t x0 = part * (U * 32); x0 < total; x0 += share * (U * 32)) {
+      int of[U], page[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t x = (uint32_t)min(x0 + u * 32 + lane, (int64_t)total - 1);
+        int k = 0;
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1) {
+          const uint32_t to = __shfl_sync(0xffffffffu, start, k + step);
+          if (to <= x) k += step;
+        }
+        of[u] = r + k;
+        page[u] = a.table[(int64_t)(r + k) * a.max_pages + (__shfl_sync(0xffffffffu, left, k) + (int)(x - __shfl_sync(0xffffffffu, start, k)))];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (x0 + u * 32 + lane < total && (unsigned)page[u] >= (unsigned)a.n_pages) {
+          --all;
+          if (of[u] < r0) --before;
+          else if (of[u] < r0 + kReleased) gaps = true;
+        }
+    }
+  }
+  if (gaps) bad |= kKvErrPage;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, d);
@@ -155,7 +195,7 @@ __device__ void release(const KvEvictArgs& a, Shared<THREADS>& s, int r0) {
     a.lens_out[r] = q.cut ? a.keep : q.len;
     if (a.pages) a.pages[r] = left;
   }
-  int64_t wide = n;  // (512 requests of at most 2^27 pages may pass 32 bits)
+  int64_t wide = n;  // (kReleased requests of at most 2^27 pages may pass 32 bits)
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, wide, d);
@@ -166,7 +206,7 @@ __device__ void release(const KvEvictArgs& a, Shared<THREADS>& s, int r0) {
     s.sum2[warp] = before;
     s.sum3[warp] = all;
   }
-  __syncthreads();
+  gaps = __syncthreads_or(gaps);
   before = all = 0;
   int64_t ahead = wide - n, items = 0;
 #pragma unroll
@@ -184,19 +224,39 @@ __device__ void release(const KvEvictArgs& a, Shared<THREADS>& s, int r0) {
       *a.free_head_out = (int)max((int64_t)head - all, (int64_t)0);
       if (all > head) bad |= kKvErrPages;
     }
-    // entry x of these requests' pages goes to position head - all + before + x
     if (tid < kReleased) s.start[tid] = (uint32_t)min(ahead, (int64_t)0xffffffff);
     if (tid == 0) s.start[kReleased] = (uint32_t)min(items, (int64_t)0xffffffff);
     __syncthreads();
-    const int64_t at0 = (int64_t)head - all + before;
-    const int64_t skip = at0 < 0 ? -at0 : 0;  // (no room in front of the list)
+    const int64_t at0 = (int64_t)head - all + before;  // where these requests' pages begin (below 0: no room in front of the list)
     const uint32_t end = s.start[kReleased];
-    for (int64_t x = skip + tid; x < end; x += kThreads) {
+    auto page_of = [&](int64_t x, bool* ok) {  // entry x of these requests' pages, and whether it is given back
       int k = 0;
       for (int step = kReleased / 2; step > 0; step >>= 1)
         if (s.start[k + step] <= x) k += step;
       const Request o = request_of(a, r0 + k, &ignored);
-      a.free_pages[at0 + x] = a.table[(int64_t)(r0 + k) * a.max_pages + stays(a, o) + (int)(x - s.start[k])];
+      const int entry = stays(a, o) + (int)(x - s.start[k]), page = a.table[(int64_t)(r0 + k) * a.max_pages + entry];
+      *ok = (unsigned)page < (unsigned)a.n_pages || entry >= entries_of(a, o);
+      return page;
+    };
+    bool ok = false;
+    if (!gaps) {
+      for (int64_t x = (at0 < 0 ? -at0 : 0) + tid; x < min((int64_t)end, a.n_free - at0); x += kThreads) a.free_pages[at0 + x] = page_of(x, &ok);
+    } else {
+      int64_t at = at0;
+      for (int64_t x0 = 0; x0 < end; x0 += kThreads) {
+        ok = false;
+        const int page = x0 + tid < end ? page_of(x0 + tid, &ok) : 0;
+        const unsigned there = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) s.w_ties[warp] = __popc(there);
+        __syncthreads();
+        int64_t to = at + __popc(there & ((1u << lane) - 1));
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) to += s.w_ties[w];
+          at += s.w_ties[w];
+        }
+        if (ok && to >= 0 && to < a.n_free) a.free_pages[to] = page;
+        __syncthreads();
+      }
     }
   }
   if (bad) atomicOr(a.err, bad);

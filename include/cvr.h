@@ -439,7 +439,8 @@ cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_strid
  *   pages    [n_req] int32 entries that hold pages afterwards (`held` of the next step); NULL: not written
  *   free_pages [n_free] int32 the free list of cvr_kv_tables, in place: pages that a cut request no longer needs, in request
  *            and entry order, take the positions in front of *free_head, whose own pages are in use. NULL with n_free = 0:
- *            requests keep their pages
+ *            requests keep their pages. An id outside the pool in an entry of a cut request's tokens is not given back, the others close
+ *            up; entries held behind the tokens go back as they are
  *   free_head, free_head_out   int32, with free_pages: *free_head less the pages given back
  * Requests must have pages of their own (none in two of them). An array that the call writes must not overlap any other of its
  * arrays (CVR_E_ARG). Not for handles without pools or with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length,

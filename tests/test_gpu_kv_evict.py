@@ -309,3 +309,27 @@ def test_decode_steps_of_all_operators(form, dtype, dim, shared):
         del start_pages
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("heads", [1, 3])
+@pytest.mark.parametrize("n_req,n", [(3, 100), (600, 100), (3, 5000), (400, 2500)])
+def test_ids_outside_the_pool_are_not_given_back(n_req, n, heads):
+    """Of the pages that cut requests no longer need those that are none of the pool are reported; the others close up to the list's head."""
+    import torch
+    lens = [n if r % 200 in (0, 1, 33) else 15 for r in range(n_req)]
+    c = Cache4(lens, heads, 64, 8, "bf16", cache="same", seed=2)
+    need = -(-n // 8)
+    for r, e, bad in ((0, 5, -1), (0, need - 1, c.n_pages), (1, 3, 2 ** 31 - 1), (1, need // 2, c.n_pages + 7), (n_req - 1 - (n_req - 1) % 200, 4, -2 ** 31)):
+        c.table[r, e] = bad
+    ids = [i for r in range(n_req) if lens[r] == n for i in c.table[r, 3:need].tolist()]
+    back = [i for i in ids if 0 <= i < c.n_pages]
+    assert len(back) == len(ids) - 5
+    kv, n_free = c.handle(heads), len(back) + 100
+    for head in (len(back) + 50, len(back), len(back) - 3):
+        o = evict(c, kv, 40, 20, n_free=n_free, head=head)
+        assert kv.sync(check=False) == (3 if head >= len(back) else 8)
+        there = back[max(0, len(back) - head):]
+        begin = max(0, head - len(back))
+        assert int(o["out"]) == begin and o["free"].tolist() == [-5] * begin + there + [-5] * (n_free - begin - len(there))
+        assert o["lens"].tolist() == [20 if x == n else x for x in lens] and o["pages"].tolist() == [3 if x == n else 2 for x in lens]
+    kv.close()
