@@ -333,3 +333,67 @@ def test_ids_outside_the_pool_are_not_given_back(n_req, n, heads):
         assert int(o["out"]) == begin and o["free"].tolist() == [-5] * begin + there + [-5] * (n_free - begin - len(there))
         assert o["lens"].tolist() == [20 if x == n else x for x in lens] and o["pages"].tolist() == [3 if x == n else 2 for x in lens]
     kv.close()
+
+
+SHARED_OUT = [  # lens, heads, dim, page, layout, shared, limit, keep: what a (request, head) is cut by
+    ([9000, 5, 4001], 2, 128, 16, "page", False, 2000, 1501),     # 8 CTAs of 256 threads
+    ([5000, 4999, 300], 3, 64, 8, "gaps", False, 1000, 777),      # 4 of 256
+    ([20000, 300], 2, 128, 32, "token", False, 12000, 9001),      # 8 of 1024
+    ([33000, 16500], 2, 32, 64, "page", True, 3000, 2999),        # 8 of 1024
+    ([18000, 2, 16400], 11, 32, 8, "page", False, 4000, 3333),    # 4 of 1024
+    ([17000] + [300] * 99, 1, 64, 16, "page", False, 250, 129),   # one of 1024
+]
+
+
+@pytest.mark.parametrize("form", ["same", "i8", "fp4"])
+@pytest.mark.parametrize("lens,heads,dim,page,layout,shared,limit,keep", SHARED_OUT)
+def test_clusters_and_large_ctas(lens, heads, dim, page, layout, shared, limit, keep, form):
+    """Rows of every size with their scales, one pool and two, moved by clusters and by CTAs of 1024 threads, over many rounds."""
+    check(Cache4(lens, heads, dim, page, "bf16", cache=form, layout=layout, shared=shared, seed=len(lens) + dim), limit, keep, 3, 40)
+
+
+@pytest.mark.parametrize("form", ["same", "fp4"])
+@pytest.mark.parametrize("max_pages", [64, 256, 4096])
+@pytest.mark.parametrize("limit,keep,first,last", [(1, 1, 0, 0), (4, 3, 1, 1), (300, 200, 0, 20)])
+def test_short_histories_in_wide_tables(limit, keep, first, last, max_pages, form):
+    """A table with room for far more tokens than there are: clusters most of whose CTAs have few tokens of a request or none."""
+    check(Cache4([2, 3, 5, 0, 1, 40, 700], 2, 64, 16, "bf16", cache=form, max_pages=max_pages, seed=limit), limit, keep, first, last)
+
+
+@pytest.mark.parametrize("form,dtype,dim,shared", [("same", "bf16", 64, False), ("i8", "f16", 32, True), ("fp4", "bf16", 128, False), ("fp4", "f16", 32, True)])
+def test_attention_of_what_stays(form, dtype, dim, shared):
+    """Steps of append, attend, weigh and evict, then the attention of the cut histories against 64 bits on what the cache holds."""
+    import torch
+    n, heads, group, page, limit, keep = 4, 2, 3, 8, 60, 33
+    c = Cache4([60, 59, 40, 17], heads, dim, page, dtype, cache=form, shared=shared, max_pages=9, spare=30, seed=dim)
+    for r in range(n):  # pages of its own for a request's next tokens
+        have = -(-c.lens_list[r] // page)
+        spare = sorted(set(range(c.n_pages)) - set(c.table[s, e].item() for s in range(n) for e in range(9 if s < r else -(-c.lens_list[s] // page))))
+        c.table[r, have:] = dev(spare[:c.max_pages - have])
+    assert len(set(c.table.flatten().tolist())) == n * c.max_pages
+    kv, t = c.handle(heads * group), torch_type(dtype)
+    weight, lens = torch.zeros((c.n_pages, heads, page), device="cuda"), list(c.lens_list)
+    cuts, scale = 0, dim ** -0.5
+    out, lse = torch.zeros((n, heads * group, dim), dtype=t, device="cuda"), torch.zeros((n, heads * group), device="cuda")
+    kept, after = torch.zeros((n, heads, keep), dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    for _ in range(35):
+        slots = torch.cat([c.slots(r, torch.tensor([lens[r]], device="cuda")) for r in range(n)])
+        k, v = (torch.randn((n, heads, dim), generator=c.gen, device="cuda").to(t) for _ in range(2))
+        q = torch.randn((n, heads * group, dim), generator=c.gen, device="cuda").to(t)
+        c.lens.copy_(dev([x + 1 for x in lens]))
+        kv.append(n, slots.data_ptr(), k.data_ptr(), 0 if shared else v.data_ptr())
+        kv.attend(n, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), scale, out.data_ptr(), lse.data_ptr())
+        kv.weigh(n, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), scale, lse.data_ptr(), weight.data_ptr())
+        kv.evict(n, c.lens.data_ptr(), limit, keep, c.table.data_ptr(), weight.data_ptr(), kept.data_ptr(), after.data_ptr(), 2, 8)
+        kv.sync()
+        assert after.tolist() == [keep if x + 1 > limit else x + 1 for x in lens]
+        cuts += sum(x + 1 > limit for x in lens)
+        lens = after.tolist()
+    assert cuts >= 5
+    c.lens.copy_(after)
+    c.lens_list = lens
+    kv.attend(n, q.data_ptr(), c.lens.data_ptr(), c.table.data_ptr(), scale, out.data_ptr(), lse.data_ptr())
+    kv.sync()
+    ref, ref_lse, bound, b_lse = c.reference(q, scale)
+    assert_within(out, ref, bound, "out")
+    assert_within(lse, ref_lse, b_lse, "lse")

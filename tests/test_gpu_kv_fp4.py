@@ -163,6 +163,35 @@ def test_a_row_with_an_infinity_reads_as_no_number():
     assert st == 0 and bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all())
 
 
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("page,group,shared", [(8, 2, False), (8, 12, True), (16, 33, False), (256, 2, False), (256, 8, True)])
+def test_bad_pages_and_lengths_are_reported_and_spare_the_others(page, group, shared, dim):
+    """Ids outside the pool at every place of a tile, in one box of many and in pages longer than a tile; lengths out of range."""
+    import torch
+    c = Cache4([900, 901, 40, 9], 2, dim, page, "bf16", shared=shared, seed=15)
+    q, good, _, st = attend(c, 2 * group)
+    assert st == 0
+    ref, _, bound, _ = c.reference(q, dim ** -0.5)
+    last = -(-900 // page) - 1
+    for bad in (-1, c.n_pages, 2 ** 31 - 1, -2 ** 31):
+        for e in sorted({0, 1, last // 2, last}):
+            table = c.table.clone()
+            c.table[0, e] = bad
+            _, out, lse, st = attend(c, 2 * group)
+            assert st == 3 and torch.equal(out[1:], good[1:])
+            c.table.copy_(table)
+    for bad in (-1, -2 ** 31, c.max_pages * page + 1, 2 ** 31 - 1):  # (another length, another split of the work: the others within their bounds)
+        c.lens[3] = bad
+        _, out, _, st = attend(c, 2 * group)
+        assert st in (3, 6)
+        assert_within(out[:3], ref[:3], bound[:3], "out")
+        if bad < 0:
+            assert st == 6 and not bool(out[3].any())
+    c.lens[3] = 9
+    _, out, _, st = attend(c, 2 * group)
+    assert st == 0 and torch.equal(out, good)
+
+
 # ---- append ----
 def append(x, dim, page, layout="page", dtype="bf16", shared=True):
     """Rows x [n, heads, dim] into shuffled slots of a pool; returns the pool, the slots and a copy of what it held before."""
