@@ -13,7 +13,10 @@
 //
 // Measured (one GB300, copy rate 6.78 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128: 70.8 us, 45% of the copy rate (pages
 // of 16; 65.7 us with pages of 32 and more, whose rows take fewer copies), against 112.6 us on bf16 rows; one request of 131071: 48.5 us,
-// 48%. Bound by issue: 26 to 28 warp instructions per token and kv head; the schedulers issue half of the time and the ALU pipe (conversions, masks, regrouping) is 48% busy. With the heads on M (112.3 and 61.4 us) the sums
+// 48%. 26 to 28 warp instructions per token and kv head, about 10 of them conversions, scaling and regrouping; no pipe is full: the
+// schedulers issue half of the time, the ALU pipe is 48% busy, the tensor pipe 22 to 24%. 3.4 warps per scheduler do not cover what they
+// wait for: of 6.7 warp cycles per instruction issued 2.0 are loads and barriers of tiles (1.3 of 6.3 on the long request), 1.2 the last
+// instruction's own latency, 0.5 a busy pipe. With the heads on M (112.3 and 61.4 us) the sums
 // took twice the registers and two CTAs shared an SM. 512 histories of up to 2000 events, 4 heads of 32, K = V: 46.4 us, 35.1 us on bf16
 // rows: rows of 32 are mostly softmax, and 4 bits add conversions. One request of 200: 6.0 us, latency.
 #pragma once

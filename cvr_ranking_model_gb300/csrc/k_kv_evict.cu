@@ -16,7 +16,7 @@
 //
 // Measured (one GB300, copy rate 6.78 TB/s): 64 requests of up to 8191 tokens cut to 1023 each, 8 heads of 128, bf16: 96.8 us. Cut to 8
 // tokens each they take 29 us (mostly selection: latency of dependent loads, three passes over shared memory); the other 68 move 410 MB,
-// at 89% of the copy rate. Rows by bulk copies, two in and two out per token: 181 us, some 20 ns each per SM. Rounds of register-held
+// at 89% of the copy rate; on 8 bits 67 us, on 4 bits 56. Rows by bulk copies, two in and two out per token: 181 us, some 20 ns each per SM. Rounds of register-held
 // rows whose lookups waited for one another: 187 us. One request of 131071 cut to 32768: 153 us in 8 clusters of 8 CTAs of 1024 threads, 457 us in CTAs of 256.
 #include <cstddef>
 
@@ -611,7 +611,9 @@ template <int CODE>
 cudaError_t launch(const KvEvictArgs& a, int num_sms, cudaStream_t s) {
   // As many CTAs per (request, head) as the SMs hold, of 1024 tokens at least: a large one per SM for long histories, two small ones for
   // others. A cluster pays for its meetings: 4 requests of 20000 tokens, 8 heads, 51 us in 4 large CTAs each, 67 us in 8 small ones; 512
-  // (request, head)s in clusters of two 153 us instead of 104.
+  // (request, head)s in clusters of two 153 us instead of 104. The lengths are on the device, so it is the table's room that decides: 16
+  // histories of up to 2000 events, 4 heads of 32, take 15.6 us in a table of 125 pages of 16 and 22.6 in one of 1024 or more; 8 of up to
+  // 2000 tokens, 8 heads of 128, 50 and 33.
   const int64_t pairs = (int64_t)a.n_req * a.kv_heads, most = (int64_t)a.max_pages << a.page_log2;
   const bool large = most >= 16384 && pairs <= num_sms;
   // (clusters of 8 have to find 8 free SMs of one group: 16 of them on 128 SMs run in two waves)

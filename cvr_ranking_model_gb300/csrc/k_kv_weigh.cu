@@ -12,8 +12,11 @@
 //
 // Measured (one GB300, copy rate 6.78 TB/s): 64 requests of up to 8191 tokens, 32 / 8 heads of 128, bf16: 65.4 us, 85% of the copy rate;
 // straight into registers 77.6 us (two CTAs per SM, the next block's loads in flight). 32 requests of up to 16383 on 4 bits, 64 / 8 heads:
-// 41.9 us, 43%: bound by issue, 334 warp instructions per block of 16 tokens, 70% of the time. More than 16 query heads per kv head are
-// bound by the products and the exponents of every head: 198 us for 64 where 8 take 41.9.
+// 42.8 us, 43%: 328 warp instructions per block of 16 tokens, issued 68% of the time; 64 of them convert and scale codes, the others are
+// the copies' addresses and predicates, logits, exponents and sums. The first requests on 8 bits 44.8 us, 66%. 16 query heads per kv head
+// 74 us on bf16. More are far from their bytes (24: 110 us on bf16; 64: 220, and 206 on 4 bits where 8 take 42.8): their query fragments
+// leave an SM one CTA, two warps per scheduler, which cannot cover a head tile's one chain of products (issue 44%), and the grid, of
+// two CTAs per SM, runs in two waves.
 #include "../../include/cvr.h"
 #include "cvr_kv_rows.cuh"
 
@@ -72,7 +75,7 @@ __device__ __forceinline__ int64_t scan_before(int64_t x, int64_t* sums, int64_t
   return before;
 }
 
-// CTAs that share an SM (two head tiles of rows of 128, or many, need the registers)
+// CTAs that share an SM by their registers (two head tiles of rows of 128, or many, need more); with many, shared memory may hold fewer
 constexpr int ctas_per_sm(int dim, int tiles) { return tiles == 1 || dim < 128 ? 3 : 2; }
 
 // TILES: head tiles held in registers (1 or 2), or 0: any number, in shared memory

@@ -368,7 +368,7 @@ cvr_status cvr_kv_tables(cvr_kv* h, int32_t n_req, const int32_t* lens, const in
  * scale 0; a row with an infinity or NaN gets a scale that is not finite, so that it reads as no number.
  * CVR_DTYPE_FP4 pools: per row scale = max|x| / 2688 (6 * 448, the largest code times the largest block scale); per 16 values
  * block scale = e4m3(448 max|x of the block| / max|x|), code = e2m1(2688 x / (max|x| * block scale)), both to the nearest, ties to
- * even, codes beyond 6 as 6; a block whose scale is 0 (largest value below 2^-19 of the row's) has codes 0; infinities and NaN
+ * even, codes beyond 6 as 6; a block whose scale is 0 (largest value below 2^-19 of the row's) has codes of zero, of either sign; infinities and NaN
  * as for 8 bits. */
 cvr_status cvr_kv_append(cvr_kv* h, int64_t n_tok, const int64_t* slots, const void* k, int64_t k_stride, const void* v,
                          int64_t v_stride);
@@ -402,7 +402,8 @@ cvr_status cvr_kv_attend(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stri
  *         the same slot may come more than once
  *   k, v  DEVICE [n_tok][kv_heads][head_dim] of `dtype`, 16-byte aligned, written by the call; consecutive tokens k_stride /
  *         v_stride values apart (a multiple of 8, at least kv_heads * head_dim). NULL: not wanted (one of them at least is);
- *         with K = V pass v = NULL. k and v must not overlap each other, the slots or the pools.
+ *         with K = V pass v = NULL. k and v must not overlap each other (rows that take turns have the same stride), the slots or
+ *         the pools.
  * 16-bit pools give the rows' bits; 8- and 4-bit pools the values that codes and scales stand for, in fp32, rounded to `dtype`. */
 cvr_status cvr_kv_read(cvr_kv* h, int64_t n_tok, const int64_t* slots, void* k, int64_t k_stride, void* v, int64_t v_stride);
 
@@ -417,9 +418,9 @@ cvr_status cvr_kv_read(cvr_kv* h, int64_t n_tok, const int64_t* slots, void* k, 
  *   decay     finite, >= 0; 1 adds up over a token's whole life, less forgets; 0 reads no old weight
  *   weight    fp32 [n_pages][kv_heads][page_size], in place; places of other tokens are left as they are
  * Sums are fp32, in one order on every call. Logits and lse are rounded to fp32, which moves a term by percents at logits of 2^20, by a
- * factor of e at 2^24. A page must not be in two of the call's requests. weight must not overlap the
- * other arrays. Not for handles with a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length or new length out
- * of range (used clamped), CVR_E_ID_RANGE for a page id outside the pool (its tokens are left out). */
+ * factor of e at 2^24. A page must not be in two of the call's requests. weight must not overlap the other arrays. Not for handles with
+ * a window (CVR_E_ARG). Errors at cvr_kv_sync: CVR_E_INPUT for a length or new length out of range (used clamped), CVR_E_ID_RANGE for a
+ * page id outside the pool (its tokens are left out). */
 cvr_status cvr_kv_weigh(cvr_kv* h, int32_t n_req, const void* q, int64_t q_stride, const int32_t* lens,
                         const int32_t* new_lens, const int32_t* table, float scale, const float* lse, float decay,
                         float* weight);
